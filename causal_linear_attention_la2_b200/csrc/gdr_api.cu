@@ -1,0 +1,243 @@
+// gdr_api.cu -- the C ABI of the gated delta rule and of the state pool
+// (la2_gdr_*, la2_state_copy in include/la2.h): argument checks, workspace
+// layout and launches.  The kernels are in gdr_rec.cuh and state_pool.cuh.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+#include <mutex>
+
+#include "gdr_common.cuh"
+#include "gdr_rec.cuh"
+#include "la2.h"
+#include "state_pool.cuh"
+
+namespace {
+
+using la2::gdr::Args;
+
+constexpr int kMaxDevices = 64;
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+int cdiv(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
+
+bool set_smem_attrs() {
+    const auto set = [](const void* f, size_t bytes) {
+        return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) ==
+               cudaSuccess;
+    };
+    return set(reinterpret_cast<const void*>(la2::gdr::gdr_grad_rec<float>), sizeof(la2::gdr::GradSmem)) &&
+           set(reinterpret_cast<const void*>(la2::gdr::gdr_grad_rec<__nv_bfloat16>), sizeof(la2::gdr::GradSmem)) &&
+           set(reinterpret_cast<const void*>(la2::gdr::pool_copy<float4>), 200 << 10) &&
+           set(reinterpret_cast<const void*>(la2::gdr::pool_copy<float>), 200 << 10);
+}
+
+// Once per device: the shared-memory limits of the kernels that need more than
+// 48 KB.  A failed attempt is tried again by the next call.
+bool device_setup() {
+    static std::mutex m;
+    static bool done[kMaxDevices] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    std::lock_guard<std::mutex> lock(m);
+    if (!done[dev]) done[dev] = set_smem_attrs();
+    return done[dev];
+}
+
+la2_status launched() { return cudaGetLastError() == cudaSuccess ? LA2_OK : LA2_ERR_CUDA; }
+
+// Workspace of a backward on the token-by-token kernels.
+struct RecWs {
+    size_t S0, dS1, W, X, bytes;
+};
+
+RecWs rec_ws(long long BH, int T, int d, int e) {
+    const size_t seqs = static_cast<size_t>(BH);
+    const size_t chunks = cdiv(T, la2::gdr::kRecChunk);
+    const size_t pages = align256(seqs * chunks * d * e * sizeof(float));
+    const size_t rows = align256(seqs * T * e * sizeof(float));
+    RecWs w;
+    w.S0 = 0;
+    w.dS1 = w.S0 + pages;
+    w.W = w.dS1 + pages;
+    w.X = w.W + rows;
+    w.bytes = w.X + rows;
+    return w;
+}
+
+template <typename Tin>
+la2_status rec_forward(const Args& A, cudaStream_t stream) {
+    const dim3 grid(A.B * A.H, cdiv(A.e, la2::gdr::kRecCols));
+    la2::gdr::gdr_rec_fwd<Tin, false><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, nullptr, nullptr);
+    return launched();
+}
+
+template <typename Tin>
+la2_status rec_backward(const Args& A, char* ws, cudaStream_t stream) {
+    const RecWs w = rec_ws(static_cast<long long>(A.B) * A.H, A.T, A.d, A.e);
+    float* S0 = reinterpret_cast<float*>(ws + w.S0);
+    float* dS1 = reinterpret_cast<float*>(ws + w.dS1);
+    float* W = reinterpret_cast<float*>(ws + w.W);
+    float* X = reinterpret_cast<float*>(ws + w.X);
+    const dim3 grid(A.B * A.H, cdiv(A.e, la2::gdr::kRecCols));
+    if (A.T > 0)
+        la2::gdr::gdr_rec_fwd<Tin, true><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, S0, W);
+    la2::gdr::gdr_rec_rev<Tin><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, dS1, X);
+    if (A.T > 0)
+        la2::gdr::gdr_grad_rec<Tin><<<static_cast<unsigned>(A.B) * A.Hk * cdiv(A.T, la2::gdr::kRecChunk),
+                                      la2::gdr::kGradThreads, sizeof(la2::gdr::GradSmem), stream>>>(A, S0, dS1, W, X);
+    return launched();
+}
+
+// Sizes and enums of a sequence call; *empty: nothing to do (no batch entry or
+// no head: there is neither a row nor a state).
+la2_status size_checks(int B, int Hk, int H, int T, int d, int e, la2_dtype dtype, la2_dtype out_dtype,
+                       la2_layout layout, bool* empty) {
+    if (dtype != LA2_DTYPE_F32 && dtype != LA2_DTYPE_BF16) return LA2_ERR_INVALID_ARG;
+    if (out_dtype != LA2_DTYPE_F32 && out_dtype != LA2_DTYPE_BF16) return LA2_ERR_INVALID_ARG;
+    if (layout != LA2_LAYOUT_BHTD && layout != LA2_LAYOUT_BTHD) return LA2_ERR_INVALID_ARG;
+    if (B < 0 || Hk < 0 || H < 0 || T < 0 || d < 1 || e < 1) return LA2_ERR_INVALID_ARG;
+    if (H > 0 && (Hk == 0 || H % Hk != 0)) return LA2_ERR_INVALID_ARG;
+    if (d > la2::gdr::kMaxDim || e > la2::gdr::kMaxDim) return LA2_ERR_UNSUPPORTED;
+    if (dtype == LA2_DTYPE_F32 && out_dtype == LA2_DTYPE_BF16) return LA2_ERR_UNSUPPORTED;
+    // one CTA per (sequence, chunk) at most, in one grid dimension
+    if (B > 0 && H > 0 && static_cast<long long>(B) * H > (INT_MAX - 1) / (static_cast<long long>(T) / 32 + 1))
+        return LA2_ERR_UNSUPPORTED;
+    *empty = B == 0 || H == 0;
+    return LA2_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t la2_gdr_workspace_bytes(int B, int Hk, int H, int T, int d, int e, la2_dtype dtype, int is_bwd) {
+    bool empty = false;
+    if (size_checks(B, Hk, H, T, d, e, dtype, LA2_DTYPE_F32, LA2_LAYOUT_BHTD, &empty) != LA2_OK)
+        return static_cast<size_t>(-1);
+    if (empty || !is_bwd || T == 0) return 0;
+    return rec_ws(static_cast<long long>(B) * H, T, d, e).bytes;
+}
+
+la2_status la2_gdr_fwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                       void* out, const float* init_state, float* final_state, const int* seq_lens, int B,
+                       int Hk, int H, int T, int d, int e, la2_dtype dtype, la2_dtype out_dtype,
+                       la2_layout layout, void* workspace, size_t workspace_bytes, la2_stream_t stream) {
+    bool empty = false;
+    const la2_status st = size_checks(B, Hk, H, T, d, e, dtype, out_dtype, layout, &empty);
+    if (st != LA2_OK) return st;
+    if (empty || (T == 0 && !final_state)) return LA2_OK;
+    if (T > 0 && (!q || !k || !v || !beta || !out)) return LA2_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(g, 4) ||
+        !aligned(beta, 4) || !aligned(init_state, 4) || !aligned(final_state, 4) || !aligned(seq_lens, 4))
+        return LA2_ERR_INVALID_ARG;
+    const size_t need = la2_gdr_workspace_bytes(B, Hk, H, T, d, e, dtype, 0);
+    if (need && (!workspace || workspace_bytes < need)) return LA2_ERR_WORKSPACE;
+    if (need && !aligned(workspace, 256)) return LA2_ERR_INVALID_ARG;
+    if (!device_setup()) return LA2_ERR_CUDA;
+    Args A = {};
+    A.q = q; A.k = k; A.v = v; A.g = g; A.beta = beta; A.o = out;
+    A.init = init_state; A.fin = final_state; A.lens = seq_lens;
+    A.B = B; A.Hk = Hk; A.H = H; A.T = T; A.d = d; A.e = e;
+    A.bthd = layout == LA2_LAYOUT_BTHD;
+    A.out_bf16 = out_dtype == LA2_DTYPE_BF16;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == LA2_DTYPE_BF16 ? rec_forward<__nv_bfloat16>(A, s) : rec_forward<float>(A, s);
+}
+
+la2_status la2_gdr_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                       const void* dout, const float* init_state, const float* d_final_state, void* dq,
+                       void* dk, void* dv, float* dg, float* dbeta, float* d_init_state, const int* seq_lens,
+                       int B, int Hk, int H, int T, int d, int e, la2_dtype dtype, la2_dtype out_dtype,
+                       la2_layout layout, void* workspace, size_t workspace_bytes, la2_stream_t stream) {
+    bool empty = false;
+    const la2_status st = size_checks(B, Hk, H, T, d, e, dtype, out_dtype, layout, &empty);
+    if (st != LA2_OK) return st;
+    if (empty || (T == 0 && !d_init_state)) return LA2_OK;
+    if (T > 0 && (!q || !k || !v || !beta || !dout || !dq || !dk || !dv || !dbeta)) return LA2_ERR_INVALID_ARG;
+    if (dg && !g) return LA2_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(dout, 16) || !aligned(dq, 16) ||
+        !aligned(dk, 16) || !aligned(dv, 16) || !aligned(g, 4) || !aligned(beta, 4) || !aligned(dg, 4) ||
+        !aligned(dbeta, 4) || !aligned(init_state, 4) || !aligned(d_final_state, 4) ||
+        !aligned(d_init_state, 4) || !aligned(seq_lens, 4))
+        return LA2_ERR_INVALID_ARG;
+    const size_t need = la2_gdr_workspace_bytes(B, Hk, H, T, d, e, dtype, 1);
+    if (need && (!workspace || workspace_bytes < need)) return LA2_ERR_WORKSPACE;
+    if (need && !aligned(workspace, 256)) return LA2_ERR_INVALID_ARG;
+    if (!device_setup()) return LA2_ERR_CUDA;
+    Args A = {};
+    A.q = q; A.k = k; A.v = v; A.dout = dout; A.g = g; A.beta = beta;
+    A.dq = dq; A.dk = dk; A.dv = dv; A.dg = dg; A.dbeta = dbeta;
+    A.init = init_state; A.dfinal = d_final_state; A.dinit = d_init_state; A.lens = seq_lens;
+    A.B = B; A.Hk = Hk; A.H = H; A.T = T; A.d = d; A.e = e;
+    A.bthd = layout == LA2_LAYOUT_BTHD;
+    A.out_bf16 = out_dtype == LA2_DTYPE_BF16;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    return dtype == LA2_DTYPE_BF16 ? rec_backward<__nv_bfloat16>(A, ws, s) : rec_backward<float>(A, ws, s);
+}
+
+la2_status la2_gdr_decode(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                          float* states, const int* slots, int n_slots, float* out, int B, int Hk, int H,
+                          int d, int e, la2_dtype dtype, la2_stream_t stream) {
+    bool empty = false;
+    const la2_status st =
+        size_checks(B, Hk, H, 1, d, e, dtype, LA2_DTYPE_F32, LA2_LAYOUT_BHTD, &empty);
+    if (st != LA2_OK) return st;
+    if (n_slots < 0) return LA2_ERR_INVALID_ARG;
+    if (empty) return LA2_OK;
+    if (!q || !k || !v || !beta || !out || (n_slots > 0 && !states)) return LA2_ERR_INVALID_ARG;
+    const uintptr_t el = dtype == LA2_DTYPE_BF16 ? 2 : 4;
+    if (!aligned(q, el) || !aligned(k, el) || !aligned(v, el) || !aligned(g, 4) || !aligned(beta, 4) ||
+        !aligned(states, 4) || !aligned(slots, 4) || !aligned(out, 4))
+        return LA2_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool vec = e % 4 == 0 && aligned(states, 16);
+    const dim3 grid(B * H, vec ? 1 : cdiv(e, 32));
+    const auto go = [&](auto tag) {
+        using Tin = decltype(tag);
+        const Tin *qq = static_cast<const Tin*>(q), *kk = static_cast<const Tin*>(k), *vv = static_cast<const Tin*>(v);
+        if (vec)
+            la2::gdr::gdr_step<Tin, 4><<<grid, la2::gdr::kStepThreads, 0, s>>>(qq, kk, vv, g, beta, states, slots,
+                                                                             n_slots, out, Hk, H, d, e);
+        else
+            la2::gdr::gdr_step<Tin, 1><<<grid, la2::gdr::kStepThreads, 0, s>>>(qq, kk, vv, g, beta, states, slots,
+                                                                             n_slots, out, Hk, H, d, e);
+    };
+    if (dtype == LA2_DTYPE_BF16) go(__nv_bfloat16());
+    else go(float());
+    return launched();
+}
+
+la2_status la2_state_copy(float* states, const int* src, const int* dst, int n, int n_slots,
+                          long long slot_elems, la2_stream_t stream) {
+    if (n < 0 || n_slots < 0 || slot_elems < 0) return LA2_ERR_INVALID_ARG;
+    if (n == 0 || n_slots == 0 || slot_elems == 0) return LA2_OK;
+    if (n > la2::gdr::kPoolMaxPairs) return LA2_ERR_UNSUPPORTED;
+    if (!states || !src || !dst || !aligned(states, 4) || !aligned(src, 4) || !aligned(dst, 4))
+        return LA2_ERR_INVALID_ARG;
+    if (!device_setup()) return LA2_ERR_CUDA;
+    const bool vec = slot_elems % 4 == 0 && aligned(states, 16);
+    const size_t item = vec ? 16 : 4;
+    const long long page = vec ? slot_elems / 4 : slot_elems;
+    // slices of at most 64 KB of shared memory, so that three CTAs share an SM,
+    // down to 32 bytes of a page
+    int units = la2::gdr::kPoolThreads;
+    while (units > static_cast<int>(32 / item) && static_cast<size_t>(n) * units * item > (64u << 10)) units >>= 1;
+    const size_t smem = static_cast<size_t>(n) * (units * item + 2 * sizeof(int));
+    const long long grid = (page + units - 1) / units;
+    if (grid > INT_MAX) return LA2_ERR_UNSUPPORTED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (vec)
+        la2::gdr::pool_copy<float4><<<static_cast<unsigned>(grid), la2::gdr::kPoolThreads, smem, s>>>(
+            reinterpret_cast<float4*>(states), src, dst, n, n_slots, page, units);
+    else
+        la2::gdr::pool_copy<float><<<static_cast<unsigned>(grid), la2::gdr::kPoolThreads, smem, s>>>(
+            states, src, dst, n, n_slots, page, units);
+    return launched();
+}
+
+}  // extern "C"

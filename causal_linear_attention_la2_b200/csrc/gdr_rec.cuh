@@ -1,0 +1,401 @@
+// gdr_rec.cuh -- the gated delta rule token by token in fp32 on the SIMT cores:
+// every 1 <= d, e <= 128 and both input types (the bf16 sizes 64 and 128 have
+// tensor-core kernels of their own).
+//
+// The columns of the state do not interact: column j of S needs k, q, beta, g
+// and v_j alone.  So eight lanes hold one column (16 rows each at d = 128) in
+// registers for the whole sequence, a token costs three multiply-adds a row and
+// two sums over eight lanes, and the state never leaves the registers.  The
+// backward runs the same recurrence for dS from the last row to the first,
+//
+//   dS += q do^T,  x = dS^T k,  dv = beta x,  dS = a (dS - k (beta x)^T),
+//
+// and a third kernel, parallel over 32-row chunks, makes dq, dk, dg and dbeta
+// from the states on the chunk borders, the rows w and the rows x (gdr_grad_rec).
+#pragma once
+#include "gdr_common.cuh"
+
+namespace la2 {
+namespace gdr {
+
+constexpr int kMaxDim = 128;
+constexpr int kRecThreads = 128;  // 4 warps of 4 columns
+constexpr int kRecCols = 16;
+constexpr int kRecRows = 16;      // rows of the state per lane: kMaxDim / 8
+constexpr int kRecStep = 16;      // tokens staged in shared memory at a time
+constexpr int kRecChunk = 32;     // chunk length of gdr_grad_rec
+
+struct RecSmem {
+    float k[kRecStep][kMaxDim + 4];
+    float q[kRecStep][kMaxDim + 4];
+    float v[kRecStep][kRecCols];
+    float a[kRecStep];
+    float b[kRecStep];
+};
+
+// Rows t0 .. t0 + n - 1 of k, q and 16 columns of `vals` (v or dout) into
+// shared memory; rows i >= d are zero.
+template <typename Tin>
+__device__ __forceinline__ void rec_stage(const Args& A, RecSmem& sm, const Tin* vals, int b, int h,
+                                          int t0, int n, int col0) {
+    const int tid = threadIdx.x, hk = h / (A.H / A.Hk);
+    const Tin* k = static_cast<const Tin*>(A.k);
+    const Tin* q = static_cast<const Tin*>(A.q);
+    for (int x = tid; x < n * kMaxDim; x += kRecThreads) {
+        const int r = x / kMaxDim, i = x % kMaxDim;
+        const size_t at = row_at(A, b, hk, A.Hk, t0 + r, A.d) + i;
+        sm.k[r][i] = i < A.d ? to_float(k[at]) : 0.f;
+        sm.q[r][i] = i < A.d ? to_float(q[at]) : 0.f;
+    }
+    for (int x = tid; x < n * kRecCols; x += kRecThreads) {
+        const int r = x / kRecCols, j = col0 + x % kRecCols;
+        sm.v[r][x % kRecCols] = j < A.e ? to_float(vals[row_at(A, b, h, A.H, t0 + r, A.e) + j]) : 0.f;
+    }
+    if (tid < n) {
+        const size_t at = row_at(A, b, h, A.H, t0 + tid, 1);
+        sm.a[tid] = expf(gate_at(A, at));
+        sm.b[tid] = A.beta[at];
+    }
+}
+
+__device__ __forceinline__ float sum8(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    return x;
+}
+
+// Forward.  kSave: no output; the state entering each chunk goes to S0
+// [B*H][chunks][d][e] and the rows w to W [B*H][T][e], for the backward.
+template <typename Tin, bool kSave>
+__global__ void __launch_bounds__(kRecThreads)
+gdr_rec_fwd(Args A, float* S0, float* W) {
+    __shared__ RecSmem sm;
+    const int n = blockIdx.x, b = n / A.H, h = n % A.H;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = lane & 7, lc = warp * 4 + (lane >> 3), col0 = blockIdx.y * kRecCols;
+    const int j = col0 + lc;
+    const bool on = j < A.e;
+    const int len = length_of(A, b);
+    const int chunks = (A.T + kRecChunk - 1) / kRecChunk;
+    const size_t page = static_cast<size_t>(A.d) * A.e;
+    float S[kRecRows];
+#pragma unroll
+    for (int m = 0; m < kRecRows; ++m) {
+        const int i = r + 8 * m;
+        S[m] = A.init && on && i < A.d ? A.init[n * page + static_cast<size_t>(i) * A.e + j] : 0.f;
+    }
+    for (int t0 = 0; t0 < len; t0 += kRecStep) {
+        const int m16 = min(kRecStep, len - t0);
+        __syncthreads();
+        rec_stage<Tin>(A, sm, static_cast<const Tin*>(A.v), b, h, t0, m16, col0);
+        __syncthreads();
+        if (kSave && t0 % kRecChunk == 0 && on) {
+            float* to = S0 + (static_cast<size_t>(n) * chunks + t0 / kRecChunk) * page + j;
+#pragma unroll
+            for (int m = 0; m < kRecRows; ++m)
+                if (r + 8 * m < A.d) to[static_cast<size_t>(r + 8 * m) * A.e] = S[m];
+        }
+        for (int t = 0; t < m16; ++t) {
+            const float a = sm.a[t];
+            float p = 0.f;
+#pragma unroll
+            for (int m = 0; m < kRecRows; ++m) {
+                S[m] *= a;
+                p = fmaf(S[m], sm.k[t][r + 8 * m], p);
+            }
+            const float w = sm.v[t][lc] - sum8(p);
+            const float u = sm.b[t] * w;
+            float o = 0.f;
+#pragma unroll
+            for (int m = 0; m < kRecRows; ++m) {
+                S[m] = fmaf(sm.k[t][r + 8 * m], u, S[m]);
+                if (!kSave) o = fmaf(S[m], sm.q[t][r + 8 * m], o);
+            }
+            if (kSave) {
+                if (on && r == 0) W[(static_cast<size_t>(n) * A.T + t0 + t) * A.e + j] = w;
+            } else {
+                o = sum8(o);
+                if (on && r == 0) put(A.o, row_at(A, b, h, A.H, t0 + t, A.e) + j, o, A.out_bf16);
+            }
+        }
+    }
+    if (!kSave && A.fin && on) {
+#pragma unroll
+        for (int m = 0; m < kRecRows; ++m)
+            if (r + 8 * m < A.d) A.fin[n * page + static_cast<size_t>(r + 8 * m) * A.e + j] = S[m];
+    }
+}
+
+// Backward in time: dv, d_init_state, the rows x to X [B*H][T][e] and the
+// gradient of the state after each chunk to dS1 [B*H][chunks][d][e].
+template <typename Tin>
+__global__ void __launch_bounds__(kRecThreads)
+gdr_rec_rev(Args A, float* dS1, float* X) {
+    __shared__ RecSmem sm;
+    const int n = blockIdx.x, b = n / A.H, h = n % A.H;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = lane & 7, lc = warp * 4 + (lane >> 3), col0 = blockIdx.y * kRecCols;
+    const int j = col0 + lc;
+    const bool on = j < A.e;
+    const int len = length_of(A, b);
+    const int chunks = (A.T + kRecChunk - 1) / kRecChunk;
+    const size_t page = static_cast<size_t>(A.d) * A.e;
+    float D[kRecRows];
+#pragma unroll
+    for (int m = 0; m < kRecRows; ++m) {
+        const int i = r + 8 * m;
+        D[m] = A.dfinal && on && i < A.d ? A.dfinal[n * page + static_cast<size_t>(i) * A.e + j] : 0.f;
+    }
+    for (int t0 = len > 0 ? (len - 1) / kRecStep * kRecStep : -1; t0 >= 0; t0 -= kRecStep) {
+        const int m16 = min(kRecStep, len - t0);
+        __syncthreads();
+        rec_stage<Tin>(A, sm, static_cast<const Tin*>(A.dout), b, h, t0, m16, col0);
+        __syncthreads();
+        // the last rows of a chunk: its dS1 is what arrives here
+        if (on && ((t0 + kRecStep) % kRecChunk == 0 || t0 + m16 == len)) {
+            float* to = dS1 + (static_cast<size_t>(n) * chunks + t0 / kRecChunk) * page + j;
+#pragma unroll
+            for (int m = 0; m < kRecRows; ++m)
+                if (r + 8 * m < A.d) to[static_cast<size_t>(r + 8 * m) * A.e] = D[m];
+        }
+        for (int t = m16 - 1; t >= 0; --t) {
+            const float dout = sm.v[t][lc];
+            float p = 0.f;
+#pragma unroll
+            for (int m = 0; m < kRecRows; ++m) {
+                D[m] = fmaf(sm.q[t][r + 8 * m], dout, D[m]);
+                p = fmaf(D[m], sm.k[t][r + 8 * m], p);
+            }
+            const float x = sum8(p), dw = sm.b[t] * x, a = sm.a[t];
+#pragma unroll
+            for (int m = 0; m < kRecRows; ++m) D[m] = a * fmaf(-sm.k[t][r + 8 * m], dw, D[m]);
+            if (on && r == 0) {
+                X[(static_cast<size_t>(n) * A.T + t0 + t) * A.e + j] = x;
+                put(A.dv, row_at(A, b, h, A.H, t0 + t, A.e) + j, dw, A.out_bf16);
+            }
+        }
+    }
+    if (A.dinit && on) {
+#pragma unroll
+        for (int m = 0; m < kRecRows; ++m)
+            if (r + 8 * m < A.d) A.dinit[n * page + static_cast<size_t>(r + 8 * m) * A.e + j] = D[m];
+    }
+}
+
+// dq, dk, dg, dbeta of one chunk of C = 32 rows of key head hk, summed over the
+// value heads that share it in their order.  With G the cumulative gates of the
+// chunk, S0 the state before it, dS1 the gradient of the state after it,
+// U = beta W, M_ts = exp(G_t - G_s) (s <= t):
+//
+//   dP = M o (dO U^T),   E_ts = -beta_t M_ts (x_t . u_s)  (s < t)
+//   dq_t  = e^{G_t} S0 do_t + sum_s dP_ts k_s
+//   row_t = sum_s E_ts k_s - beta_t e^{G_t} S0 x_t             (k_t read as a query of the state)
+//   col_s = sum_t (E_ts k_t + dP_ts q_t) + e^{G_C - G_s} dS1 u_s   (k_s written into the state)
+//   dk = row + col,   dbeta_t = x_t . w_t
+//   dL/dG_t = q_t . dq_t + k_t . row_t - k_t . col_t, and <dS1, S1> more at the chunk's end,
+//   with k_t . row_t = beta_t x_t . (w_t - v_t) (the rows' definition, so no product is needed);
+//   dg = sums of dL/dG from a row to the chunk's end.
+struct GradSmem {
+    static constexpr int C = kRecChunk, P = kMaxDim + 1;
+    float q[C][P], k[C][P], dout[C][P], u[C][P], x[C][P];
+    float S[kMaxDim][P];
+    float dp[C][C + 1], E[C][C + 1];
+    float G[C], Gl[C], b[C], db[C], xr[C], dG[C];
+    float part[8][C];
+    float red[8];
+};
+
+constexpr int kGradThreads = 256;
+
+template <typename Tin>
+__global__ void __launch_bounds__(kGradThreads)
+gdr_grad_rec(Args A, const float* S0, const float* dS1, const float* W, const float* X) {
+    constexpr int C = kRecChunk;
+    extern __shared__ float gsm_raw[];
+    GradSmem& sm = *reinterpret_cast<GradSmem*>(gsm_raw);
+    const int chunks = (A.T + C - 1) / C;
+    const int c = blockIdx.x % chunks, hk = blockIdx.x / chunks % A.Hk;
+    const int b = blockIdx.x / chunks / A.Hk;
+    const int len = length_of(A, b), t0 = c * C;
+    if (t0 >= len) return;
+    const int n = min(C, len - t0), rep = A.H / A.Hk, tid = threadIdx.x;
+    const int lane = tid & 31, warp = tid >> 5;
+    const int i = tid & 127, half = tid >> 7;  // column i of dq and dk, rows half, half + 2, ...
+    const size_t page = static_cast<size_t>(A.d) * A.e;
+    const Tin* q = static_cast<const Tin*>(A.q);
+    const Tin* k = static_cast<const Tin*>(A.k);
+    const Tin* v = static_cast<const Tin*>(A.v);
+    const Tin* dout = static_cast<const Tin*>(A.dout);
+    for (int y = tid; y < C * kMaxDim; y += kGradThreads) {
+        const int t = y / kMaxDim, m = y % kMaxDim;
+        const bool ok = t < n && m < A.d;
+        const size_t at = ok ? row_at(A, b, hk, A.Hk, t0 + t, A.d) + m : 0;
+        sm.q[t][m] = ok ? to_float(q[at]) : 0.f;
+        sm.k[t][m] = ok ? to_float(k[at]) : 0.f;
+    }
+    float accq[C / 2], acck[C / 2];
+#pragma unroll
+    for (int m = 0; m < C / 2; ++m) accq[m] = acck[m] = 0.f;
+    for (int hh = 0; hh < rep; ++hh) {
+        const int h = hk * rep + hh;
+        const size_t seq = static_cast<size_t>(b) * A.H + h;
+        const float* S0c = S0 + (seq * chunks + c) * page;
+        const float* dS1c = dS1 + (seq * chunks + c) * page;
+        __syncthreads();
+        if (tid < C) {  // cumulative gates, as two floats: a difference of two large ones keeps its digits
+            double s = 0.0;
+            for (int t = 0; t <= tid; ++t)
+                s += t < n ? static_cast<double>(gate_at(A, row_at(A, b, h, A.H, t0 + t, 1))) : 0.0;
+            sm.G[tid] = static_cast<float>(s);
+            sm.Gl[tid] = static_cast<float>(s - sm.G[tid]);
+            sm.b[tid] = tid < n ? A.beta[row_at(A, b, h, A.H, t0 + tid, 1)] : 0.f;
+        }
+        __syncthreads();
+        // a warp takes rows warp, warp + 8, ..: u, x, dout and the row sums
+        for (int t = warp; t < C; t += 8) {
+            float db = 0.f, xr = 0.f;
+            for (int j = lane; j < kMaxDim; j += 32) {
+                float w = 0.f, x = 0.f, dd = 0.f, vv = 0.f;
+                if (t < n && j < A.e) {
+                    const size_t at = (seq * A.T + t0 + t) * A.e + j;
+                    const size_t io = row_at(A, b, h, A.H, t0 + t, A.e) + j;
+                    w = W[at];
+                    x = X[at];
+                    dd = to_float(dout[io]);
+                    vv = to_float(v[io]);
+                }
+                sm.u[t][j] = sm.b[t] * w;
+                sm.x[t][j] = x;
+                sm.dout[t][j] = dd;
+                db = fmaf(x, w, db);
+                xr = fmaf(x, w - vv, xr);
+            }
+            for (int m = 16; m; m >>= 1) {
+                db += __shfl_xor_sync(0xffffffffu, db, m);
+                xr += __shfl_xor_sync(0xffffffffu, xr, m);
+            }
+            if (lane == 0) {
+                sm.db[t] = db;
+                sm.xr[t] = sm.b[t] * xr;
+            }
+        }
+        for (int y = tid; y < A.d * A.e; y += kGradThreads) sm.S[y / A.e][y % A.e] = S0c[y];
+        __syncthreads();
+        for (int y = tid; y < C * C; y += kGradThreads) {
+            const int t = y / C, s = y % C;
+            float p = 0.f, x = 0.f;
+            if (s <= t) {
+                for (int j = 0; j < A.e; ++j) {
+                    p = fmaf(sm.dout[t][j], sm.u[s][j], p);
+                    x = fmaf(sm.x[t][j], sm.u[s][j], x);
+                }
+                const float M = expf((sm.G[t] - sm.G[s]) + (sm.Gl[t] - sm.Gl[s]));
+                p *= M;
+                x = s < t ? -x * M * sm.b[t] : 0.f;
+            }
+            sm.dp[t][s] = p;
+            sm.E[t][s] = x;
+        }
+        __syncthreads();
+        float fq[C / 2], row[C / 2], col[C / 2], colS[C / 2];
+#pragma unroll
+        for (int m = 0; m < C / 2; ++m) fq[m] = row[m] = col[m] = colS[m] = 0.f;
+        if (i < A.d) {
+            for (int j = 0; j < A.e; ++j) {
+                const float s = sm.S[i][j];
+#pragma unroll
+                for (int m = 0; m < C / 2; ++m) {
+                    fq[m] = fmaf(sm.dout[half + 2 * m][j], s, fq[m]);
+                    row[m] = fmaf(sm.x[half + 2 * m][j], s, row[m]);
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < C / 2; ++m) {
+                const int t = half + 2 * m;
+                const float eg = expf(sm.G[t]) * (1.f + sm.Gl[t]);
+                fq[m] *= eg;
+                row[m] *= -sm.b[t] * eg;
+            }
+            for (int s = 0; s < C; ++s) {
+                const float ks = sm.k[s][i], qs = sm.q[s][i];
+#pragma unroll
+                for (int m = 0; m < C / 2; ++m) {
+                    const int t = half + 2 * m;
+                    fq[m] = fmaf(sm.dp[t][s], ks, fq[m]);
+                    row[m] = fmaf(sm.E[t][s], ks, row[m]);
+                    col[m] = fmaf(sm.E[s][t], ks, fmaf(sm.dp[s][t], qs, col[m]));
+                }
+            }
+        }
+        __syncthreads();
+        // <dS1, S0> while the states change places
+        float dot = 0.f;
+        for (int y = tid; y < A.d * A.e; y += kGradThreads) {
+            const float ds = dS1c[y];
+            dot = fmaf(ds, sm.S[y / A.e][y % A.e], dot);
+            sm.S[y / A.e][y % A.e] = ds;
+        }
+        for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+        if (lane == 0) sm.red[warp] = dot;
+        __syncthreads();
+        if (i < A.d) {
+            for (int j = 0; j < A.e; ++j) {
+                const float s = sm.S[i][j];
+#pragma unroll
+                for (int m = 0; m < C / 2; ++m) colS[m] = fmaf(sm.u[half + 2 * m][j], s, colS[m]);
+            }
+        }
+        // row sums over i (128 threads of this half: 4 warps), then <dS1, S1>
+        float gc = 0.f;
+#pragma unroll
+        for (int m = 0; m < C / 2; ++m) {
+            const int t = half + 2 * m;
+            const float ki = i < A.d ? sm.k[t][i] : 0.f, qi = i < A.d ? sm.q[t][i] : 0.f;
+            colS[m] *= expf((sm.G[C - 1] - sm.G[t]) + (sm.Gl[C - 1] - sm.Gl[t]));
+            col[m] += colS[m];
+            gc = fmaf(ki, colS[m], gc);
+            float s = fmaf(qi, fq[m], -ki * col[m]);
+            for (int z = 16; z; z >>= 1) s += __shfl_xor_sync(0xffffffffu, s, z);
+            if (lane == 0) sm.part[warp][t] = s;
+            accq[m] += fq[m];
+            acck[m] += row[m] + col[m];
+        }
+        for (int z = 16; z; z >>= 1) gc += __shfl_xor_sync(0xffffffffu, gc, z);
+        __syncthreads();
+        if (lane == 0) sm.red[warp] = fmaf(expf(sm.G[C - 1]) * (1.f + sm.Gl[C - 1]), sm.red[warp], gc);
+        __syncthreads();
+        if (tid < C) {
+            const int w0 = (tid & 1) * 4;
+            float s = sm.part[w0][tid] + sm.part[w0 + 1][tid] + sm.part[w0 + 2][tid] + sm.part[w0 + 3][tid];
+            s += sm.xr[tid];
+            if (tid == C - 1)
+                for (int w = 0; w < 8; ++w) s += sm.red[w];
+            sm.dG[tid] = s;
+        }
+        __syncthreads();
+        if (tid < n) {
+            const size_t at = row_at(A, b, h, A.H, t0 + tid, 1);
+            A.dbeta[at] = sm.db[tid];
+            if (A.dg) {
+                float s = 0.f;
+                for (int t = C - 1; t >= tid; --t) s += sm.dG[t];
+                A.dg[at] = s;
+            }
+        }
+    }
+    if (i < A.d) {
+#pragma unroll
+        for (int m = 0; m < C / 2; ++m) {
+            const int t = half + 2 * m;
+            if (t < n) {
+                const size_t at = row_at(A, b, hk, A.Hk, t0 + t, A.d) + i;
+                put(A.dq, at, accq[m], A.out_bf16);
+                put(A.dk, at, acck[m], A.out_bf16);
+            }
+        }
+    }
+}
+
+}  // namespace gdr
+}  // namespace la2

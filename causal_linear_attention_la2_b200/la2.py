@@ -30,7 +30,9 @@ EXPORTS = ("la2_workspace_bytes", "la2_fwd", "la2_fwd_state", "la2_fwd_ex", "la2
            "la2_decode", "la2_status_str", "la2_device_status", "la2_last_launch_count",
            "la2_fwd_noalloc", "la2_set_schedule", "la2_plan_info", "la2_selftest_timeout",
            "la2_bwd_state", "la2_dlambda", "la2_dlambda_workspace_bytes",
-           "la2_norm_workspace_bytes", "la2_fwd_norm", "la2_bwd_norm")
+           "la2_norm_workspace_bytes", "la2_fwd_norm", "la2_bwd_norm",
+           "la2_gdr_workspace_bytes", "la2_gdr_fwd", "la2_gdr_bwd", "la2_gdr_decode",
+           "la2_state_copy")
 
 LA2_LAYOUT_BHTD = 0
 LA2_LAYOUT_BTHD = 1
@@ -104,6 +106,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.la2_bwd_norm.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i,
                                  vp, sz, vp]
     lib.la2_bwd_norm.restype = i
+    lib.la2_gdr_workspace_bytes.argtypes = [i] * 8
+    lib.la2_gdr_workspace_bytes.restype = sz
+    lib.la2_gdr_fwd.argtypes = [vp] * 9 + [i] * 9 + [vp, sz, vp]
+    lib.la2_gdr_fwd.restype = i
+    lib.la2_gdr_bwd.argtypes = [vp] * 15 + [i] * 9 + [vp, sz, vp]
+    lib.la2_gdr_bwd.restype = i
+    lib.la2_gdr_decode.argtypes = [vp] * 7 + [i, vp] + [i] * 6 + [vp]
+    lib.la2_gdr_decode.restype = i
+    lib.la2_state_copy.argtypes = [vp, vp, vp, i, i, ctypes.c_longlong, vp]
+    lib.la2_state_copy.restype = i
     _lib = lib
     return lib
 
@@ -544,3 +556,244 @@ def la2_bwd(q, k, v, decay, dout, dq=None, dk=None, dv=None, block: int = 128, s
     if st != LA2_OK:
         raise LA2Error(st, "la2_bwd")
     return dq, dk, dv
+
+
+# ------------------------------------------------------- the gated delta rule
+
+def la2_gdr_workspace_bytes(B, Hk, H, T, d, e, dtype, is_bwd) -> int:
+    return int(load().la2_gdr_workspace_bytes(B, Hk, H, T, d, e, dtype, int(is_bwd)))
+
+
+def la2_gdr_fwd_raw(q, k, v, g, beta, out, init_state, final_state, seq_lens, B, Hk, H, T, d, e,
+                    dtype, out_dtype, layout, workspace=0, ws_bytes=0, stream=0) -> int:
+    """The C call with integer pointers (0 = NULL); returns the status."""
+    return int(load().la2_gdr_fwd(q, k, v, g, beta, out, init_state, final_state, seq_lens, B, Hk,
+                                  H, T, d, e, dtype, out_dtype, layout, workspace, ws_bytes, stream))
+
+
+def la2_gdr_bwd_raw(q, k, v, g, beta, dout, init_state, d_final_state, dq, dk, dv, dg, dbeta,
+                    d_init_state, seq_lens, B, Hk, H, T, d, e, dtype, out_dtype, layout,
+                    workspace=0, ws_bytes=0, stream=0) -> int:
+    """The C call with integer pointers (0 = NULL); returns the status."""
+    return int(load().la2_gdr_bwd(q, k, v, g, beta, dout, init_state, d_final_state, dq, dk, dv,
+                                  dg, dbeta, d_init_state, seq_lens, B, Hk, H, T, d, e, dtype,
+                                  out_dtype, layout, workspace, ws_bytes, stream))
+
+
+def la2_gdr_decode_raw(q, k, v, g, beta, states, slots, n_slots, out, B, Hk, H, d, e, dtype,
+                       stream=0) -> int:
+    """The C call with integer pointers (0 = NULL); returns the status."""
+    return int(load().la2_gdr_decode(q, k, v, g, beta, states, slots, n_slots, out, B, Hk, H, d, e,
+                                     dtype, stream))
+
+
+def la2_state_copy_raw(states, src, dst, n, n_slots, slot_elems, stream=0) -> int:
+    """The C call with integer pointers; returns the status."""
+    return int(load().la2_state_copy(states, src, dst, n, n_slots, slot_elems, stream))
+
+
+def _same_device(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _stream_on(stream, device) -> int:
+    """The caller's stream, or the current stream of the tensors' device."""
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    return int(s.cuda_stream)
+
+
+def _own_workspace(nbytes: int, device, stream, workspace):
+    """(pointer, size, tensor): the caller's workspace, or one of this call's own.
+
+    A call allocates its workspace from torch's caching allocator on the stream
+    that it runs on, so two calls on two streams, or two captured graphs, never
+    share one; the allocator hands the memory on in stream order."""
+    if workspace is not None:
+        if workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+        p, n = _workspace(nbytes, device, workspace)
+        return p, n, workspace
+    if nbytes <= 0:
+        return 0, 0, None
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    with torch.cuda.stream(s):
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return buf.data_ptr(), nbytes, buf
+
+
+def _gdr_dims(q, v, layout):
+    """(B, Hk, H, T, d, e) from q's and v's shapes in the given layout."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and v must have 4 dimensions")
+    B, Hk, T, d, e = _dims(q, v, layout)
+    H = v.shape[1] if layout == "bhtd" else v.shape[2]
+    if Hk == 0 or H % Hk != 0:
+        if not (H == 0 and Hk == 0):
+            raise ValueError(f"{H} value heads are not a multiple of {Hk} key heads")
+    return B, Hk, H, T, d, e
+
+
+def _gdr_inputs(q, k, v, g, beta, layout, seq_lens, states):
+    """Checks what both directions take; returns the sizes and the dtype code."""
+    B, Hk, H, T, d, e = _gdr_dims(q, v, layout)
+    dt = _dtype_code(q)
+    _check(q, "q", _shape(layout, B, Hk, T, d), q.dtype)
+    _check(k, "k", _shape(layout, B, Hk, T, d), q.dtype)
+    _check(v, "v", _shape(layout, B, H, T, e), q.dtype)
+    gate = (B, H, T) if layout == "bhtd" else (B, T, H)
+    _check(beta, "beta", gate, torch.float32)
+    if g is not None:
+        _check(g, "g", gate, torch.float32)
+    if seq_lens is not None:
+        _check(seq_lens, "seq_lens", (B,), torch.int32)
+    for name, s in states.items():
+        if s is not None:
+            _check(s, name, (B, H, d, e), torch.float32)
+    _same_device(q.device, k=k, v=v, g=g, beta=beta, seq_lens=seq_lens, **states)
+    return B, Hk, H, T, d, e, dt
+
+
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def la2_gdr_fwd(q, k, v, g, beta, layout: str = "bhtd", init_state=None, seq_lens=None, out=None,
+                final_state=None, want_final: bool = False, stream=None, workspace=None,
+                out_dtype=None):
+    """The gated delta rule over whole sequences:
+
+        S_t = exp(g_t) (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,   o_t = S_t^T q_t
+
+    q, k [B, Hk, T, d], v [B, H, T, e] (bf16 or fp32; 'bthd': [B, T, heads, .]), g (log-gate, or
+    None) and beta fp32 [B, H, T] ('bthd': [B, T, H]); value head h reads key head h // (H // Hk).
+    seq_lens (int32 [B]): rows of each sequence; the rows behind them are left as they were in
+    `out` (zero in an out allocated here).  Returns out, or (out, final_state) with want_final or
+    a final_state buffer given."""
+    B, Hk, H, T, d, e, dt = _gdr_inputs(q, k, v, g, beta, layout, seq_lens,
+                                        {"init_state": init_state, "final_state": final_state})
+    odt, oc = _out_dtype(out_dtype)
+    shape = _shape(layout, B, H, T, e)
+    with torch.cuda.device(q.device):
+        sp = _stream_on(stream, q.device)
+        if out is None:
+            out = (torch.empty if seq_lens is None else torch.zeros)(shape, dtype=odt, device=q.device)
+        _check(out, "out", shape, odt)
+        if final_state is None and want_final:
+            final_state = torch.empty((B, H, d, e), dtype=torch.float32, device=q.device)
+        _same_device(q.device, out=out)
+        wp, wn, keep = _own_workspace(la2_gdr_workspace_bytes(B, Hk, H, T, d, e, dt, 0), q.device,
+                                      stream, workspace)
+        st = la2_gdr_fwd_raw(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), beta.data_ptr(),
+                             out.data_ptr(), _ptr(init_state), _ptr(final_state), _ptr(seq_lens),
+                             B, Hk, H, T, d, e, dt, oc, _LAYOUTS[layout], wp, wn, sp)
+    if st != LA2_OK:
+        raise LA2Error(st, "la2_gdr_fwd")
+    return out if final_state is None else (out, final_state)
+
+
+def la2_gdr_bwd(q, k, v, g, beta, dout, layout: str = "bhtd", init_state=None, d_final_state=None,
+                seq_lens=None, dq=None, dk=None, dv=None, dg=None, dbeta=None, d_init_state=None,
+                want_d_init: bool = False, stream=None, workspace=None, out_dtype=None):
+    """(dq, dk, dv, dg, dbeta[, d_init_state]) of sum(dout * out) + sum(d_final_state * final_state)
+    for la2_gdr_fwd; dg is None without a gate.  d_init_state is returned with want_d_init or a
+    buffer given.  Rows behind seq_lens are left as they were (zero in tensors allocated here)."""
+    B, Hk, H, T, d, e, dt = _gdr_inputs(q, k, v, g, beta, layout, seq_lens,
+                                        {"init_state": init_state, "d_final_state": d_final_state,
+                                         "d_init_state": d_init_state})
+    odt, oc = _out_dtype(out_dtype)
+    _check(dout, "dout", _shape(layout, B, H, T, e), q.dtype)
+    if dg is not None and g is None:
+        raise ValueError("dg needs a gate g")
+    gate = tuple(beta.shape)
+    new = torch.empty if seq_lens is None else torch.zeros
+    with torch.cuda.device(q.device):
+        sp = _stream_on(stream, q.device)
+        o = dict(dtype=odt, device=q.device)
+        f = dict(dtype=torch.float32, device=q.device)
+        dq = new(_shape(layout, B, Hk, T, d), **o) if dq is None else dq
+        dk = new(_shape(layout, B, Hk, T, d), **o) if dk is None else dk
+        dv = new(_shape(layout, B, H, T, e), **o) if dv is None else dv
+        dbeta = new(gate, **f) if dbeta is None else dbeta
+        if g is not None and dg is None:
+            dg = new(gate, **f)
+        if d_init_state is None and want_d_init:
+            d_init_state = torch.empty((B, H, d, e), **f)
+        _check(dq, "dq", _shape(layout, B, Hk, T, d), odt)
+        _check(dk, "dk", _shape(layout, B, Hk, T, d), odt)
+        _check(dv, "dv", _shape(layout, B, H, T, e), odt)
+        _check(dbeta, "dbeta", gate, torch.float32)
+        if dg is not None:
+            _check(dg, "dg", gate, torch.float32)
+        _same_device(q.device, dout=dout, dq=dq, dk=dk, dv=dv, dg=dg, dbeta=dbeta)
+        wp, wn, keep = _own_workspace(la2_gdr_workspace_bytes(B, Hk, H, T, d, e, dt, 1), q.device,
+                                      stream, workspace)
+        st = la2_gdr_bwd_raw(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), beta.data_ptr(),
+                             dout.data_ptr(), _ptr(init_state), _ptr(d_final_state), dq.data_ptr(),
+                             dk.data_ptr(), dv.data_ptr(), _ptr(dg), dbeta.data_ptr(),
+                             _ptr(d_init_state), _ptr(seq_lens), B, Hk, H, T, d, e, dt, oc,
+                             _LAYOUTS[layout], wp, wn, sp)
+    if st != LA2_OK:
+        raise LA2Error(st, "la2_gdr_bwd")
+    r = (dq, dk, dv, dg, dbeta)
+    return r if d_init_state is None else r + (d_init_state,)
+
+
+def la2_gdr_decode(q, k, v, g, beta, states, slots=None, out=None, stream=None) -> torch.Tensor:
+    """One token of the gated delta rule for each sequence, on its slot of the pool `states`
+    ([slots, H, d, e] fp32, updated in place); returns out [B, H, e] fp32.
+
+    q, k [B, Hk, d], v [B, H, e] (bf16 or fp32), g (or None) and beta fp32 [B, H]; slots int32 [B]
+    (None: sequence b has slot b).  A slot outside the pool, or named by an earlier row already,
+    gives zeros and changes no state."""
+    if q.dim() != 3 or v.dim() != 3 or states.dim() != 4:
+        raise ValueError("q and v must have 3 dimensions, states 4")
+    B, Hk, d = q.shape
+    H, e = v.shape[1:]
+    dt = _dtype_code(q)
+    _check(q, "q", (B, Hk, d), q.dtype)
+    _check(k, "k", (B, Hk, d), q.dtype)
+    _check(v, "v", (B, H, e), q.dtype)
+    _check(beta, "beta", (B, H), torch.float32)
+    if g is not None:
+        _check(g, "g", (B, H), torch.float32)
+    n_slots = states.shape[0]
+    _check(states, "states", (n_slots, H, d, e), torch.float32)
+    if slots is not None:
+        _check(slots, "slots", (B,), torch.int32)
+    elif n_slots < B:
+        raise ValueError(f"{B} sequences but {n_slots} slots")
+    with torch.cuda.device(q.device):
+        sp = _stream_on(stream, q.device)
+        if out is None:
+            out = torch.empty((B, H, e), dtype=torch.float32, device=q.device)
+        _check(out, "out", (B, H, e), torch.float32)
+        _same_device(q.device, k=k, v=v, g=g, beta=beta, states=states, slots=slots, out=out)
+        st = la2_gdr_decode_raw(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), beta.data_ptr(),
+                                states.data_ptr(), _ptr(slots), n_slots, out.data_ptr(), B, Hk, H,
+                                d, e, dt, sp)
+    if st != LA2_OK:
+        raise LA2Error(st, "la2_gdr_decode")
+    return out
+
+
+def la2_state_copy(states, src, dst, stream=None) -> torch.Tensor:
+    """Slot copies inside the pool `states` ([slots, ...] fp32, in place): slot dst[i] takes what
+    slot src[i] held before the call, src[i] < 0 clears it (src, dst int32 [n]).  Pairs outside
+    the pool do nothing; of several pairs with one destination the last counts.  Returns states."""
+    if states.dim() < 1 or src.dim() != 1:
+        raise ValueError("states must have a slot dimension, src and dst one dimension")
+    n = src.shape[0]
+    _check(states, "states", states.shape, torch.float32)
+    _check(src, "src", (n,), torch.int32)
+    _check(dst, "dst", (n,), torch.int32)
+    _same_device(states.device, src=src, dst=dst)
+    n_slots = states.shape[0]
+    with torch.cuda.device(states.device):
+        st = la2_state_copy_raw(states.data_ptr(), src.data_ptr(), dst.data_ptr(), n, n_slots,
+                                states.numel() // n_slots if n_slots else 0,
+                                _stream_on(stream, states.device))
+    if st != LA2_OK:
+        raise LA2Error(st, "la2_state_copy")
+    return states

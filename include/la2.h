@@ -380,6 +380,95 @@ la2_status la2_bwd_norm(const void *q, const void *k, const void *v, const float
                         la2_layout layout, void *workspace, size_t workspace_bytes,
                         la2_stream_t stream);
 
+/*
+ * The gated delta rule.  Each position first forgets (a per-position, per-head
+ * gate), then corrects the state towards its value along its key:
+ *
+ *   S_t = a_t (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,   a_t = exp(g_t),
+ *   o_t = S_t^T q_t                                    (S_{-1} = init_state or 0),
+ *
+ * the recurrence of la2_fwd_state with a gate per position in place of the
+ * per-head decay and a write that first takes out what the state already
+ * answers for k_t.  No 1/sqrt(d) and no normalisation of k inside the call; the
+ * caller keeps beta_t |k_t|^2 within (0, 2) for a state that does not grow.
+ *
+ * q, k: [B, Hk, T, d] of `dtype` (or [B, T, Hk, d], see la2_layout); v, out,
+ * dout, dv: [B, H, T, e] (or [B, T, H, e]); g (log-gate, natural logarithm;
+ * NULL: no gate, a_t = 1) and beta: fp32 [B, H, T] (or [B, T, H]).  H is a
+ * multiple of Hk; value head h reads key head h / (H / Hk), and dq and dk are
+ * sums over the value heads that share a key head, in a fixed order.  A gate of
+ * -inf (or any g below -104, where exp(g) is 0 in fp32) forgets everything.
+ *
+ * seq_lens: device int32 [B], or NULL (every sequence has T rows): sequence b
+ * has seq_lens[b] rows, brought into 0 .. T; rows behind them are not read, and
+ * left as they were in out, dq, dk, dv, dg and dbeta.  The final state is the
+ * one after the last row of each sequence.
+ *
+ * init_state, final_state, d_final_state, d_init_state: fp32 [B, H, d, e], or
+ * NULL (zero / not wanted); T = 0 or an empty sequence hands the initial state
+ * (d_final_state) on.  out, dq, dk, dv have type out_dtype (F32, or BF16 with
+ * BF16 inputs); dg (may be NULL, and must be without g), dbeta and the states
+ * are fp32.  No output may alias an input or another output.
+ *
+ * 1 <= d, e <= 128 for both dtypes (more: LA2_ERR_UNSUPPORTED).  q, k, v, out,
+ * dout, dq, dk, dv 16-byte aligned, the others 4-byte.  workspace: device
+ * memory of at least la2_gdr_workspace_bytes() bytes, 256-byte aligned, not
+ * used by another call that may run at the same time; it grows with T (the
+ * backward keeps the state at each chunk's border).  The result does not
+ * depend on scheduling (no atomics).  Asynchronous on `stream`.
+ *
+ * la2_gdr_bwd gives the gradients of
+ * L = sum_t dout_t . out_t + <d_final_state, S_last>.
+ */
+size_t la2_gdr_workspace_bytes(int B, int Hk, int H, int T, int d, int e, la2_dtype dtype,
+                               int is_bwd);
+
+la2_status la2_gdr_fwd(const void *q, const void *k, const void *v, const float *g,
+                       const float *beta, void *out, const float *init_state, float *final_state,
+                       const int *seq_lens, int B, int Hk, int H, int T, int d, int e,
+                       la2_dtype dtype, la2_dtype out_dtype, la2_layout layout, void *workspace,
+                       size_t workspace_bytes, la2_stream_t stream);
+
+la2_status la2_gdr_bwd(const void *q, const void *k, const void *v, const float *g,
+                       const float *beta, const void *dout, const float *init_state,
+                       const float *d_final_state, void *dq, void *dk, void *dv, float *dg,
+                       float *dbeta, float *d_init_state, const int *seq_lens, int B, int Hk,
+                       int H, int T, int d, int e, la2_dtype dtype, la2_dtype out_dtype,
+                       la2_layout layout, void *workspace, size_t workspace_bytes,
+                       la2_stream_t stream);
+
+/*
+ * One token of the gated delta rule for each of B sequences whose states live
+ * in a pool [n_slots, H, d, e] (fp32):  with S = states[slots[b], h],
+ *
+ *   u = beta (v - a S^T k),   S <- a S + k u^T,   out = S^T q  (the new state).
+ *
+ * q, k: [B, Hk, d]; v: [B, H, e] of `dtype` (element aligned); g (or NULL), beta:
+ * fp32 [B, H]; out: fp32 [B, H, e].  slots: device int32 [B], or NULL (sequence
+ * b has slot b).  A slot outside 0 .. n_slots - 1 (the padding of a captured
+ * batch), or one that an earlier row of the call already names, gives a row of
+ * zeros and changes no state.  1 <= d, e <= 128.  One launch, asynchronous on
+ * `stream`; no workspace.
+ */
+la2_status la2_gdr_decode(const void *q, const void *k, const void *v, const float *g,
+                          const float *beta, float *states, const int *slots, int n_slots,
+                          float *out, int B, int Hk, int H, int d, int e, la2_dtype dtype,
+                          la2_stream_t stream);
+
+/*
+ * Copies inside a pool of states [n_slots, slot_elems] (fp32): for every pair i
+ * slot dst[i] takes what slot src[i] held before the call; src[i] < 0 clears
+ * the slot.  Forking (one source, several destinations), compacting (sources
+ * that are destinations of other pairs) and freeing are lists of such pairs.
+ * A pair with dst outside 0 .. n_slots - 1 or src >= n_slots does nothing;
+ * where a slot is the destination of several pairs the last one counts.  src,
+ * dst: device int32 [n]; n <= 4096 (more: LA2_ERR_UNSUPPORTED).  The states of
+ * la2_decode and la2_gdr_decode are such pools with slot_elems = H d e.  One
+ * launch, asynchronous on `stream`; no workspace.
+ */
+la2_status la2_state_copy(float *states, const int *src, const int *dst, int n, int n_slots,
+                          long long slot_elems, la2_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 const char *la2_status_str(la2_status status);
 

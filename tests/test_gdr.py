@@ -1,0 +1,621 @@
+"""The gated delta rule (la2_gdr_fwd, la2_gdr_bwd, la2_gdr_decode) and the state pool's copies (la2_state_copy).
+
+CPU: the 64-bit reference against autograd, differences and special cases; refusals.  GPU: every call against the
+reference.
+
+Tolerances.  With fp32 outputs max|err| <= TOL rms(exact).  fp32 inputs: 1e-5, the library's contract: a result is a
+sum of at most 128 + 128 products whose roundings (2^-24 each) add up like a random walk, sqrt(256) 2^-24 = 1e-6 of
+the sum's size, and the largest element of a few 10^4 is some 5 sigma out.  bf16 inputs: operands that the kernels form
+are split into two bf16 numbers (off by at most 2^-8 2^-8 = 2^-16 relative), so a product is off by 2^-15 = 3e-5 of
+itself at worst; the sums average that, and 5e-5 rms covers the largest element.  A bf16 output adds its one rounding,
+2^-8 |x|.  dg is a difference of terms larger than itself (`mag` in the reference, summed over a chunk of 64 rows): its
+error is measured against rms(dg) + 8 rms(mag), 8 = sqrt(64)."""
+import numpy as np
+import pytest
+import torch
+
+import gdr_ref as R
+from causal_linear_attention_la2_b200 import la2 as L
+
+TOL = {torch.float32: 1e-5, torch.bfloat16: 5e-5}
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+# ------------------------------------------------------------------------------------------------ CPU: reference
+
+def _leaves(x):
+    return {n: x[n].double().requires_grad_() for n in ("q", "k", "v", "g", "beta", "init")}
+
+
+@pytest.mark.parametrize("T,lens", [(1, None), (7, None), (9, [9, 4, 0])])
+def test_reference_gradients_are_autograds(T, lens):
+    x = R.make(3, 2, 4, T, 5, 6, F32, 1, init=True, final=True, lens=lens)
+    y = dict(x, **_leaves(x))
+    o, S = R.forward(y)
+    ((o * x["do"].double()).sum() + (S * x["dfinal"].double()).sum()).backward()
+    r = R.backward(x)
+    for n, m in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("g", "dg"), ("beta", "dbeta"), ("init", "dinit")):
+        assert torch.allclose(y[n].grad, r[m], rtol=1e-11, atol=1e-12), n
+
+
+def test_reference_gradients_are_differences():
+    x = R.make(1, 1, 2, 6, 4, 3, F32, 2, init=True, final=True)
+    x = {n: t.double() if t is not None and t.is_floating_point() else t for n, t in x.items()}
+
+    def loss(y):
+        o, S = R.forward(y)
+        return float((o * x["do"]).sum() + (S * x["dfinal"]).sum())
+
+    r, h = R.backward(x), 1e-4
+    gen = torch.Generator().manual_seed(0)
+    for n, m in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("g", "dg"), ("beta", "dbeta"), ("init", "dinit")):
+        z = torch.randn(x[n].shape, generator=gen, dtype=torch.float64)
+        f = lambda s: loss(dict(x, **{n: x[n] + s * z}))  # noqa: E731,B023
+        diff = (8 * (f(h) - f(-h)) - (f(2 * h) - f(-2 * h))) / (12 * h)  # error O(h^4) = 1e-16, roundings 1e-16 / h
+        assert abs(diff - float((r[m] * z).sum())) <= 1e-9, n
+
+
+def test_reference_without_overlap_is_linear_attention():
+    """Orthonormal keys with beta = 1 never correct one another: o_t = sum_s e^{G_t - G_s} (q_t . k_s) v_s."""
+    x = R.make(1, 1, 1, 8, 8, 5, F32, 3)
+    x["k"] = torch.linalg.qr(torch.randn(8, 8, dtype=torch.float64, generator=torch.Generator().manual_seed(1)))[0][None, None]
+    x["beta"] = torch.ones(1, 1, 8)
+    o, _ = R.forward(x)
+    G = x["g"].double().cumsum(-1)[0, 0]
+    M = (G[:, None] - G[None]).exp().tril()
+    want = (x["q"][0, 0].double() @ x["k"][0, 0].T * M) @ x["v"][0, 0].double()
+    assert torch.allclose(o[0, 0], want, rtol=1e-12, atol=1e-13)
+
+
+# ------------------------------------------------------------------------------------------------ CPU: refusals
+
+FAKE = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from causal_linear_attention_la2_b200 import build
+    build.build()
+    return L.load()
+
+
+def _raw_fwd(**kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, g=FAKE, beta=FAKE, out=FAKE, init=0, fin=0, lens=0, B=1, Hk=1, H=2, T=64, d=64, e=64,
+             dtype=1, out_dtype=1, layout=0, ws=FAKE, n=1 << 40)
+    a.update(kw)
+    return L.la2_gdr_fwd_raw(*a.values())
+
+
+def _raw_bwd(**kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, g=FAKE, beta=FAKE, dout=FAKE, init=0, dfinal=0, dq=FAKE, dk=FAKE, dv=FAKE, dg=FAKE,
+             dbeta=FAKE, dinit=0, lens=0, B=1, Hk=1, H=2, T=64, d=64, e=64, dtype=1, out_dtype=1, layout=0, ws=FAKE,
+             n=1 << 40)
+    a.update(kw)
+    return L.la2_gdr_bwd_raw(*a.values())
+
+
+def _raw_decode(**kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, g=FAKE, beta=FAKE, states=FAKE, slots=0, n_slots=4, out=FAKE, B=1, Hk=1, H=2, d=64,
+             e=64, dtype=1)
+    a.update(kw)
+    return L.la2_gdr_decode_raw(*a.values())
+
+
+def _raw_copy(**kw):
+    a = dict(states=FAKE, src=FAKE, dst=FAKE, n=2, n_slots=4, elems=64)
+    a.update(kw)
+    return L.la2_state_copy_raw(*a.values())
+
+
+SIZES = [dict(B=-1), dict(Hk=-1), dict(H=-2), dict(Hk=0), dict(H=3, Hk=2), dict(d=0), dict(e=0), dict(dtype=5)]
+
+
+@pytest.mark.parametrize("kw", SIZES + [dict(T=-1), dict(out_dtype=3), dict(layout=2), dict(layout=-1)])
+def test_sequence_calls_refuse_sizes(lib, kw):
+    assert _raw_fwd(**kw) == L.LA2_ERR_INVALID_ARG
+    assert _raw_bwd(**kw) == L.LA2_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", SIZES + [dict(n_slots=-1)])
+def test_decode_refuses_sizes(lib, kw):
+    assert _raw_decode(**kw) == L.LA2_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(d=129), dict(e=200)])
+def test_wide_heads_are_unsupported(lib, kw):
+    for call in (_raw_fwd, _raw_bwd, _raw_decode):
+        assert call(**kw) == L.LA2_ERR_UNSUPPORTED
+    assert _raw_fwd(dtype=0) == L.LA2_ERR_UNSUPPORTED  # bf16 outputs of fp32 inputs
+    assert _raw_bwd(dtype=0) == L.LA2_ERR_UNSUPPORTED
+
+
+def test_more_rows_than_a_grid_holds_are_unsupported(lib):
+    assert _raw_fwd(B=1 << 14, H=1 << 13, T=1 << 20) == L.LA2_ERR_UNSUPPORTED
+    assert L.la2_gdr_workspace_bytes(1 << 14, 1, 1 << 13, 1 << 20, 64, 64, 1, 1) == (1 << 64) - 1
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "beta", "out"])
+def test_forward_refuses_null_and_misaligned(lib, name):
+    assert _raw_fwd(**{name: 0}) == L.LA2_ERR_INVALID_ARG
+    assert _raw_fwd(**{name: FAKE + (2 if name == "beta" else 8)}) == L.LA2_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "beta", "dout", "dq", "dk", "dv", "dbeta"])
+def test_backward_refuses_null_and_misaligned(lib, name):
+    assert _raw_bwd(**{name: 0}) == L.LA2_ERR_INVALID_ARG
+    assert _raw_bwd(**{name: FAKE + (2 if name in ("beta", "dbeta") else 8)}) == L.LA2_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name", ["init", "lens", "g"])
+def test_optional_pointers_refuse_misalignment(lib, name):
+    for call in (_raw_fwd, _raw_bwd):
+        assert call(**{name: FAKE + 2}) == L.LA2_ERR_INVALID_ARG
+
+
+def test_gate_gradient_needs_a_gate(lib):
+    assert _raw_bwd(g=0) == L.LA2_ERR_INVALID_ARG
+
+
+def test_workspace_is_checked(lib):
+    need = L.la2_gdr_workspace_bytes(1, 1, 2, 64, 64, 64, 1, 1)
+    assert need > 0
+    assert _raw_bwd(ws=0, n=0) == L.LA2_ERR_WORKSPACE
+    assert _raw_bwd(n=need - 1) == L.LA2_ERR_WORKSPACE
+    assert _raw_bwd(ws=FAKE + 16) == L.LA2_ERR_INVALID_ARG
+
+
+def test_empty_problems(lib):
+    for kw in (dict(B=0), dict(H=0), dict(H=0, Hk=0), dict(T=0)):
+        assert _raw_fwd(**{n: 0 for n in ("q", "k", "v", "g", "beta", "out")}, **kw) == L.LA2_OK
+        assert _raw_bwd(**{n: 0 for n in ("q", "k", "v", "g", "beta", "dout", "dq", "dk", "dv", "dg", "dbeta")},
+                        **kw) == L.LA2_OK
+    assert _raw_decode(B=0, q=0, states=0) == L.LA2_OK
+    assert _raw_copy(n=0, states=0, src=0, dst=0) == L.LA2_OK
+    assert _raw_copy(n_slots=0, states=0) == L.LA2_OK
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "beta", "out", "states"])
+def test_decode_refuses_null_and_misaligned(lib, name):
+    assert _raw_decode(**{name: 0}) == L.LA2_ERR_INVALID_ARG
+    assert _raw_decode(**{name: FAKE + 1}) == L.LA2_ERR_INVALID_ARG
+
+
+def test_copy_refuses(lib):
+    for kw in (dict(n=-1), dict(n_slots=-1), dict(elems=-1), dict(states=0), dict(src=0), dict(dst=0),
+               dict(states=FAKE + 2), dict(src=FAKE + 1), dict(dst=FAKE + 2)):
+        assert _raw_copy(**kw) == L.LA2_ERR_INVALID_ARG
+    assert _raw_copy(n=4097) == L.LA2_ERR_UNSUPPORTED
+
+
+def test_the_binding_refuses_cpu_tensors():
+    z = torch.zeros(1, 1, 4, 8)
+    with pytest.raises(ValueError):
+        L.la2_gdr_fwd(z, z, z, None, z[..., 0])
+    with pytest.raises(ValueError):
+        L.la2_gdr_bwd(z, z, z, None, z[..., 0], z)
+    with pytest.raises(ValueError):
+        L.la2_gdr_decode(z[0], z[0], z[0], None, z[0, ..., 0], z)
+    with pytest.raises(ValueError):
+        L.la2_state_copy(z, torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+# ------------------------------------------------------------------------------------------------ GPU
+
+@pytest.fixture(scope="module")
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from causal_linear_attention_la2_b200 import build
+    build.build()
+    L.load()
+    return torch.device("cuda")
+
+
+def _put(x, layout, dev):
+    """The call's tensors on the device; NaN behind each sequence's end."""
+    y = {}
+    for n, t in x.items():
+        if t is None:
+            y[n] = None
+            continue
+        if n in ("q", "k", "v", "do", "g", "beta"):
+            if x["lens"] is not None:
+                t = t.clone()
+                for b, m in enumerate(x["lens"].tolist()):
+                    t[b, :, max(0, m):] = float("nan")
+            if layout == "bthd":
+                t = t.transpose(1, 2)
+        y[n] = t.contiguous().to(dev)
+    return y
+
+
+def _back(t, layout):
+    t = t.detach().double().cpu()
+    return t.transpose(1, 2) if layout == "bthd" else t
+
+
+def _close(got, want, tol, extra=0.0, name=""):
+    """max|err| <= tol (rms(want) + extra), one bf16 rounding more where `got` is bf16."""
+    assert torch.isfinite(got).all(), name
+    if not want.numel():
+        return
+    rms = float(want.square().mean().sqrt()) + extra
+    slack = 2.0 ** -8 * want.abs() if name.endswith("bf16") else 0.0
+    err = float(((got - want).abs() - slack).max())
+    assert err <= tol * rms * (1 + 2.0 ** -8) + 1e-30, f"{name}: {err / max(rms, 1e-300):.3e} rms"
+
+
+def _check_fwd(dev, x, layout="bhtd", out_dtype=None, **kw):
+    y = _put(x, layout, dev)
+    o, S = L.la2_gdr_fwd(y["q"], y["k"], y["v"], y["g"], y["beta"], layout=layout, init_state=y["init"],
+                         seq_lens=y["lens"], want_final=True, out_dtype=out_dtype, **kw)
+    ro, rS = R.forward(x)
+    tol = TOL[x["q"].dtype]
+    _close(_back(o, layout), ro, tol, name="o" + ("bf16" if out_dtype == BF16 else ""))
+    _close(S.double().cpu(), rS, tol, name="state")
+    return o, S
+
+
+def _check_bwd(dev, x, layout="bhtd", out_dtype=None):
+    y = _put(x, layout, dev)
+    got = L.la2_gdr_bwd(y["q"], y["k"], y["v"], y["g"], y["beta"], y["do"], layout=layout, init_state=y["init"],
+                        d_final_state=y["dfinal"], seq_lens=y["lens"], want_d_init=True, out_dtype=out_dtype)
+    r = R.backward(x)
+    tol = TOL[x["q"].dtype]
+    for n, t in zip(("dq", "dk", "dv", "dg", "dbeta", "dinit"), got):
+        if t is None:
+            assert n == "dg" and x["g"] is None
+            continue
+        extra = 8 * float(r["mag"].square().mean().sqrt()) if n == "dg" else 0.0
+        half = out_dtype == BF16 and n in ("dq", "dk", "dv")
+        _close(t.double().cpu() if n == "dinit" else _back(t, layout), r[n], tol, extra, n + ("bf16" if half else ""))
+    return got
+
+
+LENGTHS = [1, 2, 15, 16, 17, 33, 63, 64, 65, 127, 128, 130, 200]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", LENGTHS)
+@pytest.mark.parametrize("dtype,d,e", [(BF16, 64, 64), (BF16, 128, 128), (F32, 64, 64), (F32, 33, 20)])
+def test_lengths(gpu, dtype, d, e, T):
+    x = R.make(2, 1, 2, T, d, e, dtype, T + d, init=T % 2 == 0, final=T % 3 == 0)
+    _check_fwd(gpu, x)
+    _check_bwd(gpu, x)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,e", [(BF16, 64, 128), (BF16, 128, 64), (BF16, 1, 1), (BF16, 72, 100), (BF16, 128, 17),
+                                       (F32, 1, 1), (F32, 128, 128), (F32, 3, 128), (F32, 127, 5), (F32, 128, 16)])
+@pytest.mark.parametrize("layout", ["bhtd", "bthd"])
+def test_widths_and_layouts(gpu, dtype, d, e, layout):
+    x = R.make(2, 2, 4, 77, d, e, dtype, d * 3 + e, init=True, final=True)
+    _check_fwd(gpu, x, layout)
+    _check_bwd(gpu, x, layout)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("layout", ["bhtd", "bthd"])
+@pytest.mark.parametrize("d,e", [(64, 64), (128, 128), (64, 128), (40, 24)])
+def test_output_types(gpu, d, e, layout, out_dtype):
+    x = R.make(1, 2, 2, 100, d, e, BF16, 5, init=True, final=True)
+    _check_fwd(gpu, x, layout, out_dtype)
+    _check_bwd(gpu, x, layout, out_dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hk,H", [(1, 1), (1, 4), (3, 3), (2, 6), (5, 5)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_heads(gpu, dtype, Hk, H):
+    x = R.make(3, Hk, H, 70, 64, 64, dtype, H, final=True)
+    _check_fwd(gpu, x)
+    _check_bwd(gpu, x)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["bhtd", "bthd"])
+@pytest.mark.parametrize("dtype,d,e", [(BF16, 64, 64), (BF16, 128, 128), (F32, 24, 40)])
+def test_ragged_batches_leave_rows_behind_the_end(gpu, dtype, d, e, layout):
+    """Lengths of 0, 1, chunk borders and beyond T; NaN in the inputs and a mark in the outputs behind each end."""
+    lens = [0, 1, 64, 65, 131, 32, -3, 1000]
+    T = 131
+    x = R.make(len(lens), 1, 2, T, d, e, dtype, 9, init=True, final=True, lens=lens)
+    _check_fwd(gpu, x, layout)
+    _check_bwd(gpu, x, layout)
+    y = _put(x, layout, gpu)
+    mark = 7.0
+    like = lambda t, dt=torch.float32: torch.full(t.shape, mark, dtype=dt, device=gpu)  # noqa: E731
+    o = like(y["v"])
+    L.la2_gdr_fwd(y["q"], y["k"], y["v"], y["g"], y["beta"], layout=layout, seq_lens=y["lens"], out=o)
+    outs = dict(dq=like(y["q"]), dk=like(y["k"]), dv=like(y["v"]), dg=like(y["g"]), dbeta=like(y["beta"]))
+    L.la2_gdr_bwd(y["q"], y["k"], y["v"], y["g"], y["beta"], y["do"], layout=layout, seq_lens=y["lens"], **outs)
+    for name, t in dict(outs, o=o).items():
+        t = t.transpose(1, 2) if layout == "bthd" else t
+        for b, m in enumerate(lens):
+            m = min(max(m, 0), T)
+            assert (t[b, :, m:] == mark).all(), name
+            assert torch.isfinite(t[b, :, :m]).all(), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [(BF16, 64), (BF16, 128), (F32, 48)])
+def test_without_a_gate(gpu, dtype, d):
+    x = R.make(2, 2, 2, 150, d, d, dtype, 4, gate=False, init=True, final=True)
+    _check_fwd(gpu, x)
+    _check_bwd(gpu, x)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [(BF16, 64), (BF16, 128), (F32, 48)])
+def test_extreme_gates_and_strengths(gpu, dtype, d):
+    """Gates of -inf, -1e30 and 0 (forget all, keep all), beta of 0 and 1, repeated and zero keys."""
+    x = R.make(2, 1, 2, 140, d, d, dtype, 8, init=True, final=True)
+    x["g"][:, :, 3] = -float("inf")
+    x["g"][:, :, 64] = -1e30
+    x["g"][:, :, 66:75] = -300.0
+    x["g"][:, :, 100:] = 0.0
+    x["beta"][:, :, 5:9] = 0.0
+    x["beta"][:, :, 20:40] = 1.0
+    x["beta"][:, :, 63] = 0.0
+    x["k"][:, :, 20:36] = x["k"][:, :, 20:21]
+    x["k"][:, :, 50] = 0.0
+    _check_fwd(gpu, x)
+    # the reference's product exp(-inf) * S is 0 and its gradients are finite
+    _check_bwd(gpu, x)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_correlated_keys(gpu, dtype):
+    """Keys close to one another with beta near 1: every position corrects nearly all of the ones before it."""
+    x = R.make(1, 1, 2, 192, 64, 64, dtype, 11, gate=False)
+    base = torch.randn(1, 1, 1, 64, generator=torch.Generator().manual_seed(3))
+    k = base / base.norm() + 0.1 * x["k"].float()
+    x["k"] = (k / k.norm(dim=-1, keepdim=True)).to(dtype)
+    x["beta"] = torch.full_like(x["beta"], 0.98)
+    _check_fwd(gpu, x)
+    _check_bwd(gpu, x)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,cut", [(BF16, 128, 64), (BF16, 64, 37), (F32, 50, 37)])
+def test_pieces_are_the_whole(gpu, dtype, d, cut):
+    """Forward and backward over two pieces with handed-on states against the reference over the whole."""
+    T = 150
+    x = R.make(2, 1, 2, T, d, d, dtype, 13, init=True, final=True)
+    y = _put(x, "bhtd", gpu)
+    part = lambda a, b: {n: (t[:, :, a:b].contiguous() if n in ("q", "k", "v", "do", "g", "beta") else t)  # noqa: E731
+                         for n, t in y.items()}
+    p, q = part(0, cut), part(cut, T)
+    o1, S1 = L.la2_gdr_fwd(p["q"], p["k"], p["v"], p["g"], p["beta"], init_state=y["init"], want_final=True)
+    o2, S2 = L.la2_gdr_fwd(q["q"], q["k"], q["v"], q["g"], q["beta"], init_state=S1, want_final=True)
+    g2 = L.la2_gdr_bwd(q["q"], q["k"], q["v"], q["g"], q["beta"], q["do"], init_state=S1, d_final_state=y["dfinal"],
+                       want_d_init=True)
+    g1 = L.la2_gdr_bwd(p["q"], p["k"], p["v"], p["g"], p["beta"], p["do"], init_state=y["init"], d_final_state=g2[5],
+                       want_d_init=True)
+    ro, rS = R.forward(x)
+    r, tol = R.backward(x), TOL[dtype]
+    _close(torch.cat([o1, o2], 2).double().cpu(), ro, tol, name="o")
+    _close(S2.double().cpu(), rS, tol, name="state")
+    for i, n in enumerate(("dq", "dk", "dv", "dg", "dbeta")):
+        extra = 8 * float(r["mag"].square().mean().sqrt()) if n == "dg" else 0.0
+        _close(torch.cat([g1[i], g2[i]], 2).double().cpu(), r[n], tol, extra, n)
+    _close(g1[5].double().cpu(), r["dinit"], tol, name="dinit")
+
+
+@pytest.mark.gpu
+def test_empty_sequences_hand_states_on(gpu):
+    s = torch.randn(2, 2, 8, 8, device=gpu)
+    z = torch.zeros(2, 2, 0, 8, device=gpu)
+    o, S = L.la2_gdr_fwd(z, z, z, z[..., 0], z[..., 0], init_state=s, want_final=True)
+    assert o.numel() == 0 and torch.equal(S, s)
+    assert torch.equal(L.la2_gdr_bwd(z, z, z, z[..., 0], z[..., 0], z, d_final_state=s, want_d_init=True)[5], s)
+    S = L.la2_gdr_fwd(z, z, z, None, z[..., 0], want_final=True)[1]
+    assert not S.any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 30)])
+def test_runs_are_bitwise_repeatable(gpu, dtype, d):
+    x = R.make(2, 2, 4, 260, d, d, dtype, 17, init=True, final=True)
+    y = _put(x, "bhtd", gpu)
+    a, b = ([*L.la2_gdr_fwd(y["q"], y["k"], y["v"], y["g"], y["beta"], want_final=True),
+             *L.la2_gdr_bwd(y["q"], y["k"], y["v"], y["g"], y["beta"], y["do"], want_d_init=True)] for _ in range(2))
+    for s, t in zip(a, b):
+        assert torch.equal(s, t)
+
+
+# ---- decode
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("dtype,d,e,Hk,H", [(BF16, 128, 128, 2, 4), (BF16, 64, 64, 3, 3), (F32, 64, 64, 1, 2),
+                                            (F32, 1, 1, 1, 1), (F32, 100, 72, 2, 2), (BF16, 128, 7, 1, 3),
+                                            (F32, 5, 127, 1, 1), (F32, 128, 4, 1, 1), (BF16, 127, 126, 1, 1)])
+def test_decode_step(gpu, dtype, d, e, Hk, H, gate):
+    B, N = 5, 9
+    x = R.make(B, Hk, H, 1, d, e, dtype, d + e, gate=gate)
+    one = {n: (x[n][:, :, 0].contiguous() if x[n] is not None else None) for n in ("q", "k", "v", "g", "beta")}
+    pool = torch.randn(N, H, d, e, generator=torch.Generator().manual_seed(1))
+    slots = torch.tensor([7, -1, 2, 9, 0], dtype=torch.int32)
+    dp = pool.to(gpu)
+    dev = {n: (t.to(gpu) if t is not None else None) for n, t in one.items()}
+    o = L.la2_gdr_decode(dev["q"], dev["k"], dev["v"], dev["g"], dev["beta"], dp, slots=slots.to(gpu))
+    live = [0, 2, 4]
+    at = slots[live].long()
+    ro, rS = R.decode(*(None if one[n] is None else one[n][live] for n in ("q", "k", "v", "g", "beta")), pool[at])
+    # fp32 arithmetic whatever the inputs' type
+    _close(o[live].double().cpu(), ro, 1e-5, name="o")
+    _close(dp[at].double().cpu(), rS, 1e-5, name="state")
+    rest = [i for i in range(N) if i not in at.tolist()]
+    assert torch.equal(dp[rest].cpu(), pool[rest])
+    assert not o[[1, 3]].any()
+
+
+@pytest.mark.gpu
+def test_decode_same_slot_twice(gpu):
+    """The first row that names a slot has it; later ones give zeros."""
+    x = R.make(4, 1, 2, 1, 64, 64, F32, 2)
+    one = {n: x[n][:, :, 0].contiguous() for n in ("q", "k", "v", "g", "beta")}
+    pool = torch.randn(3, 2, 64, 64)
+    dp, dev = pool.to(gpu), {n: t.to(gpu) for n, t in one.items()}
+    slots = torch.tensor([1, 1, 0, 1], dtype=torch.int32, device=gpu)
+    o = L.la2_gdr_decode(dev["q"], dev["k"], dev["v"], dev["g"], dev["beta"], dp, slots=slots)
+    ro, rS = R.decode(*(one[n][[0, 2]] for n in ("q", "k", "v", "g", "beta")), pool[[1, 0]])
+    _close(o[[0, 2]].double().cpu(), ro, 1e-5, name="o")
+    _close(dp[[1, 0]].double().cpu(), rS, 1e-5, name="state")
+    assert not o[[1, 3]].any() and torch.equal(dp[2].cpu(), pool[2])
+
+
+@pytest.mark.gpu
+def test_decode_without_slots_and_unaligned_pool(gpu):
+    x = R.make(3, 2, 2, 1, 16, 20, F32, 2)
+    one = {n: x[n][:, :, 0].contiguous().to(gpu) for n in ("q", "k", "v", "g", "beta")}
+    flat = torch.randn(1 + 4 * 2 * 16 * 20, device=gpu)
+    pool = flat[1:].view(4, 2, 16, 20)  # 4-byte aligned
+    before = pool.clone()
+    o = L.la2_gdr_decode(one["q"], one["k"], one["v"], one["g"], one["beta"], pool)
+    ro, rS = R.decode(*(x[n][:, :, 0] for n in ("q", "k", "v", "g", "beta")), before[:3].cpu())
+    _close(o.double().cpu(), ro, 1e-5, name="o")
+    _close(pool[:3].double().cpu(), rS, 1e-5, name="state")
+    assert torch.equal(pool[3], before[3])
+    with pytest.raises(ValueError):
+        L.la2_gdr_decode(one["q"], one["k"], one["v"], one["g"], one["beta"], pool[:2])
+
+
+# ---- the state pool
+
+def _copied(pool, src, dst):
+    want = pool.clone()
+    for s, t in zip(src, dst):
+        if 0 <= t < len(pool) and s < len(pool):
+            want[t] = pool[s] if s >= 0 else 0.0
+    return want
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(2, 16, 16), (1, 1, 1), (3, 5, 7), (1, 128, 128), (40, 64, 64)])
+@pytest.mark.parametrize("n", [1, 3, 17, 60])
+def test_state_copy(gpu, shape, n):
+    """Random pairs: chains, cycles, forks, clears, slots out of range and repeated destinations."""
+    N = 41
+    rng = np.random.RandomState(n)
+    src = rng.randint(-2, N + 1, n).tolist()
+    dst = rng.randint(-1, N + 1, n).tolist()
+    pool = torch.randn(N, *shape, device=gpu)
+    want = _copied(pool.cpu(), src, dst)
+    i32 = dict(dtype=torch.int32, device=gpu)
+    assert L.la2_state_copy(pool, torch.tensor(src, **i32), torch.tensor(dst, **i32)) is pool
+    assert torch.equal(pool.cpu(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,elems", [(257, 3), (1000, 16), (4096, 40), (4096, 9)])
+def test_state_copy_of_many_pairs(gpu, n, elems):
+    """A rotation of the whole pool, then one destination for all pairs."""
+    flat = torch.randn(n * elems + 1, device=gpu)
+    for pool in (flat[:n * elems].view(n, elems), flat[1:].view(n, elems)):
+        i = torch.arange(n, dtype=torch.int32, device=gpu)
+        before = pool.clone()
+        L.la2_state_copy(pool, i, torch.roll(i, 1).contiguous())
+        assert torch.equal(pool[torch.roll(i, 1).long()], before)
+        before = pool.clone()
+        L.la2_state_copy(pool, i, torch.full_like(i, 5))
+        before[5] = before[n - 1]
+        assert torch.equal(pool, before)
+
+
+# ---- together, and how a program runs them
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 32)])
+def test_prefill_fork_and_decode(gpu, dtype, d):
+    """Two ragged prompts into slots, each forked, every branch continued token by token; against the reference over
+    prompt and continuation."""
+    B, H, P, G = 2, 2, 70, 5
+    lens = [70, 33]
+    x = R.make(B, 1, H, P, d, d, dtype, 21, lens=lens)
+    y = _put(x, "bthd", gpu)
+    _, S = L.la2_gdr_fwd(y["q"], y["k"], y["v"], y["g"], y["beta"], layout="bthd", seq_lens=y["lens"], want_final=True)
+    pool = torch.full((6, H, d, d), float("nan"), device=gpu)
+    pool[1], pool[4] = S[0], S[1]
+    i32 = dict(dtype=torch.int32, device=gpu)
+    L.la2_state_copy(pool, torch.tensor([1, 4, -1], **i32), torch.tensor([0, 5, 3], **i32))
+    more = [R.make(4, 1, H, 1, d, d, dtype, 30 + i) for i in range(G)]
+    slots = torch.tensor([1, 0, 4, 5], **i32)
+    outs = []
+    for m in more:
+        t = {n: m[n][:, :, 0].contiguous().to(gpu) for n in ("q", "k", "v", "g", "beta")}
+        outs.append(L.la2_gdr_decode(t["q"], t["k"], t["v"], t["g"], t["beta"], pool, slots=slots))
+    for row, src in enumerate((0, 0, 1, 1)):
+        n = lens[src]
+        z = {m: torch.cat([x[m][src:src + 1, :, :n]] + [s[m][row:row + 1] for s in more], 2)
+             for m in ("q", "k", "v", "do", "g", "beta")}
+        ro, rS = R.forward(dict(z, init=None, lens=None))
+        got = torch.stack([o[row] for o in outs], 1).double().cpu()
+        _close(got, ro[0, :, n:], TOL[dtype], name="o")
+        _close(pool[int(slots[row])].double().cpu(), rS[0], TOL[dtype], name="state")
+    assert not pool[3].any() and torch.isnan(pool[2]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (F32, 32)])
+def test_two_streams_and_a_captured_step(gpu, dtype, d):
+    """A forward and backward captured into a graph and replayed on new inputs, with other calls on another stream."""
+    x = [R.make(2, 1, 2, 200, d, d, dtype, 40 + i, init=True, final=True) for i in range(2)]
+    y = [_put(t, "bhtd", gpu) for t in x]
+
+    def step(t):
+        o, S = L.la2_gdr_fwd(t["q"], t["k"], t["v"], t["g"], t["beta"], init_state=t["init"], want_final=True)
+        return [o, S, *L.la2_gdr_bwd(t["q"], t["k"], t["v"], t["g"], t["beta"], t["do"], init_state=t["init"],
+                                     d_final_state=t["dfinal"], want_d_init=True)]
+
+    want = [step(t) for t in y]
+    torch.cuda.synchronize()
+    held = {n: (t.clone() if t is not None else None) for n, t in y[0].items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(held)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for i in (1, 0):
+        for n, t in held.items():
+            if t is not None:
+                t.copy_(y[i][n])
+        graph.replay()
+        with torch.cuda.stream(side):
+            other = step(y[1 - i])
+        torch.cuda.synchronize()
+        for a, b in zip(got, want[i]):
+            assert torch.equal(a, b)
+        for a, b in zip(other, want[1 - i]):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_the_binding_refuses(gpu):
+    x = _put(R.make(2, 1, 2, 8, 16, 16, F32, 1), "bhtd", gpu)
+    a = (x["q"], x["k"], x["v"], x["g"], x["beta"])
+    with pytest.raises(ValueError):
+        L.la2_gdr_fwd(x["q"], x["k"][:, :, :4], *a[2:])
+    with pytest.raises(ValueError):
+        L.la2_gdr_fwd(x["q"], x["k"], x["v"], x["g"], x["beta"].transpose(1, 2))
+    with pytest.raises(ValueError):
+        L.la2_gdr_fwd(*a, layout="tbhd")
+    with pytest.raises(TypeError):
+        L.la2_gdr_fwd(x["q"].half(), *a[1:])
+    with pytest.raises(TypeError):
+        L.la2_gdr_fwd(x["q"], x["k"].bfloat16(), *a[2:])
+    with pytest.raises(TypeError):
+        L.la2_gdr_fwd(*a, seq_lens=torch.tensor([8, 8], device=gpu))
+    with pytest.raises(L.LA2Error):
+        L.la2_gdr_fwd(*a, out_dtype=BF16)  # fp32 inputs
+    with pytest.raises(ValueError):
+        L.la2_gdr_bwd(*a, x["v"][:1])
+    with pytest.raises(ValueError):
+        L.la2_gdr_bwd(x["q"], x["k"], x["v"], None, x["beta"], x["do"], dg=torch.empty_like(x["beta"]))
+    with pytest.raises(ValueError):
+        L.la2_gdr_bwd(*a, x["do"], workspace=torch.empty(16, dtype=torch.uint8, device=gpu))
+    with pytest.raises(TypeError):
+        L.la2_state_copy(x["v"], torch.zeros(1, dtype=torch.int64, device=gpu), torch.zeros(1, dtype=torch.int64, device=gpu))
