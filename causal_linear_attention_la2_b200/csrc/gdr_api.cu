@@ -1,12 +1,14 @@
 // gdr_api.cu -- the C ABI of the gated delta rule and of the state pool
 // (la2_gdr_*, la2_state_copy in include/la2.h): argument checks, workspace
-// layout and launches.  The kernels are in gdr_rec.cuh and state_pool.cuh.
+// layout and launches.  The kernels are in gdr_chunk.cuh (bf16, d and e 64 or
+// 128), gdr_rec.cuh (everything else) and state_pool.cuh.
 #include <cuda_runtime.h>
 
 #include <climits>
 #include <cstdint>
 #include <mutex>
 
+#include "gdr_chunk.cuh"
 #include "gdr_common.cuh"
 #include "gdr_rec.cuh"
 #include "la2.h"
@@ -24,12 +26,24 @@ bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(
 
 int cdiv(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
+bool set(const void* f, size_t bytes) {
+    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) == cudaSuccess;
+}
+
+template <int D>
+bool set_chunk_attrs() {
+    using namespace la2::gdr;
+    return set(reinterpret_cast<const void*>(gdr_prep<D>), sizeof(PrepSmem<D>)) &&
+           set(reinterpret_cast<const void*>(gdr_chain<D, false>), sizeof(WalkSmem<D>)) &&
+           set(reinterpret_cast<const void*>(gdr_chain<D, true>), sizeof(WalkSmem<D>)) &&
+           set(reinterpret_cast<const void*>(gdr_chain_rev<D>), sizeof(WalkSmem<D>)) &&
+           set(reinterpret_cast<const void*>(gdr_grad<D, 64>), sizeof(GradTiles<D, 64>)) &&
+           set(reinterpret_cast<const void*>(gdr_grad<D, 128>), sizeof(GradTiles<D, 128>));
+}
+
 bool set_smem_attrs() {
-    const auto set = [](const void* f, size_t bytes) {
-        return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) ==
-               cudaSuccess;
-    };
-    return set(reinterpret_cast<const void*>(la2::gdr::gdr_grad_rec<float>), sizeof(la2::gdr::GradSmem)) &&
+    return set_chunk_attrs<64>() && set_chunk_attrs<128>() &&
+           set(reinterpret_cast<const void*>(la2::gdr::gdr_grad_rec<float>), sizeof(la2::gdr::GradSmem)) &&
            set(reinterpret_cast<const void*>(la2::gdr::gdr_grad_rec<__nv_bfloat16>), sizeof(la2::gdr::GradSmem)) &&
            set(reinterpret_cast<const void*>(la2::gdr::pool_copy<float4>), 200 << 10) &&
            set(reinterpret_cast<const void*>(la2::gdr::pool_copy<float>), 200 << 10);
@@ -92,6 +106,68 @@ la2_status rec_backward(const Args& A, char* ws, cudaStream_t stream) {
     return launched();
 }
 
+// The tensor-core kernels' sizes.
+bool by_chunks(la2_dtype dtype, int d, int e) {
+    return dtype == LA2_DTYPE_BF16 && (d == 64 || d == 128) && (e == 64 || e == 128);
+}
+
+struct ChunkLayout {
+    size_t prep, S0, dS1, W, X, bytes;
+};
+
+ChunkLayout chunk_ws(long long BH, int T, int d, int e, bool bwd) {
+    const size_t seqs = static_cast<size_t>(BH), chunks = cdiv(T, la2::gdr::kC);
+    ChunkLayout w = {};
+    size_t at = align256(seqs * chunks * sizeof(la2::gdr::ChunkWs));
+    if (bwd) {
+        const size_t pages = align256(seqs * chunks * 2 * d * e * 2);  // two bf16 parts
+        const size_t rows = align256(seqs * T * e * sizeof(float));
+        w.S0 = at;
+        w.dS1 = w.S0 + pages;
+        w.W = w.dS1 + pages;
+        w.X = w.W + rows;
+        at = w.X + rows;
+    }
+    w.bytes = at;
+    return w;
+}
+
+template <int D>
+la2_status chunk_forward(const Args& A, char* ws, cudaStream_t stream) {
+    using namespace la2::gdr;
+    const int chunks = cdiv(A.T, kC);
+    ChunkWs* cw = reinterpret_cast<ChunkWs*>(ws);
+    if (chunks > 0)
+        gdr_prep<D><<<static_cast<unsigned>(A.B) * A.H * chunks, kPrepThreads, sizeof(PrepSmem<D>), stream>>>(A, cw, chunks);
+    gdr_chain<D, false><<<A.B * A.H * (A.e / kWalkCols), kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, Saved{}, chunks);
+    return launched();
+}
+
+template <int D>
+la2_status chunk_backward(const Args& A, char* ws, cudaStream_t stream) {
+    using namespace la2::gdr;
+    const int chunks = cdiv(A.T, kC);
+    const ChunkLayout w = chunk_ws(static_cast<long long>(A.B) * A.H, A.T, A.d, A.e, true);
+    ChunkWs* cw = reinterpret_cast<ChunkWs*>(ws + w.prep);
+    Saved sv;
+    sv.S0 = reinterpret_cast<__nv_bfloat16*>(ws + w.S0);
+    sv.dS1 = reinterpret_cast<__nv_bfloat16*>(ws + w.dS1);
+    sv.W = reinterpret_cast<float*>(ws + w.W);
+    sv.X = reinterpret_cast<float*>(ws + w.X);
+    const int walks = A.B * A.H * (A.e / kWalkCols);
+    if (chunks > 0) {
+        gdr_prep<D><<<static_cast<unsigned>(A.B) * A.H * chunks, kPrepThreads, sizeof(PrepSmem<D>), stream>>>(A, cw, chunks);
+        gdr_chain<D, true><<<walks, kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, sv, chunks);
+    }
+    gdr_chain_rev<D><<<walks, kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, sv, chunks);
+    if (chunks > 0) {
+        const unsigned grid = static_cast<unsigned>(A.B) * A.Hk * chunks;
+        if (A.e == 64) gdr_grad<D, 64><<<grid, 32 * kGradWarps, sizeof(GradTiles<D, 64>), stream>>>(A, cw, sv, chunks);
+        else gdr_grad<D, 128><<<grid, 32 * kGradWarps, sizeof(GradTiles<D, 128>), stream>>>(A, cw, sv, chunks);
+    }
+    return launched();
+}
+
 // Sizes and enums of a sequence call; *empty: nothing to do (no batch entry or
 // no head: there is neither a row nor a state).
 la2_status size_checks(int B, int Hk, int H, int T, int d, int e, la2_dtype dtype, la2_dtype out_dtype,
@@ -118,7 +194,9 @@ size_t la2_gdr_workspace_bytes(int B, int Hk, int H, int T, int d, int e, la2_dt
     bool empty = false;
     if (size_checks(B, Hk, H, T, d, e, dtype, LA2_DTYPE_F32, LA2_LAYOUT_BHTD, &empty) != LA2_OK)
         return static_cast<size_t>(-1);
-    if (empty || !is_bwd || T == 0) return 0;
+    if (empty || T == 0) return 0;
+    if (by_chunks(dtype, d, e)) return chunk_ws(static_cast<long long>(B) * H, T, d, e, is_bwd != 0).bytes;
+    if (!is_bwd) return 0;
     return rec_ws(static_cast<long long>(B) * H, T, d, e).bytes;
 }
 
@@ -145,6 +223,10 @@ la2_status la2_gdr_fwd(const void* q, const void* k, const void* v, const float*
     A.bthd = layout == LA2_LAYOUT_BTHD;
     A.out_bf16 = out_dtype == LA2_DTYPE_BF16;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (by_chunks(dtype, d, e)) {
+        char* ws = static_cast<char*>(workspace);
+        return d == 64 ? chunk_forward<64>(A, ws, s) : chunk_forward<128>(A, ws, s);
+    }
     return dtype == LA2_DTYPE_BF16 ? rec_forward<__nv_bfloat16>(A, s) : rec_forward<float>(A, s);
 }
 
@@ -177,6 +259,7 @@ la2_status la2_gdr_bwd(const void* q, const void* k, const void* v, const float*
     A.out_bf16 = out_dtype == LA2_DTYPE_BF16;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
+    if (by_chunks(dtype, d, e)) return d == 64 ? chunk_backward<64>(A, ws, s) : chunk_backward<128>(A, ws, s);
     return dtype == LA2_DTYPE_BF16 ? rec_backward<__nv_bfloat16>(A, ws, s) : rec_backward<float>(A, ws, s);
 }
 

@@ -1,0 +1,1092 @@
+// gdr_chunk.cuh -- the gated delta rule by chunks of C = 64 rows on the tensor
+// cores, for bf16 inputs with d, e in {64, 128}.
+//
+// With G_t the cumulative gates of a chunk, S0 the state before it and
+// Ah_ts = e^{G_t - G_s} (k_t . k_s) (s < t), P_ts = e^{G_t - G_s} (q_t . k_s) (s <= t),
+// the rows w_t of the chunk solve (I + Ah diag(beta)) W = Z, Z = V - diag(e^G) K S0.
+// With N = (I + Ah diag(beta))^{-1} Ah (strictly lower, one forward substitution
+// per column) both inverses that the two directions need are plain:
+//
+//   (I + Ah diag(beta))^{-1} = I - N diag(beta),  (I + diag(beta) Ah)^{-1} = I - diag(beta) N,
+//
+// without dividing by beta (which may be 0).  So
+//
+//   W = Z - N (beta Z),   U = beta W,
+//   O = diag(e^G) Q S0 + P U,   S1 = e^{G_C} S0 + K^T (e^{G_C - G} U),
+//
+// and backward, with dS1 the gradient of the state after the chunk,
+//
+//   dU = P^T dO + e^{G_C - G} K dS1,   X = dU - N^T (beta dU),   dV = beta X,
+//   dS0 = e^{G_C} dS1 + Q^T (e^G dO) - K^T (beta e^G X).
+//
+// gdr_prep makes N and P of all chunks at once; gdr_chain and gdr_chain_rev walk
+// the chunks of a sequence; gdr_grad, again for all chunks at once, makes
+// dq, dk, dg and dbeta (gdr_rec.cuh has its formulas).
+//
+// Precision: q, k, v, dO enter the products as they are (bf16, exact); every
+// operand that is formed here (states, N, P, W, X, dP, E) is split into a high
+// and a low bf16 part, 2^-17 of the value being lost, and the product of two
+// low parts is dropped.  Sums, states and exponentials are fp32; cumulative
+// gates are fp64 sums kept as two floats.
+//
+// The walks run transposed, S^T [e][d] with 16 rows (value columns of the
+// state, which do not interact) per warp: the accumulator fragment of one
+// product is the A fragment of the next (the 16 x 8 accumulator of two
+// neighbouring tiles is the 16 x 16 operand), so the state and everything formed
+// from it stay in the registers of one warp from the first row to the last,
+// and the warps of a CTA share only the tiles of K, Q, N and P.
+#pragma once
+#include "gdr_common.cuh"
+
+namespace la2 {
+namespace gdr {
+
+constexpr int kC = 64;
+
+// Workspace of one chunk of one value head: N and P, each as a high and a low
+// 64 x 64 bf16 image (row t of 128 bytes, 16-byte pieces permuted by t % 8, as
+// they lie in shared memory), and e^G, e^{G_C - G}, beta.
+struct ChunkWs {
+    unsigned char img[4][kC * kC * 2];  // N hi, N lo, P hi, P lo
+    float eg[kC], rest[kC], beta[kC], g[kC], gl[kC];
+};
+static_assert(sizeof(ChunkWs) % 256 == 0, "chunks stay 256-byte aligned");
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+    const int n = ok ? 16 : 0;  // 0: zeros, src is not read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack(float x, float y) {  // x in the low half
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+    return r;
+}
+__device__ __forceinline__ float low_of(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float high_of(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+
+// (x, y) as a high and a low pair of bf16
+__device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
+    hi = pack(x, y);
+    lo = pack(x - low_of(hi), y - high_of(hi));
+}
+
+// The A fragments of columns 16 kk .. 16 kk + 15 of an accumulator
+__device__ __forceinline__ void frag_split(const float (&c0)[4], const float (&c1)[4], uint32_t (&h)[4],
+                                           uint32_t (&l)[4]) {
+    split(c0[0], c0[1], h[0], l[0]);
+    split(c0[2], c0[3], h[1], l[1]);
+    split(c1[0], c1[1], h[2], l[2]);
+    split(c1[2], c1[3], h[3], l[3]);
+}
+
+// Byte offset of 16-byte piece `p` of row `r` in a tile of rows of `kBytes`
+// bytes, the pieces permuted so that eight rows' equal pieces fall into
+// different banks.
+template <int kBytes>
+__device__ __forceinline__ uint32_t piece(int r, int p) {
+    return static_cast<uint32_t>(r * kBytes + ((p ^ (r & 7)) << 4));
+}
+
+// The four fragment addressings of ldmatrix; rows of kBytes bytes.
+// rows [n][k]: B fragments of n tiles 2 jp, 2 jp + 1 (b[0..1], b[2..3]), k step kk
+template <int kBytes>
+__device__ __forceinline__ void ld_b(uint32_t (&b)[4], uint32_t tile, int jp, int kk, int lane) {
+    const int m = lane >> 3, r = lane & 7;
+    ldsm(b, tile + piece<kBytes>(8 * (2 * jp + (m >> 1)) + r, 2 * kk + (m & 1)));
+}
+// rows [k][n]: the same fragments from the transposed tile
+template <int kBytes>
+__device__ __forceinline__ void ld_bt(uint32_t (&b)[4], uint32_t tile, int jp, int kk, int lane) {
+    const int m = lane >> 3, r = lane & 7;
+    ldsm_t(b, tile + piece<kBytes>(16 * kk + (m & 1) * 8 + r, 2 * jp + (m >> 1)));
+}
+// rows [m][k]: A fragment of rows 16 mi .., k step kk
+template <int kBytes>
+__device__ __forceinline__ void ld_a(uint32_t (&a)[4], uint32_t tile, int mi, int kk, int lane) {
+    const int m = lane >> 3, r = lane & 7;
+    ldsm(a, tile + piece<kBytes>(16 * mi + (m & 1) * 8 + r, 2 * kk + (m >> 1)));
+}
+// rows [k][m]: the same fragment from the transposed tile; as accumulator
+// values: a[0], a[1] tile 2 kk (rows g, g + 8), a[2], a[3] tile 2 kk + 1
+template <int kBytes>
+__device__ __forceinline__ void ld_at(uint32_t (&a)[4], uint32_t tile, int mi, int kk, int lane) {
+    const int m = lane >> 3, r = lane & 7;
+    ldsm_t(a, tile + piece<kBytes>(16 * kk + (m >> 1) * 8 + r, 2 * mi + (m & 1)));
+}
+
+__device__ __forceinline__ void mma2(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[4], const uint32_t (&b)[4]) {
+    mma(c0, a, b[0], b[1]);
+    mma(c1, a, b[2], b[3]);
+}
+
+// Rows t0 .. t0 + 63 (those behind `len` as zeros) of W columns from column c0
+// of a bf16 tensor of `width` columns into a tile of rows of 2 W bytes.
+template <int W, int kThreads>
+__device__ __forceinline__ void load_tile(uint32_t tile, const Args& A, const void* src, int b, int h, int nh,
+                                          int width, int c0, int t0, int len) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(src);
+    constexpr int kPieces = W / 8;
+#pragma unroll
+    for (int x = threadIdx.x; x < kC * kPieces; x += kThreads) {
+        const int r = x / kPieces, c = x % kPieces;
+        const bool ok = t0 + r < len;
+        cp16(tile + piece<2 * W>(r, c), p + (ok ? row_at(A, b, h, nh, t0 + r, width) + c0 + 8 * c : 0), ok);
+    }
+}
+
+template <int kThreads>
+__device__ __forceinline__ void load_bytes(uint32_t dst, const void* src, int bytes) {
+    for (int x = threadIdx.x * 16; x < bytes; x += kThreads * 16)
+        cp16(dst + x, static_cast<const char*>(src) + x, true);
+}
+
+// ------------------------------------------------------------------ gdr_prep
+
+constexpr int kPrepThreads = 128;
+
+template <int D>
+struct PrepSmem {
+    unsigned char k[kC * D * 2], q[kC * D * 2];
+    float a[kC][kC + 1];   // Ah
+    float ab[kC][kC + 4];  // Ah diag(beta): rows read as float4
+    ChunkWs out;
+};
+
+// N and P of one chunk.  Four warps take 16 rows of K K^T and Q K^T each; then a
+// thread takes a column of N:  N_ts = Ah_ts - sum_{s < r < t} Ah_tr beta_r N_rs.
+template <int D>
+__global__ void __launch_bounds__(kPrepThreads)
+gdr_prep(Args A, ChunkWs* ws, int chunks) {
+    extern __shared__ __align__(128) unsigned char prep_raw[];
+    PrepSmem<D>& sm = *reinterpret_cast<PrepSmem<D>*>(prep_raw);
+    const int c = blockIdx.x % chunks, n = blockIdx.x / chunks, b = n / A.H, h = n % A.H;
+    const int len = length_of(A, b), t0 = c * kC;
+    if (t0 >= len) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hk = h / (A.H / A.Hk);
+    const uint32_t kt = smem_addr(sm.k), qt = smem_addr(sm.q);
+    load_tile<D, kPrepThreads>(kt, A, A.k, b, hk, A.Hk, A.d, 0, t0, len);
+    load_tile<D, kPrepThreads>(qt, A, A.q, b, hk, A.Hk, A.d, 0, t0, len);
+    cp_commit();
+    if (warp == 0) {  // gates: two rows per lane, rows behind the end keep everything and write nothing
+        const int t = 2 * lane;
+        double g0 = 0.0, g1 = 0.0;
+        float b0 = 0.f, b1 = 0.f;
+        if (t0 + t < len) {
+            const size_t at = row_at(A, b, h, A.H, t0 + t, 1);
+            g0 = gate_at(A, at);
+            b0 = A.beta[at];
+        }
+        if (t0 + t + 1 < len) {
+            const size_t at = row_at(A, b, h, A.H, t0 + t + 1, 1);
+            g1 = gate_at(A, at);
+            b1 = A.beta[at];
+        }
+        double s = g0 + g1;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, s, m);
+            if (lane >= m) s += y;
+        }
+        const double all = __shfl_sync(0xffffffffu, s, 31), first = s - g1;
+        sm.out.g[t] = static_cast<float>(first);
+        sm.out.g[t + 1] = static_cast<float>(s);
+        sm.out.gl[t] = static_cast<float>(first - sm.out.g[t]);
+        sm.out.gl[t + 1] = static_cast<float>(s - sm.out.g[t + 1]);
+        sm.out.eg[t] = expf(sm.out.g[t]) * (1.f + sm.out.gl[t]);
+        sm.out.eg[t + 1] = expf(sm.out.g[t + 1]) * (1.f + sm.out.gl[t + 1]);
+        sm.out.rest[t] = expf(static_cast<float>(all - first));
+        sm.out.rest[t + 1] = expf(static_cast<float>(all - s));
+        sm.out.beta[t] = b0;
+        sm.out.beta[t + 1] = b1;
+    }
+    cp_wait<0>();
+    __syncthreads();
+    const int g = lane >> 2, i = lane & 3;
+    {
+        float ck[8][4] = {}, cq[8][4] = {};
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t ka[4], qa[4], bb[4];
+            ld_a<2 * D>(ka, kt, warp, kk, lane);
+            ld_a<2 * D>(qa, qt, warp, kk, lane);
+#pragma unroll
+            for (int jp = 0; jp < 4; ++jp) {
+                if (jp <= warp) {
+                    ld_b<2 * D>(bb, kt, jp, kk, lane);
+                    mma2(ck[2 * jp], ck[2 * jp + 1], ka, bb);
+                    mma2(cq[2 * jp], cq[2 * jp + 1], qa, bb);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int t = 16 * warp + g + 8 * half, s = 8 * j + 2 * i;
+                float p[2], a[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const bool low = s + x <= t;
+                    const float M = low ? expf((sm.out.g[t] - sm.out.g[s + x]) + (sm.out.gl[t] - sm.out.gl[s + x])) : 0.f;
+                    p[x] = cq[j][2 * half + x] * M;
+                    a[x] = s + x < t ? ck[j][2 * half + x] * M : 0.f;
+                    sm.a[t][s + x] = a[x];
+                    sm.ab[t][s + x] = a[x] * sm.out.beta[s + x];
+                }
+                uint32_t hi, lo;
+                split(p[0], p[1], hi, lo);
+                const uint32_t at = piece<128>(t, j) + 4 * i;
+                *reinterpret_cast<uint32_t*>(sm.out.img[2] + at) = hi;
+                *reinterpret_cast<uint32_t*>(sm.out.img[3] + at) = lo;
+            }
+        }
+    }
+    __syncthreads();
+    if (tid < kC) {
+        float N[kC];
+        N[0] = 0.f;
+#pragma unroll
+        for (int t = 1; t < kC; ++t) {
+            float x0 = sm.a[t][tid], x1 = 0.f, x2 = 0.f, x3 = 0.f;
+#pragma unroll
+            for (int r = 0; r < t; r += 4) {
+                const float4 y = *reinterpret_cast<const float4*>(&sm.ab[t][r]);
+                x0 = fmaf(-y.x, N[r], x0);
+                if (r + 1 < t) x1 = fmaf(-y.y, N[r + 1], x1);
+                if (r + 2 < t) x2 = fmaf(-y.z, N[r + 2], x2);
+                if (r + 3 < t) x3 = fmaf(-y.w, N[r + 3], x3);
+            }
+            N[t] = tid < t ? (x0 + x1) + (x2 + x3) : 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < kC; ++t) {
+            const __nv_bfloat16 hi = __float2bfloat16_rn(N[t]);
+            const uint32_t at = piece<128>(t, tid >> 3) + 2 * (tid & 7);
+            *reinterpret_cast<__nv_bfloat16*>(sm.out.img[0] + at) = hi;
+            *reinterpret_cast<__nv_bfloat16*>(sm.out.img[1] + at) = __float2bfloat16_rn(N[t] - __bfloat162float(hi));
+        }
+    }
+    __syncthreads();
+    const uint4* from = reinterpret_cast<const uint4*>(&sm.out);
+    uint4* to = reinterpret_cast<uint4*>(ws + static_cast<size_t>(n) * chunks + c);
+    for (int x = tid; x < static_cast<int>(sizeof(ChunkWs) / 16); x += kPrepThreads) to[x] = from[x];
+}
+
+// ----------------------------------------------------------------- gdr_chain
+
+constexpr int kWalkThreads = 128;  // 4 warps of 16 value columns
+constexpr int kWalkCols = 64;
+
+// What the walks leave for gdr_grad, per chunk: the state before it (forward)
+// and the gradient of the state after it (backward), as S^T [e][d] in a high and
+// a low image; the rows w and x as fp32 [B*H][T][e].
+struct Saved {
+    __nv_bfloat16 *S0, *dS1;  // [B*H][chunks][2][e][d]
+    float *W, *X;
+};
+
+template <int D>
+__device__ __forceinline__ void save_state(const float (&S)[D / 8][4], __nv_bfloat16* to, int e, int row, int lane) {
+    const int i = lane & 3;
+    uint32_t* hi = reinterpret_cast<uint32_t*>(to);
+    uint32_t* lo = hi + static_cast<size_t>(e) * D / 2;
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t h, l;
+            split(S[j][2 * half], S[j][2 * half + 1], h, l);
+            const int at = ((row + 8 * half) * D + 8 * j + 2 * i) / 2;
+            hi[at] = h;
+            lo[at] = l;
+        }
+    }
+}
+
+template <int D>
+struct WalkSmem {  // two CTAs per SM at D = 128
+    unsigned char k[2][kC * D * 2], q[2][kC * D * 2], v[2][kC * kWalkCols * 2];
+    unsigned char np[4][kC * kC * 2];
+    float coef[2][3][kC];  // e^G, e^{G_C - G}, beta
+};
+
+// Rows [t][16 columns of this warp] of an accumulator to global memory
+__device__ __forceinline__ void store_rows(const Args& A, void* out, int bf16, const float (&o)[8][4], int b, int h,
+                                           int t0, int len, int col, unsigned char* stage, int wcol, int lane) {
+    const int g = lane >> 2, i = lane & 3;
+    if (!bf16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int t = t0 + 8 * j + 2 * i + x;
+                if (t < len) {
+                    float* p = static_cast<float*>(out) + row_at(A, b, h, A.H, t, A.e) + col;
+                    p[g] = o[j][x];
+                    p[g + 8] = o[j][2 + x];
+                }
+            }
+        return;
+    }
+    // through this warp's own columns of a [64][64] tile that it has read out
+    __syncwarp();
+    const uint32_t base = smem_addr(stage);
+#pragma unroll
+    for (int jp = 0; jp < 4; ++jp) {
+        const int m = lane >> 3, r = lane & 7;
+        const uint32_t a = base + piece<128>(8 * (2 * jp + (m >> 1)) + r, wcol / 8 + (m & 1));
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a),
+                     "r"(pack(o[2 * jp][0], o[2 * jp][1])), "r"(pack(o[2 * jp][2], o[2 * jp][3])),
+                     "r"(pack(o[2 * jp + 1][0], o[2 * jp + 1][1])), "r"(pack(o[2 * jp + 1][2], o[2 * jp + 1][3]))
+                     : "memory");
+    }
+    __syncwarp();
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        const int r = 16 * y + (lane >> 1), p = lane & 1;
+        if (t0 + r < len) {
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + piece<128>(r, wcol / 8 + p));
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + row_at(A, b, h, A.H, t0 + r, A.e) + col +
+                                      8 * p) = x;
+        }
+    }
+}
+
+// The state of 16 value columns from memory [d][e] (or zero) and back
+template <int D>
+__device__ __forceinline__ void state_in(float (&S)[D / 8][4], const float* from, int e, int col, int lane) {
+    const int g = lane >> 2, i = lane & 3;
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            S[j][x] = from ? from[static_cast<size_t>(8 * j + 2 * i + (x & 1)) * e + col + g + 8 * (x >> 1)] : 0.f;
+}
+template <int D>
+__device__ __forceinline__ void state_out(const float (&S)[D / 8][4], float* to, int e, int col, int lane) {
+    const int g = lane >> 2, i = lane & 3;
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            to[static_cast<size_t>(8 * j + 2 * i + (x & 1)) * e + col + g + 8 * (x >> 1)] = S[j][x];
+}
+
+// Forward walk over the chunks of one sequence, 64 value columns per CTA.
+// kSave: no output; states and rows w for the backward.
+template <int D, bool kSave>
+__global__ void __launch_bounds__(kWalkThreads, 2)
+gdr_chain(Args A, const ChunkWs* ws, Saved out, int chunks) {
+    extern __shared__ __align__(128) unsigned char walk_raw[];
+    WalkSmem<D>& sm = *reinterpret_cast<WalkSmem<D>*>(walk_raw);
+    const int slices = A.e / kWalkCols;
+    const int n = blockIdx.x / slices, b = n / A.H, h = n % A.H, hk = h / (A.H / A.Hk);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, i = lane & 3;
+    const int cta0 = blockIdx.x % slices * kWalkCols, wcol = 16 * warp, col = cta0 + wcol;
+    const int len = length_of(A, b), nc = (len + kC - 1) / kC;
+    const size_t page = static_cast<size_t>(A.d) * A.e;
+    const ChunkWs* cw = ws + static_cast<size_t>(n) * chunks;
+    float S[D / 8][4];
+    state_in<D>(S, A.init ? A.init + n * page : nullptr, A.e, col, lane);
+
+    const auto load_rows = [&](int c) {
+        const int s = c & 1;
+        load_tile<D, kWalkThreads>(smem_addr(sm.k[s]), A, A.k, b, hk, A.Hk, D, 0, c * kC, len);
+        if (!kSave) load_tile<D, kWalkThreads>(smem_addr(sm.q[s]), A, A.q, b, hk, A.Hk, D, 0, c * kC, len);
+        load_tile<kWalkCols, kWalkThreads>(smem_addr(sm.v[s]), A, A.v, b, h, A.H, A.e, cta0, c * kC, len);
+        load_bytes<kWalkThreads>(smem_addr(sm.coef[s]), cw[c].eg, 3 * kC * 4);
+        cp_commit();
+    };
+    const auto load_mats = [&](int c) {
+        load_bytes<kWalkThreads>(smem_addr(sm.np), cw[c].img, (kSave ? 2 : 4) * kC * kC * 2);
+        cp_commit();
+    };
+    if (nc > 0) {
+        load_rows(0);
+        load_mats(0);
+    }
+    for (int c = 0; c < nc; ++c) {
+        const int s = c & 1;
+        if (c + 1 < nc) load_rows(c + 1);
+        else cp_commit();
+        cp_wait<2>();
+        __syncthreads();
+        const uint32_t kt = smem_addr(sm.k[s]), qt = smem_addr(sm.q[s]), vt = smem_addr(sm.v[s]);
+        const float *eg = sm.coef[s][0], *rest = sm.coef[s][1], *beta = sm.coef[s][2];
+        float z[8][4] = {}, o[8][4] = {};
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t ah[4], al[4], bb[4];
+            frag_split(S[2 * kk], S[2 * kk + 1], ah, al);
+#pragma unroll
+            for (int jp = 0; jp < 4; ++jp) {
+                ld_b<2 * D>(bb, kt, jp, kk, lane);
+                mma2(z[2 * jp], z[2 * jp + 1], ah, bb);
+                mma2(z[2 * jp], z[2 * jp + 1], al, bb);
+                if (!kSave) {
+                    ld_b<2 * D>(bb, qt, jp, kk, lane);
+                    mma2(o[2 * jp], o[2 * jp + 1], ah, bb);
+                    mma2(o[2 * jp], o[2 * jp + 1], al, bb);
+                }
+            }
+        }
+        if (kSave) save_state<D>(S, out.S0 + (static_cast<size_t>(n) * chunks + c) * 2 * page, A.e, col + g, lane);
+        // Z = V - e^G (K S0), then -beta Z as the operand of N
+        uint32_t fh[4][4], fl[4][4];
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            uint32_t vv[4];
+            ld_at<128>(vv, vt, warp, kk, lane);
+            float y[2][4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int j = 2 * kk + x;
+                const float2 e2 = *reinterpret_cast<const float2*>(eg + 8 * j + 2 * i);
+                const float2 b2 = *reinterpret_cast<const float2*>(beta + 8 * j + 2 * i);
+                z[j][0] = fmaf(-e2.x, z[j][0], low_of(vv[2 * x]));
+                z[j][1] = fmaf(-e2.y, z[j][1], high_of(vv[2 * x]));
+                z[j][2] = fmaf(-e2.x, z[j][2], low_of(vv[2 * x + 1]));
+                z[j][3] = fmaf(-e2.y, z[j][3], high_of(vv[2 * x + 1]));
+                y[x][0] = -b2.x * z[j][0];
+                y[x][1] = -b2.y * z[j][1];
+                y[x][2] = -b2.x * z[j][2];
+                y[x][3] = -b2.y * z[j][3];
+                if (!kSave) {
+                    o[j][0] *= e2.x;
+                    o[j][1] *= e2.y;
+                    o[j][2] *= e2.x;
+                    o[j][3] *= e2.y;
+                }
+            }
+            frag_split(y[0], y[1], fh[kk], fl[kk]);
+        }
+        cp_wait<1>();
+        __syncthreads();
+        const uint32_t nh = smem_addr(sm.np[0]), nl = smem_addr(sm.np[1]);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+            for (int jp = kk; jp < 4; ++jp) {
+                uint32_t bb[4];
+                ld_b<128>(bb, nh, jp, kk, lane);
+                mma2(z[2 * jp], z[2 * jp + 1], fh[kk], bb);
+                mma2(z[2 * jp], z[2 * jp + 1], fl[kk], bb);
+                ld_b<128>(bb, nl, jp, kk, lane);
+                mma2(z[2 * jp], z[2 * jp + 1], fh[kk], bb);
+            }
+        }
+        if (kSave) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int t = c * kC + 8 * j + 2 * i + x;
+                    if (t < len) {
+                        float* p = out.W + (static_cast<size_t>(n) * A.T + t) * A.e + col;
+                        p[g] = z[j][x];
+                        p[g + 8] = z[j][2 + x];
+                    }
+                }
+        }
+        // U = beta W
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 b2 = *reinterpret_cast<const float2*>(beta + 8 * j + 2 * i);
+            z[j][0] *= b2.x;
+            z[j][1] *= b2.y;
+            z[j][2] *= b2.x;
+            z[j][3] *= b2.y;
+        }
+        if (!kSave) {
+            const uint32_t ph = smem_addr(sm.np[2]), pl = smem_addr(sm.np[3]);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                uint32_t uh[4], ul[4];
+                frag_split(z[2 * kk], z[2 * kk + 1], uh, ul);
+#pragma unroll
+                for (int jp = kk; jp < 4; ++jp) {
+                    uint32_t bb[4];
+                    ld_b<128>(bb, ph, jp, kk, lane);
+                    mma2(o[2 * jp], o[2 * jp + 1], uh, bb);
+                    mma2(o[2 * jp], o[2 * jp + 1], ul, bb);
+                    ld_b<128>(bb, pl, jp, kk, lane);
+                    mma2(o[2 * jp], o[2 * jp + 1], uh, bb);
+                }
+            }
+            store_rows(A, A.o, A.out_bf16, o, b, h, c * kC, len, col, sm.v[s], wcol, lane);
+        }
+        __syncthreads();
+        if (c + 1 < nc) load_mats(c + 1);
+        else cp_commit();
+        const float ec = eg[kC - 1];
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) S[j][x] *= ec;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            float y[2][4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int j = 2 * kk + x;
+                const float2 r2 = *reinterpret_cast<const float2*>(rest + 8 * j + 2 * i);
+                y[x][0] = r2.x * z[j][0];
+                y[x][1] = r2.y * z[j][1];
+                y[x][2] = r2.x * z[j][2];
+                y[x][3] = r2.y * z[j][3];
+            }
+            uint32_t uh[4], ul[4];
+            frag_split(y[0], y[1], uh, ul);
+#pragma unroll
+            for (int jp = 0; jp < D / 16; ++jp) {
+                uint32_t bb[4];
+                ld_bt<2 * D>(bb, kt, jp, kk, lane);
+                mma2(S[2 * jp], S[2 * jp + 1], uh, bb);
+                mma2(S[2 * jp], S[2 * jp + 1], ul, bb);
+            }
+        }
+        __syncthreads();
+    }
+    if (!kSave && A.fin) state_out<D>(S, A.fin + n * page, A.e, col, lane);
+}
+
+// Backward walk: the gradient of the state from the last chunk to the first.
+template <int D>
+__global__ void __launch_bounds__(kWalkThreads, 2)
+gdr_chain_rev(Args A, const ChunkWs* ws, Saved out, int chunks) {
+    extern __shared__ __align__(128) unsigned char walk_raw[];
+    WalkSmem<D>& sm = *reinterpret_cast<WalkSmem<D>*>(walk_raw);
+    const int slices = A.e / kWalkCols;
+    const int n = blockIdx.x / slices, b = n / A.H, h = n % A.H, hk = h / (A.H / A.Hk);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, i = lane & 3;
+    const int cta0 = blockIdx.x % slices * kWalkCols, wcol = 16 * warp, col = cta0 + wcol;
+    const int len = length_of(A, b), nc = (len + kC - 1) / kC;
+    const size_t page = static_cast<size_t>(A.d) * A.e;
+    const ChunkWs* cw = ws + static_cast<size_t>(n) * chunks;
+    float S[D / 8][4];  // the gradient
+    state_in<D>(S, A.dfinal ? A.dfinal + n * page : nullptr, A.e, col, lane);
+
+    const auto load_rows = [&](int c) {
+        const int s = c & 1;
+        load_tile<D, kWalkThreads>(smem_addr(sm.k[s]), A, A.k, b, hk, A.Hk, D, 0, c * kC, len);
+        load_tile<D, kWalkThreads>(smem_addr(sm.q[s]), A, A.q, b, hk, A.Hk, D, 0, c * kC, len);
+        load_tile<kWalkCols, kWalkThreads>(smem_addr(sm.v[s]), A, A.dout, b, h, A.H, A.e, cta0, c * kC, len);
+        load_bytes<kWalkThreads>(smem_addr(sm.coef[s]), cw[c].eg, 3 * kC * 4);
+        cp_commit();
+    };
+    const auto load_mats = [&](int c) {
+        load_bytes<kWalkThreads>(smem_addr(sm.np), cw[c].img, 4 * kC * kC * 2);
+        cp_commit();
+    };
+    if (nc > 0) {
+        load_rows(nc - 1);
+        load_mats(nc - 1);
+    }
+    for (int c = nc - 1; c >= 0; --c) {
+        const int s = c & 1;
+        if (c > 0) load_rows(c - 1);
+        else cp_commit();
+        cp_wait<2>();
+        __syncthreads();
+        const uint32_t kt = smem_addr(sm.k[s]), qt = smem_addr(sm.q[s]), vt = smem_addr(sm.v[s]);
+        const float *eg = sm.coef[s][0], *rest = sm.coef[s][1], *beta = sm.coef[s][2];
+        save_state<D>(S, out.dS1 + (static_cast<size_t>(n) * chunks + c) * 2 * page, A.e, col + g, lane);
+        float x[8][4] = {};
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t ah[4], al[4], bb[4];
+            frag_split(S[2 * kk], S[2 * kk + 1], ah, al);
+#pragma unroll
+            for (int jp = 0; jp < 4; ++jp) {
+                ld_b<2 * D>(bb, kt, jp, kk, lane);
+                mma2(x[2 * jp], x[2 * jp + 1], ah, bb);
+                mma2(x[2 * jp], x[2 * jp + 1], al, bb);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 r2 = *reinterpret_cast<const float2*>(rest + 8 * j + 2 * i);
+            x[j][0] *= r2.x;
+            x[j][1] *= r2.y;
+            x[j][2] *= r2.x;
+            x[j][3] *= r2.y;
+        }
+        cp_wait<1>();
+        __syncthreads();
+        const uint32_t nh = smem_addr(sm.np[0]), nl = smem_addr(sm.np[1]);
+        const uint32_t ph = smem_addr(sm.np[2]), pl = smem_addr(sm.np[3]);
+        // + P^T dO
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            uint32_t da[4];
+            ld_at<128>(da, vt, warp, kk, lane);
+#pragma unroll
+            for (int jp = 0; jp <= kk; ++jp) {
+                uint32_t bb[4];
+                ld_bt<128>(bb, ph, jp, kk, lane);
+                mma2(x[2 * jp], x[2 * jp + 1], da, bb);
+                ld_bt<128>(bb, pl, jp, kk, lane);
+                mma2(x[2 * jp], x[2 * jp + 1], da, bb);
+            }
+        }
+        // X = dU - N^T (beta dU)
+        {
+            uint32_t fh[4][4], fl[4][4];
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                float y[2][4];
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int j = 2 * kk + w;
+                    const float2 b2 = *reinterpret_cast<const float2*>(beta + 8 * j + 2 * i);
+                    y[w][0] = -b2.x * x[j][0];
+                    y[w][1] = -b2.y * x[j][1];
+                    y[w][2] = -b2.x * x[j][2];
+                    y[w][3] = -b2.y * x[j][3];
+                }
+                frag_split(y[0], y[1], fh[kk], fl[kk]);
+            }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+                for (int jp = 0; jp <= kk; ++jp) {
+                    uint32_t bb[4];
+                    ld_bt<128>(bb, nh, jp, kk, lane);
+                    mma2(x[2 * jp], x[2 * jp + 1], fh[kk], bb);
+                    mma2(x[2 * jp], x[2 * jp + 1], fl[kk], bb);
+                    ld_bt<128>(bb, nl, jp, kk, lane);
+                    mma2(x[2 * jp], x[2 * jp + 1], fh[kk], bb);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int t = c * kC + 8 * j + 2 * i + w;
+                if (t < len) {
+                    float* p = out.X + (static_cast<size_t>(n) * A.T + t) * A.e + col;
+                    p[g] = x[j][w];
+                    p[g + 8] = x[j][2 + w];
+                }
+            }
+        // dS = e^{G_C} dS + Q^T (e^G dO) - K^T (beta e^G X)
+        const float ec = eg[kC - 1];
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) S[j][w] *= ec;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 b2 = *reinterpret_cast<const float2*>(beta + 8 * j + 2 * i);
+            x[j][0] *= b2.x;
+            x[j][1] *= b2.y;
+            x[j][2] *= b2.x;
+            x[j][3] *= b2.y;
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            uint32_t da[4], h1[4], l1[4], h2[4], l2[4];
+            ld_at<128>(da, vt, warp, kk, lane);
+            float y[2][4], u[2][4];
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int j = 2 * kk + w;
+                const float2 e2 = *reinterpret_cast<const float2*>(eg + 8 * j + 2 * i);
+                y[w][0] = e2.x * low_of(da[2 * w]);
+                y[w][1] = e2.y * high_of(da[2 * w]);
+                y[w][2] = e2.x * low_of(da[2 * w + 1]);
+                y[w][3] = e2.y * high_of(da[2 * w + 1]);
+                u[w][0] = -e2.x * x[j][0];
+                u[w][1] = -e2.y * x[j][1];
+                u[w][2] = -e2.x * x[j][2];
+                u[w][3] = -e2.y * x[j][3];
+            }
+            frag_split(y[0], y[1], h1, l1);
+            frag_split(u[0], u[1], h2, l2);
+#pragma unroll
+            for (int jp = 0; jp < D / 16; ++jp) {
+                uint32_t bb[4];
+                ld_bt<2 * D>(bb, qt, jp, kk, lane);
+                mma2(S[2 * jp], S[2 * jp + 1], h1, bb);
+                mma2(S[2 * jp], S[2 * jp + 1], l1, bb);
+                ld_bt<2 * D>(bb, kt, jp, kk, lane);
+                mma2(S[2 * jp], S[2 * jp + 1], h2, bb);
+                mma2(S[2 * jp], S[2 * jp + 1], l2, bb);
+            }
+        }
+        // dv = beta X, through this warp's columns of the dO tile, which it has read
+        store_rows(A, A.dv, A.out_bf16, x, b, h, c * kC, len, col, sm.v[s], wcol, lane);
+        __syncthreads();
+        if (c > 0) load_mats(c - 1);
+        else cp_commit();
+    }
+    if (A.dinit) state_out<D>(S, A.dinit + n * page, A.e, col, lane);
+}
+
+// ------------------------------------------------------------------ gdr_grad
+
+constexpr int kGradWarps = 8;
+
+template <int D, int E>
+struct GradTiles {
+    unsigned char q[kC * D * 2], k[kC * D * 2], dout[kC * E * 2];
+    unsigned char u[2][kC * E * 2], x[2][kC * E * 2];
+    unsigned char S[2][E * D * 2];
+    unsigned char dp[2][kC * kC * 2], E_[2][kC * kC * 2];
+    float coef[5][kC];  // e^G, e^{G_C - G}, beta, G, its low part
+    float db[kC], xr[kC], part[2][kC], dG[kC], red[2 * kGradWarps];
+};
+
+// dq, dk, dg, dbeta of one chunk of key head hk, over the value heads that share
+// it in their order (formulas: gdr_rec.cuh).  Warp (rt, hf) makes rows
+// 16 rt .. 16 rt + 15 and one half of the columns of every product.
+template <int D, int E>
+__global__ void __launch_bounds__(32 * kGradWarps, 1)
+gdr_grad(Args A, const ChunkWs* ws, Saved in, int chunks) {
+    extern __shared__ __align__(128) unsigned char grad_raw[];
+    GradTiles<D, E>& sm = *reinterpret_cast<GradTiles<D, E>*>(grad_raw);
+    constexpr int kThreads = 32 * kGradWarps, kT = D / 16;  // kT: 8-column tiles of a warp's half of d
+    const int c = blockIdx.x % chunks, hk = blockIdx.x / chunks % A.Hk, b = blockIdx.x / chunks / A.Hk;
+    const int len = length_of(A, b), t0 = c * kC;
+    if (t0 >= len) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rt = warp & 3, hf = warp >> 2;
+    const int g = lane >> 2, i = lane & 3, rep = A.H / A.Hk;
+    const uint32_t qt = smem_addr(sm.q), kt = smem_addr(sm.k), dt = smem_addr(sm.dout);
+    const uint32_t uh = smem_addr(sm.u[0]), ul = smem_addr(sm.u[1]), xh = smem_addr(sm.x[0]), xl = smem_addr(sm.x[1]);
+    const uint32_t sh = smem_addr(sm.S[0]), sl = smem_addr(sm.S[1]);
+    load_tile<D, kThreads>(qt, A, A.q, b, hk, A.Hk, D, 0, t0, len);
+    load_tile<D, kThreads>(kt, A, A.k, b, hk, A.Hk, D, 0, t0, len);
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(A.v);
+    float accq[kT][4] = {}, acck[kT][4] = {};
+    const auto load_state = [&](const __nv_bfloat16* from) {  // [2][E][D]
+        constexpr int kPieces = D / 8;
+        for (int y = tid; y < 2 * E * kPieces; y += kThreads) {
+            const int r = y / kPieces, p = y % kPieces, part = r / E;
+            cp16((part ? sl : sh) + piece<2 * D>(r % E, p), from + static_cast<size_t>(r) * D + 8 * p, true);
+        }
+        cp_commit();
+    };
+    for (int hh = 0; hh < rep; ++hh) {
+        const int h = hk * rep + hh;
+        const size_t seq = static_cast<size_t>(b) * A.H + h, cn = seq * chunks + c;
+        const size_t page = static_cast<size_t>(D) * E;
+        __syncthreads();  // the tiles of the head before are read out
+        load_tile<E, kThreads>(dt, A, A.dout, b, h, A.H, E, 0, t0, len);
+        load_bytes<kThreads>(smem_addr(sm.coef), ws[cn].eg, 5 * kC * 4);
+        load_state(in.S0 + cn * 2 * page);
+        // rows of w, x, v: u and x as two parts, dbeta and the row sums of x (w - v)
+        for (int t = warp; t < kC; t += kGradWarps) {
+            constexpr int kPer = E / 32;
+            float db = 0.f, xr = 0.f;
+            const float bt = ws[cn].beta[t];
+            float w[kPer], x[kPer];
+#pragma unroll
+            for (int y = 0; y < kPer; ++y) w[y] = x[y] = 0.f;
+            if (t0 + t < len) {
+                const size_t at = (seq * A.T + t0 + t) * E + lane * kPer;
+                const size_t io = row_at(A, b, h, A.H, t0 + t, E) + lane * kPer;
+#pragma unroll
+                for (int y = 0; y < kPer; ++y) {
+                    w[y] = in.W[at + y];
+                    x[y] = in.X[at + y];
+                    db = fmaf(x[y], w[y], db);
+                    xr = fmaf(x[y], w[y] - __bfloat162float(v[io + y]), xr);
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < kPer; y += 2) {
+                const int j = lane * kPer + y;
+                const uint32_t at = piece<2 * E>(t, j >> 3) + 2 * (j & 7);
+                uint32_t hi, lo;
+                split(bt * w[y], bt * w[y + 1], hi, lo);
+                *reinterpret_cast<uint32_t*>(sm.u[0] + at) = hi;
+                *reinterpret_cast<uint32_t*>(sm.u[1] + at) = lo;
+                split(x[y], x[y + 1], hi, lo);
+                *reinterpret_cast<uint32_t*>(sm.x[0] + at) = hi;
+                *reinterpret_cast<uint32_t*>(sm.x[1] + at) = lo;
+            }
+#pragma unroll
+            for (int m = 16; m; m >>= 1) {
+                db += __shfl_xor_sync(0xffffffffu, db, m);
+                xr += __shfl_xor_sync(0xffffffffu, xr, m);
+            }
+            if (lane == 0) {
+                sm.db[t] = db;
+                sm.xr[t] = bt * xr;
+            }
+        }
+        cp_wait<0>();
+        __syncthreads();
+        const float *eg = sm.coef[0], *rest = sm.coef[1], *beta = sm.coef[2], *G = sm.coef[3], *Gl = sm.coef[4];
+        // dP and E: rows of this warp, 32 columns
+        {
+            float p[4][4] = {}, x[4][4] = {};
+            if (2 * hf <= rt) {  // else all above the diagonal
+#pragma unroll
+                for (int kk = 0; kk < E / 16; ++kk) {
+                    uint32_t da[4], xa[4], xb[4], bh[4], bl[4];
+                    ld_a<2 * E>(da, dt, rt, kk, lane);
+                    ld_a<2 * E>(xa, xh, rt, kk, lane);
+                    ld_a<2 * E>(xb, xl, rt, kk, lane);
+#pragma unroll
+                    for (int jp = 0; jp < 2; ++jp) {
+                        if (2 * hf + jp > rt) continue;
+                        ld_b<2 * E>(bh, uh, 2 * hf + jp, kk, lane);
+                        ld_b<2 * E>(bl, ul, 2 * hf + jp, kk, lane);
+                        mma2(p[2 * jp], p[2 * jp + 1], da, bh);
+                        mma2(p[2 * jp], p[2 * jp + 1], da, bl);
+                        mma2(x[2 * jp], x[2 * jp + 1], xa, bh);
+                        mma2(x[2 * jp], x[2 * jp + 1], xb, bh);
+                        mma2(x[2 * jp], x[2 * jp + 1], xa, bl);
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int t = 16 * rt + g + 8 * half, s = 32 * hf + 8 * j + 2 * i;
+                    float pp[2], ee[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float M = s + y <= t ? expf((G[t] - G[s + y]) + (Gl[t] - Gl[s + y])) : 0.f;
+                        pp[y] = p[j][2 * half + y] * M;
+                        ee[y] = s + y < t ? -x[j][2 * half + y] * M * beta[t] : 0.f;
+                    }
+                    const uint32_t at = piece<128>(t, 4 * hf + j) + 4 * i;
+                    uint32_t hi, lo;
+                    split(pp[0], pp[1], hi, lo);
+                    *reinterpret_cast<uint32_t*>(sm.dp[0] + at) = hi;
+                    *reinterpret_cast<uint32_t*>(sm.dp[1] + at) = lo;
+                    split(ee[0], ee[1], hi, lo);
+                    *reinterpret_cast<uint32_t*>(sm.E_[0] + at) = hi;
+                    *reinterpret_cast<uint32_t*>(sm.E_[1] + at) = lo;
+                }
+        }
+        float fq[kT][4] = {}, row[kT][4] = {}, col[kT][4] = {};
+        // dO S0^T and X S0^T
+#pragma unroll 2
+        for (int kk = 0; kk < E / 16; ++kk) {
+            uint32_t da[4], xa[4], xb[4], bh[4], bl[4];
+            ld_a<2 * E>(da, dt, rt, kk, lane);
+            ld_a<2 * E>(xa, xh, rt, kk, lane);
+            ld_a<2 * E>(xb, xl, rt, kk, lane);
+#pragma unroll
+            for (int jp = 0; jp < kT / 2; ++jp) {
+                ld_bt<2 * D>(bh, sh, hf * (kT / 2) + jp, kk, lane);
+                ld_bt<2 * D>(bl, sl, hf * (kT / 2) + jp, kk, lane);
+                mma2(fq[2 * jp], fq[2 * jp + 1], da, bh);
+                mma2(fq[2 * jp], fq[2 * jp + 1], da, bl);
+                mma2(row[2 * jp], row[2 * jp + 1], xa, bh);
+                mma2(row[2 * jp], row[2 * jp + 1], xb, bh);
+                mma2(row[2 * jp], row[2 * jp + 1], xa, bl);
+            }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int t = 16 * rt + g + 8 * half;
+            const float e1 = eg[t], e2 = -beta[t] * eg[t];
+#pragma unroll
+            for (int j = 0; j < kT; ++j)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    fq[j][2 * half + y] *= e1;
+                    row[j][2 * half + y] *= e2;
+                }
+        }
+        __syncthreads();  // dP, E are complete; S0 is read out
+        // <dS1, S0> from memory (S0) and what replaces it
+        load_state(in.dS1 + cn * 2 * page);
+        const uint32_t ph = smem_addr(sm.dp[0]), pl = smem_addr(sm.dp[1]);
+        const uint32_t eh = smem_addr(sm.E_[0]), el = smem_addr(sm.E_[1]);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            uint32_t a0[4], a1[4], a2[4], a3[4], bb[4];
+            if (kk <= rt) {  // rows t, columns s <= t
+                ld_a<128>(a0, ph, rt, kk, lane);
+                ld_a<128>(a1, pl, rt, kk, lane);
+                ld_a<128>(a2, eh, rt, kk, lane);
+                ld_a<128>(a3, el, rt, kk, lane);
+#pragma unroll
+                for (int jp = 0; jp < kT / 2; ++jp) {
+                    ld_bt<2 * D>(bb, kt, hf * (kT / 2) + jp, kk, lane);
+                    mma2(fq[2 * jp], fq[2 * jp + 1], a0, bb);
+                    mma2(fq[2 * jp], fq[2 * jp + 1], a1, bb);
+                    mma2(row[2 * jp], row[2 * jp + 1], a2, bb);
+                    mma2(row[2 * jp], row[2 * jp + 1], a3, bb);
+                }
+            }
+            if (kk >= rt) {  // columns s as rows, t >= s
+                ld_at<128>(a0, ph, rt, kk, lane);
+                ld_at<128>(a1, pl, rt, kk, lane);
+                ld_at<128>(a2, eh, rt, kk, lane);
+                ld_at<128>(a3, el, rt, kk, lane);
+#pragma unroll
+                for (int jp = 0; jp < kT / 2; ++jp) {
+                    ld_bt<2 * D>(bb, qt, hf * (kT / 2) + jp, kk, lane);
+                    mma2(col[2 * jp], col[2 * jp + 1], a0, bb);
+                    mma2(col[2 * jp], col[2 * jp + 1], a1, bb);
+                    ld_bt<2 * D>(bb, kt, hf * (kT / 2) + jp, kk, lane);
+                    mma2(col[2 * jp], col[2 * jp + 1], a2, bb);
+                    mma2(col[2 * jp], col[2 * jp + 1], a3, bb);
+                }
+            }
+        }
+        // q . dq of this half of d, then dq and dk take what is done
+        float qd[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < kT; ++j)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int t = 16 * rt + g + 8 * half;
+                const uint32_t qq = *reinterpret_cast<const uint32_t*>(sm.q + piece<2 * D>(t, hf * kT + j) + 4 * i);
+                qd[half] = fmaf(low_of(qq), fq[j][2 * half], fmaf(high_of(qq), fq[j][2 * half + 1], qd[half]));
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    accq[j][2 * half + y] += fq[j][2 * half + y];
+                    acck[j][2 * half + y] += row[j][2 * half + y];
+                }
+            }
+        cp_wait<0>();
+        __syncthreads();
+        float dot = 0.f;
+        {
+            const uint32_t* s0 = reinterpret_cast<const uint32_t*>(in.S0 + cn * 2 * page);
+            constexpr int kWords = D / 2;
+            for (int y = tid; y < E * kWords; y += kThreads) {
+                const int r = y / kWords, x = y % kWords;
+                const uint32_t at = piece<2 * D>(r, x >> 2) + 4 * (x & 3);
+                const uint32_t dh = *reinterpret_cast<const uint32_t*>(sm.S[0] + at);
+                const uint32_t dl = *reinterpret_cast<const uint32_t*>(sm.S[1] + at);
+                const uint32_t fh = s0[y], fl = s0[y + E * kWords];
+                dot = fmaf(low_of(dh) + low_of(dl), low_of(fh) + low_of(fl), dot);
+                dot = fmaf(high_of(dh) + high_of(dl), high_of(fh) + high_of(fl), dot);
+            }
+        }
+        // U dS1^T
+        float cs[kT][4] = {};
+#pragma unroll 2
+        for (int kk = 0; kk < E / 16; ++kk) {
+            uint32_t ua[4], ub[4], bh[4], bl[4];
+            ld_a<2 * E>(ua, uh, rt, kk, lane);
+            ld_a<2 * E>(ub, ul, rt, kk, lane);
+#pragma unroll
+            for (int jp = 0; jp < kT / 2; ++jp) {
+                ld_bt<2 * D>(bh, sh, hf * (kT / 2) + jp, kk, lane);
+                ld_bt<2 * D>(bl, sl, hf * (kT / 2) + jp, kk, lane);
+                mma2(cs[2 * jp], cs[2 * jp + 1], ua, bh);
+                mma2(cs[2 * jp], cs[2 * jp + 1], ub, bh);
+                mma2(cs[2 * jp], cs[2 * jp + 1], ua, bl);
+            }
+        }
+        float gc = 0.f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int t = 16 * rt + g + 8 * half;
+            const float r = rest[t];
+            float kd = 0.f;
+#pragma unroll
+            for (int j = 0; j < kT; ++j) {
+                const uint32_t kw = *reinterpret_cast<const uint32_t*>(sm.k + piece<2 * D>(t, hf * kT + j) + 4 * i);
+                const float k0 = low_of(kw), k1 = high_of(kw);
+                const float c0 = r * cs[j][2 * half], c1 = r * cs[j][2 * half + 1];
+                gc = fmaf(k0, c0, fmaf(k1, c1, gc));
+                const float d0 = c0 + col[j][2 * half], d1 = c1 + col[j][2 * half + 1];
+                kd = fmaf(k0, d0, fmaf(k1, d1, kd));
+                acck[j][2 * half] += d0;
+                acck[j][2 * half + 1] += d1;
+            }
+            float y = qd[half] - kd;
+            y += __shfl_xor_sync(0xffffffffu, y, 1);
+            y += __shfl_xor_sync(0xffffffffu, y, 2);
+            if (i == 0) sm.part[hf][t] = y;
+        }
+#pragma unroll
+        for (int m = 16; m; m >>= 1) {
+            gc += __shfl_xor_sync(0xffffffffu, gc, m);
+            dot += __shfl_xor_sync(0xffffffffu, dot, m);
+        }
+        if (lane == 0) {
+            sm.red[warp] = gc;
+            sm.red[kGradWarps + warp] = dot;
+        }
+        __syncthreads();
+        if (warp == 0) {  // sums of dL/dG from each row to the chunk's end: two rows per lane
+            const int t = 2 * lane;
+            float y0 = sm.part[0][t] + sm.part[1][t] + sm.xr[t];
+            float y1 = sm.part[0][t + 1] + sm.part[1][t + 1] + sm.xr[t + 1];
+            if (lane == 31) {
+                float d1 = 0.f, d2 = 0.f;
+                for (int w = 0; w < kGradWarps; ++w) {
+                    d1 += sm.red[w];
+                    d2 += sm.red[kGradWarps + w];
+                }
+                y1 += fmaf(eg[kC - 1], d2, d1);
+            }
+            float s = y0 + y1;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const float z = __shfl_down_sync(0xffffffffu, s, m);
+                if (lane + m < 32) s += z;
+            }
+            if (A.dg) {
+                if (t0 + t < len) A.dg[row_at(A, b, h, A.H, t0 + t, 1)] = s;
+                if (t0 + t + 1 < len) A.dg[row_at(A, b, h, A.H, t0 + t + 1, 1)] = s - y0;
+            }
+        } else if (warp < 3) {
+            const int t = tid - 32;
+            if (t0 + t < len) A.dbeta[row_at(A, b, h, A.H, t0 + t, 1)] = sm.db[t];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kT; ++j)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int t = t0 + 16 * rt + g + 8 * half;
+            if (t < len) {
+                const size_t at = row_at(A, b, hk, A.Hk, t, D) + 8 * (hf * kT + j) + 2 * i;
+                if (A.out_bf16) {
+                    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(A.dq) + at) =
+                        pack(accq[j][2 * half], accq[j][2 * half + 1]);
+                    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(A.dk) + at) =
+                        pack(acck[j][2 * half], acck[j][2 * half + 1]);
+                } else {
+                    *reinterpret_cast<float2*>(static_cast<float*>(A.dq) + at) =
+                        make_float2(accq[j][2 * half], accq[j][2 * half + 1]);
+                    *reinterpret_cast<float2*>(static_cast<float*>(A.dk) + at) =
+                        make_float2(acck[j][2 * half], acck[j][2 * half + 1]);
+                }
+            }
+        }
+}
+
+}  // namespace gdr
+}  // namespace la2
