@@ -2,6 +2,7 @@
 // (la2_gdr_*, la2_state_copy in include/la2.h): argument checks, workspace
 // layout and launches.  The kernels are in gdr_chunk.cuh (bf16, d and e 64 or
 // 128), gdr_rec.cuh (everything else) and state_pool.cuh.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -11,12 +12,49 @@
 #include "gdr_chunk.cuh"
 #include "gdr_common.cuh"
 #include "gdr_rec.cuh"
+#include "gdr_walk_sm100.cuh"
 #include "la2.h"
 #include "state_pool.cuh"
+
+namespace la2 {
+int* status_word();  // la2_api.cu
+}
 
 namespace {
 
 using la2::gdr::Args;
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// 4-D map over bf16 rows [B, heads, T, width] (or [B, T, heads, width]): boxes of
+// 64 columns x 64 rows of one (b, head), 128-byte swizzle, rows past T zero.
+bool row_map(CUtensorMap* m, const void* ptr, int B, int heads, int T, int width, int bthd) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t w = width, t = T, h = heads, b = B, rows = la2::gdr::kC;
+    const cuuint64_t dims[4] = {w, bthd ? h : t, bthd ? t : h, b};
+    const cuuint64_t strides[3] = {w * 2, (bthd ? h : t) * w * 2, t * h * w * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(bthd ? 1 : rows), static_cast<cuuint32_t>(bthd ? rows : 1), 1};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 constexpr int kMaxDevices = 64;
 
@@ -37,6 +75,9 @@ bool set_chunk_attrs() {
            set(reinterpret_cast<const void*>(gdr_chain<D, false>), sizeof(WalkSmem<D>)) &&
            set(reinterpret_cast<const void*>(gdr_chain<D, true>), sizeof(WalkSmem<D>)) &&
            set(reinterpret_cast<const void*>(gdr_chain_rev<D>), sizeof(WalkSmem<D>)) &&
+           set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kForward>), sizeof(walk::Smem<D>) + 1024) &&
+           set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kSave>), sizeof(walk::Smem<D>) + 1024) &&
+           set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kBackward>), sizeof(walk::Smem<D>) + 1024) &&
            set(reinterpret_cast<const void*>(gdr_grad<D, 64>), sizeof(GradTiles<D, 64>)) &&
            set(reinterpret_cast<const void*>(gdr_grad<D, 128>), sizeof(GradTiles<D, 128>));
 }
@@ -132,6 +173,23 @@ ChunkLayout chunk_ws(long long BH, int T, int d, int e, bool bwd) {
     return w;
 }
 
+// One walk along every sequence: e = 128 on tcgen05 (T = 0 has no rows to map).
+template <int D, int kMode>
+la2_status walk_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::Saved& sv, int chunks, cudaStream_t stream) {
+    using namespace la2::gdr;
+    CUtensorMap mk, mq, mv;
+    if (!row_map(&mk, A.k, A.B, A.Hk, A.T, D, A.bthd) || !row_map(&mq, A.q, A.B, A.Hk, A.T, D, A.bthd) ||
+        !row_map(&mv, kMode == walk::kBackward ? A.dout : A.v, A.B, A.H, A.T, walk::kE, A.bthd))
+        return LA2_ERR_CUDA;
+    int* status = la2::status_word();
+    if (!status) return LA2_ERR_CUDA;
+    walk::gdr_walk<D, kMode><<<A.B * A.H, walk::kThreads, sizeof(walk::Smem<D>) + 1024, stream>>>(
+        A, cw, sv, chunks, mk, mq, mv, status);
+    return LA2_OK;
+}
+
+bool on_tc(const Args& A) { return A.e == la2::gdr::walk::kE && A.T > 0; }
+
 template <int D>
 la2_status chunk_forward(const Args& A, char* ws, cudaStream_t stream) {
     using namespace la2::gdr;
@@ -139,6 +197,10 @@ la2_status chunk_forward(const Args& A, char* ws, cudaStream_t stream) {
     ChunkWs* cw = reinterpret_cast<ChunkWs*>(ws);
     if (chunks > 0)
         gdr_prep<D><<<static_cast<unsigned>(A.B) * A.H * chunks, kPrepThreads, sizeof(PrepSmem<D>), stream>>>(A, cw, chunks);
+    if (on_tc(A)) {
+        const la2_status st = walk_tc<D, walk::kForward>(A, cw, Saved{}, chunks, stream);
+        return st == LA2_OK ? launched() : st;
+    }
     gdr_chain<D, false><<<A.B * A.H * (A.e / kWalkCols), kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, Saved{}, chunks);
     return launched();
 }
@@ -157,9 +219,15 @@ la2_status chunk_backward(const Args& A, char* ws, cudaStream_t stream) {
     const int walks = A.B * A.H * (A.e / kWalkCols);
     if (chunks > 0) {
         gdr_prep<D><<<static_cast<unsigned>(A.B) * A.H * chunks, kPrepThreads, sizeof(PrepSmem<D>), stream>>>(A, cw, chunks);
-        gdr_chain<D, true><<<walks, kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, sv, chunks);
+        if (!on_tc(A)) gdr_chain<D, true><<<walks, kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, sv, chunks);
     }
-    gdr_chain_rev<D><<<walks, kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, sv, chunks);
+    if (on_tc(A)) {
+        la2_status st = walk_tc<D, walk::kSave>(A, cw, sv, chunks, stream);
+        if (st == LA2_OK) st = walk_tc<D, walk::kBackward>(A, cw, sv, chunks, stream);
+        if (st != LA2_OK) return st;
+    } else {
+        gdr_chain_rev<D><<<walks, kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, sv, chunks);
+    }
     if (chunks > 0) {
         const unsigned grid = static_cast<unsigned>(A.B) * A.Hk * chunks;
         if (A.e == 64) gdr_grad<D, 64><<<grid, 32 * kGradWarps, sizeof(GradTiles<D, 64>), stream>>>(A, cw, sv, chunks);

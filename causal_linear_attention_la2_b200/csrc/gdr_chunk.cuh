@@ -833,6 +833,17 @@ gdr_grad(Args A, const ChunkWs* ws, Saved in, int chunks) {
                 *reinterpret_cast<uint32_t*>(sm.x[0] + at) = hi;
                 *reinterpret_cast<uint32_t*>(sm.x[1] + at) = lo;
             }
+            if constexpr (E == 128) {  // dv = beta x (at e = 64 the walk writes it)
+                if (t0 + t < len) {
+                    const size_t io = row_at(A, b, h, A.H, t0 + t, E) + lane * kPer;
+                    if (A.out_bf16)
+                        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.dv) + io) =
+                            make_uint2(pack(bt * x[0], bt * x[1]), pack(bt * x[2], bt * x[3]));
+                    else
+                        *reinterpret_cast<float4*>(static_cast<float*>(A.dv) + io) =
+                            make_float4(bt * x[0], bt * x[1], bt * x[2], bt * x[3]);
+                }
+            }
 #pragma unroll
             for (int m = 16; m; m >>= 1) {
                 db += __shfl_xor_sync(0xffffffffu, db, m);

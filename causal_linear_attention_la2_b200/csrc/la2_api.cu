@@ -594,6 +594,16 @@ la2_status norm_checks(const void* q, const void* k, const void* v, const float*
 
 }  // namespace
 
+// The current device's status word, for the library's other translation unit
+// (null: set-up failed).
+namespace la2 {
+__attribute__((visibility("hidden"))) int* status_word() {
+    int dev = 0;
+    int* status = nullptr;
+    return device_setup(&dev, &status) ? status : nullptr;
+}
+}  // namespace la2
+
 extern "C" {
 
 size_t la2_workspace_bytes(int B, int H, int T, int d, int e, int block, la2_dtype dtype,
