@@ -75,9 +75,9 @@ bool set_chunk_attrs() {
            set(reinterpret_cast<const void*>(gdr_chain<D, false>), sizeof(WalkSmem<D>)) &&
            set(reinterpret_cast<const void*>(gdr_chain<D, true>), sizeof(WalkSmem<D>)) &&
            set(reinterpret_cast<const void*>(gdr_chain_rev<D>), sizeof(WalkSmem<D>)) &&
-           set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kForward>), sizeof(walk::Smem<D>) + 1024) &&
-           set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kSave>), sizeof(walk::Smem<D>) + 1024) &&
-           set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kBackward>), sizeof(walk::Smem<D>) + 1024) &&
+           set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kForward>), sizeof(walk::Smem<D>)) &&
+           set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kSave>), sizeof(walk::Smem<D>)) &&
+           set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kBackward>), sizeof(walk::Smem<D>)) &&
            set(reinterpret_cast<const void*>(gdr_grad<D, 64>), sizeof(GradTiles<D, 64>)) &&
            set(reinterpret_cast<const void*>(gdr_grad<D, 128>), sizeof(GradTiles<D, 128>));
 }
@@ -183,7 +183,7 @@ la2_status walk_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::S
         return LA2_ERR_CUDA;
     int* status = la2::status_word();
     if (!status) return LA2_ERR_CUDA;
-    walk::gdr_walk<D, kMode><<<A.B * A.H, walk::kThreads, sizeof(walk::Smem<D>) + 1024, stream>>>(
+    walk::gdr_walk<D, kMode><<<A.B * A.H, walk::kThreads, sizeof(walk::Smem<D>), stream>>>(
         A, cw, sv, chunks, mk, mq, mv, status);
     return LA2_OK;
 }

@@ -45,11 +45,15 @@ constexpr int kC = 64;
 
 // Workspace of one chunk of one value head: N and P, each as a high and a low
 // 64 x 64 bf16 image (row t of 128 bytes, 16-byte pieces permuted by t % 8, as
-// they lie in shared memory), and e^G, e^{G_C - G}, beta.
+// they lie in shared memory), and the factors of each row: e^G, e^{G_C - G}, beta
+// and what the walks multiply by, G itself as two floats.
 struct ChunkWs {
     unsigned char img[4][kC * kC * 2];  // N hi, N lo, P hi, P lo
-    float eg[kC], rest[kC], beta[kC], g[kC], gl[kC];
+    float eg[kC], rest[kC], beta[kC];
+    float neg_eg[kC], neg_beta[kC], rest_beta[kC], neg_beta_eg[kC];
+    float g[kC], gl[kC], unused[3 * kC];
 };
+constexpr int kCoefs = 7;  // eg .. neg_beta_eg
 static_assert(sizeof(ChunkWs) % 256 == 0, "chunks stay 256-byte aligned");
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -223,6 +227,14 @@ gdr_prep(Args A, ChunkWs* ws, int chunks) {
         sm.out.rest[t + 1] = expf(static_cast<float>(all - s));
         sm.out.beta[t] = b0;
         sm.out.beta[t + 1] = b1;
+#pragma unroll
+        for (int y = t; y < t + 2; ++y) {
+            const float bt = sm.out.beta[y];
+            sm.out.neg_eg[y] = -sm.out.eg[y];
+            sm.out.neg_beta[y] = -bt;
+            sm.out.rest_beta[y] = sm.out.rest[y] * bt;
+            sm.out.neg_beta_eg[y] = -bt * sm.out.eg[y];
+        }
     }
     cp_wait<0>();
     __syncthreads();
@@ -303,10 +315,11 @@ constexpr int kWalkThreads = 128;  // 4 warps of 16 value columns
 constexpr int kWalkCols = 64;
 
 // What the walks leave for gdr_grad, per chunk: the state before it (forward)
-// and the gradient of the state after it (backward), as S^T [e][d] in a high and
-// a low image; the rows w and x as fp32 [B*H][T][e].
+// and the gradient of the state after it (backward), in a high and a low part of
+// d / 8 blocks of [e][8] (one value column's 16 bytes next to the next one's);
+// the rows w and x as fp32 [B*H][T][e].
 struct Saved {
-    __nv_bfloat16 *S0, *dS1;  // [B*H][chunks][2][e][d]
+    __nv_bfloat16 *S0, *dS1;  // [B*H][chunks][2][d / 8][e][8]
     float *W, *X;
 };
 
@@ -321,7 +334,7 @@ __device__ __forceinline__ void save_state(const float (&S)[D / 8][4], __nv_bflo
         for (int half = 0; half < 2; ++half) {
             uint32_t h, l;
             split(S[j][2 * half], S[j][2 * half + 1], h, l);
-            const int at = ((row + 8 * half) * D + 8 * j + 2 * i) / 2;
+            const int at = (j * e + row + 8 * half) * 4 + i;
             hi[at] = h;
             lo[at] = l;
         }
@@ -786,11 +799,11 @@ gdr_grad(Args A, const ChunkWs* ws, Saved in, int chunks) {
     load_tile<D, kThreads>(kt, A, A.k, b, hk, A.Hk, D, 0, t0, len);
     const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(A.v);
     float accq[kT][4] = {}, acck[kT][4] = {};
-    const auto load_state = [&](const __nv_bfloat16* from) {  // [2][E][D]
+    const auto load_state = [&](const __nv_bfloat16* from) {  // [2][D / 8][E][8]
         constexpr int kPieces = D / 8;
         for (int y = tid; y < 2 * E * kPieces; y += kThreads) {
-            const int r = y / kPieces, p = y % kPieces, part = r / E;
-            cp16((part ? sl : sh) + piece<2 * D>(r % E, p), from + static_cast<size_t>(r) * D + 8 * p, true);
+            const int r = y % E, p = y / E % kPieces, part = y / E / kPieces;
+            cp16((part ? sl : sh) + piece<2 * D>(r, p), from + static_cast<size_t>(y) * 8, true);
         }
         cp_commit();
     };
@@ -800,7 +813,8 @@ gdr_grad(Args A, const ChunkWs* ws, Saved in, int chunks) {
         const size_t page = static_cast<size_t>(D) * E;
         __syncthreads();  // the tiles of the head before are read out
         load_tile<E, kThreads>(dt, A, A.dout, b, h, A.H, E, 0, t0, len);
-        load_bytes<kThreads>(smem_addr(sm.coef), ws[cn].eg, 5 * kC * 4);
+        load_bytes<kThreads>(smem_addr(sm.coef), ws[cn].eg, 3 * kC * 4);
+        load_bytes<kThreads>(smem_addr(sm.coef[3]), ws[cn].g, 2 * kC * 4);
         load_state(in.S0 + cn * 2 * page);
         // rows of w, x, v: u and x as two parts, dbeta and the row sums of x (w - v)
         for (int t = warp; t < kC; t += kGradWarps) {
@@ -992,8 +1006,8 @@ gdr_grad(Args A, const ChunkWs* ws, Saved in, int chunks) {
         {
             const uint32_t* s0 = reinterpret_cast<const uint32_t*>(in.S0 + cn * 2 * page);
             constexpr int kWords = D / 2;
-            for (int y = tid; y < E * kWords; y += kThreads) {
-                const int r = y / kWords, x = y % kWords;
+            for (int y = tid; y < E * kWords; y += kThreads) {  // word y & 3 of piece y / 4 / E of column r
+                const int r = y / 4 % E, x = y / 4 / E * 4 + y % 4;
                 const uint32_t at = piece<2 * D>(r, x >> 2) + 4 * (x & 3);
                 const uint32_t dh = *reinterpret_cast<const uint32_t*>(sm.S[0] + at);
                 const uint32_t dl = *reinterpret_cast<const uint32_t*>(sm.S[1] + at);

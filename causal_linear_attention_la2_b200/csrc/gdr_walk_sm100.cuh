@@ -15,8 +15,10 @@
 //   backward  D1 = dS K^T, D2 = P^T dO;  dU = e^{G_C - G} D1 + D2;
 //             X = dU - N^T (beta dU);
 //             dS = e^{G_C} dS + Q^T (e^G dO) - K^T (beta e^G X).
-// e^{G_C} is multiplied in when the state is read to form its two parts, one
-// chunk ahead, so the accumulation needs no extra pass.
+// e^{G_C} is multiplied in one chunk ahead, when the two parts of the state are
+// already handed to the next product.  An MMA of 64 columns takes as long as one
+// of 128 (measured: 62 cycles either way at M = 128, K = 16), so S K^T and S Q^T
+// are one product of 128 columns.
 //
 // Warps (16): 0 loads (TMA tiles, bulk copies of what gdr_prep left), 1 issues
 // the MMAs, 2 owns the TMEM allocation; 4-7 and 8-11 are the chain's epilogue,
@@ -27,6 +29,8 @@
 // abort flag, all leave their loops, copies and MMAs in flight are waited for
 // and TMEM is freed.
 #pragma once
+#include <type_traits>
+
 #include "gdr_chunk.cuh"
 #include "ptx_sm100.cuh"
 
@@ -42,17 +46,20 @@ enum Mode { kForward = 0, kSave = 1, kBackward = 2 };
 
 template <int D>
 struct Stage {  // 1024-byte aligned; tiles of 64 rows x 64 columns (128 bytes, swizzled)
-    unsigned char k[D / 64][kC * 128], q[D / 64][kC * 128], v[kE / 64][kC * 128];
+    unsigned char kq[D / 64][2][kC * 128];  // K and Q of 64 columns side by side: one operand of 128 rows
+    unsigned char v[kE / 64][kC * 128];
     unsigned char img[4][kC * kC * 2];  // N hi, N lo, P hi, P lo
-    float eg[kC], rest[kC], beta[kC];
-    unsigned char pad[1024 - 3 * kC * 4];
+    float eg[kC], rest[kC], beta[kC], neg_eg[kC], neg_beta[kC], rest_beta[kC], neg_beta_eg[kC];
+    unsigned char pad[2048 - kCoefs * kC * 4];
 };
 
-enum Bar { kFull = 0, kEmpty = 2, kD1 = 4, kZ, kW, kU, kS, kState, kD2, kD2Free, kO, kOFree, kSide, kSaved, kRaw, kEnd, kBars };
+enum Bar { kFull = 0, kEmpty = 2, kState = 4, kFullP = 6, kEmptyP = 8, kD1 = 10, kZ, kW, kU, kUp, kS, kScaled, kD2Free, kO, kOFree, kSide, kSaved, kRaw, kEnd, kBars };
 
 template <int D>
 struct Smem {
     Stage<D> stage[2];
+    unsigned char u[2][kE * 128];  // forward: U^T [e][64 rows], high and low, the operand of P U
+    unsigned char o[kSideWarps][kC * 64];  // forward: bf16 output rows of 32 value columns per warp
     unsigned long long bar[kBars];
     uint32_t tmem;
     int abort;
@@ -68,6 +75,22 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
+// One lane of the warp, always the same one.  MMAs are issued inside a branch on
+// it: under any other condition the compiler has to allow for several lanes.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// D[tmem] (+)= A[tmem] B[smem]; one thread
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+}
+
 struct Waiter {
     uint32_t bars;
     volatile int* abort;
@@ -79,17 +102,20 @@ struct Waiter {
         if (!__all_sync(0xffffffffu, ok)) ok = slow(b, parity & 1, bar);
         return __all_sync(0xffffffffu, ok);
     }
+    // The timer is read every 64 tries only: reading it takes longer than most waits.
     __device__ __noinline__ bool slow(uint32_t b, uint32_t parity, int where) const {
-        const uint64_t t0 = global_ns();
-        while (!mbar_try_wait(b, parity)) {
+        uint64_t t0 = 0;
+        for (uint32_t tries = 1;; ++tries) {
+            if (mbar_try_wait(b, parity)) return true;
+            if (tries % 64) continue;
             if (*abort) return false;
+            if (!t0) t0 = global_ns();
             if (global_ns() - t0 > 2000000000ull) {
                 *abort = 1;
                 atomicCAS(status, 0, 5 | ((200 + where) << 8));
                 return false;
             }
         }
-        return true;
     }
 };
 
@@ -103,30 +129,25 @@ __device__ __forceinline__ void split32(const float (&x)[32], uint32_t (&w)[32])
     for (int y = 0; y < 16; ++y) split_pack2v(make_float2(x[2 * y], x[2 * y + 1]), w[y], w[16 + y]);
 }
 
-// 32 values of one column of a [64 rows][128 columns] bf16 tile pair: rows r0 ..
-__device__ __forceinline__ float tile_at(uint32_t tile, int r, int c) {
-    uint32_t x;
+// Row r, column c of a [64 rows][128 columns] bf16 tile pair
+__device__ __forceinline__ uint32_t tile_bits(uint32_t tile, int r, int c) {
+    unsigned short x;
     const uint32_t a = tile + (c >> 6) * (kC * 128) + piece<128>(r, (c & 63) >> 3) + 2 * (c & 7);
-    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(x) : "r"(a));
-    return __uint_as_float(x << 16);
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a) : "memory");
+    return x;
 }
-
-__device__ __forceinline__ void put_row(const Args& A, void* out, size_t at, float x) {
-    if (A.out_bf16) static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(x);
-    else static_cast<float*>(out)[at] = x;
-}
+__device__ __forceinline__ float tile_at(uint32_t tile, int r, int c) { return __uint_as_float(tile_bits(tile, r, c) << 16); }
 
 template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant__ CUtensorMap mk,
          const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mv, int* status) {
-    extern __shared__ unsigned char walk_tc_raw[];
-    // the dynamic segment starts at a 1024-byte boundary or the tail of 1 KB makes it one
-    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(walk_tc_raw + ((1024 - (smem_addr(walk_tc_raw) & 1023)) & 1023));
+    extern __shared__ __align__(1024) unsigned char walk_tc_raw[];
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(walk_tc_raw);
     constexpr bool kRev = kMode == kBackward;
     constexpr uint32_t kTile = kC * 128;
     // TMEM columns
-    constexpr uint32_t cS = 0, cB = D, cA = 2 * D, cW = cA + 64, cD2 = cW + 64, cD4 = cD2 + 64;
+    constexpr uint32_t cS = 0, cB = D, cA = 2 * D, cD2 = cA + 64, cW = cD2 + 64, cD4 = cW + 64;
     const int n = blockIdx.x, b = n / A.H, h = n % A.H, hk = h / (A.H / A.Hk);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int len = length_of(A, b), nc = (len + kC - 1) / kC;
@@ -142,9 +163,11 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar(kFull + s), 1);
             mbar_init(bar(kEmpty + s), 1 + kChainWarps + kSideWarps);
+            mbar_init(bar(kFullP + s), 1);
+            mbar_init(bar(kEmptyP + s), 1);
         }
-        for (int i : {kD1, kW, kS, kD2, kO, kRaw, kEnd}) mbar_init(bar(i), 1);
-        for (int i : {kZ, kU, kState}) mbar_init(bar(i), kChainWarps);
+        for (int i : {kD1, kW, kS, kO, kRaw, kEnd}) mbar_init(bar(i), 1);
+        for (int i : {kState + 0, kState + 1, int(kZ), int(kU), int(kUp), int(kScaled)}) mbar_init(bar(i), kChainWarps);
         for (int i : {kD2Free, kOFree, kSide, kSaved}) mbar_init(bar(i), kSideWarps);
         fence_mbar_init();
     }
@@ -156,11 +179,17 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = sm.tmem;
+    if (tm != 0) {  // not seen: an allocation of every column starts at the first
+        if (tid == 0) atomicCAS(status, 0, 5 | (199 << 8));
+        __syncthreads();
+        if (warp == 2) tmem_dealloc(tm, 512);
+        return;
+    }
 
     if (warp == 0) {
         // ---------------------------------------------------------------- loads
         constexpr uint32_t kRows = (kMode == kSave ? D / 64 : 2 * (D / 64)) * kTile + (kE / 64) * kTile;
-        constexpr uint32_t kImg = (kMode == kSave ? 2 : 4) * kC * kC * 2, kCoef = 3 * kC * 4;
+        constexpr uint32_t kImg = (kRev ? 4 : 2) * kC * kC * 2, kCoef = kCoefs * kC * 4;
         int issued = 0;
         for (int it = 0; it < nc; ++it) {
             const int s = it & 1, c = kRev ? nc - 1 - it : it, t0 = c * kC;
@@ -170,16 +199,26 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
             const int on = cut ? kRaw : kFull + s;
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar(on), kRows + kImg + kCoef);
-                const auto rows = [&](unsigned char* to, const CUtensorMap& m, int head, int tiles) {
-                    for (int x = 0; x < tiles; ++x)
-                        tma_load_4d(smem_addr(to) + x * kTile, &m, bar(on), 64 * x, A.bthd ? head : t0,
-                                    A.bthd ? t0 : head, b);
+                const auto rows = [&](unsigned char* to, const CUtensorMap& m, int head, int x) {
+                    tma_load_4d(smem_addr(to), &m, bar(on), 64 * x, A.bthd ? head : t0, A.bthd ? t0 : head, b);
                 };
-                rows(st.k[0], mk, hk, D / 64);
-                if (kMode != kSave) rows(st.q[0], mq, hk, D / 64);
-                rows(st.v[0], mv, h, kE / 64);
+                for (int x = 0; x < D / 64; ++x) {
+                    rows(st.kq[x][0], mk, hk, x);
+                    if (kMode != kSave) rows(st.kq[x][1], mq, hk, x);
+                }
+                for (int x = 0; x < kE / 64; ++x) rows(st.v[x], mv, h, x);
                 bulk_load(smem_addr(st.img), cw[c].img, kImg, bar(on));
                 bulk_load(smem_addr(st.eg), cw[c].eg, kCoef, bar(on));
+            }
+            if (kMode == kForward) {  // P, which is read a chunk later than the rest, has barriers of its own
+                if (it >= 2 && !wait(kEmptyP + s, (it >> 1) - 1)) {
+                    ++issued;
+                    break;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(kFullP + s), 2 * kC * kC * 2);
+                    bulk_load(smem_addr(st.img[2]), cw[c].img[2], 2 * kC * kC * 2, bar(kFullP + s));
+                }
             }
             issued = it + 1;
             if (cut) {
@@ -189,8 +228,8 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
                         const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
                         for (int y = 0; y < D / 64; ++y) {
-                            *reinterpret_cast<uint4*>(st.k[y] + r * 128 + x * 16) = z;
-                            if (kMode != kSave) *reinterpret_cast<uint4*>(st.q[y] + r * 128 + x * 16) = z;
+                            *reinterpret_cast<uint4*>(st.kq[y][0] + r * 128 + x * 16) = z;
+                            if (kMode != kSave) *reinterpret_cast<uint4*>(st.kq[y][1] + r * 128 + x * 16) = z;
                         }
 #pragma unroll
                         for (int y = 0; y < kE / 64; ++y) *reinterpret_cast<uint4*>(st.v[y] + r * 128 + x * 16) = z;
@@ -205,99 +244,125 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
             const int c = kRev ? nc - 1 - it : it;
             const bool cut = c * kC + kC > len && len < A.T;
             mbar_wait(cut ? bar(kRaw) : bar(kFull + (it & 1)), cut ? 0 : (it >> 1) & 1);
+            // (a P that was never asked for, after an abort, costs this wait its two seconds)
+            if (kMode == kForward) mbar_wait(bar(kFullP + (it & 1)), (it >> 1) & 1);
         }
     } else if (warp == 1) {
         // ----------------------------------------------------------------- MMAs
-        const uint32_t lead = lane == 0;
         constexpr uint32_t kId = idesc_bf16_f32(kE, 64, 0, 0);    // B [64 rows][k]
+        constexpr uint32_t kIdQ = idesc_bf16_f32(kE, 128, 0, 0);  // B [128 rows][k]
         constexpr uint32_t kIdT = idesc_bf16_f32(kE, 64, 0, 1);   // B from rows [k][64]
         constexpr uint32_t kIdTT = idesc_bf16_f32(kE, 64, 1, 1);  // A from rows [k][128] as well
         constexpr uint32_t kIdS = idesc_bf16_f32(kE, D, 0, 1);    // B from rows [k][d]
-        for (int it = 0; it < nc; ++it) {
-            const int s = it & 1;
+        constexpr int kGroups = D / 64;
+        // All of TMEM is this CTA's, so its first column is 0 (checked above); with the
+        // stage known at compile time too, every address below is a constant, and
+        // an MMA is issued in a few cycles (78 with the addresses in registers).
+        constexpr uint32_t tm = 0;
+        // P U of chunk `it`, issued behind S K^T of the next chunk: the tensor cores
+        // would idle there, and the chain does not wait for it.
+        const auto output = [&](int it, auto stage) -> bool {
+            constexpr int s = decltype(stage)::value;
+            if (!(wait(kUp, it) && wait(kFullP + s, it >> 1) && (it == 0 || wait(kOFree, it - 1)))) return false;
+            tc_fence_after();
+            if (elect()) {
+                const uint32_t img = smem_addr(sm.stage[s].img);
+                const uint64_t uh = sdesc_sw128(smem_addr(sm.u[0]), 16, 1024), ul = sdesc_sw128(smem_addr(sm.u[1]), 16, 1024);
+                const uint64_t ph = sdesc_sw128(img + 2 * kTile, 16, 1024), pl = sdesc_sw128(img + 3 * kTile, 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    mma_bf16_ss(tm + cD4, desc_add(uh, kk * 32), desc_add(ph, kk * 32), kId, kk > 0);
+                    mma_bf16_ss(tm + cD4, desc_add(ul, kk * 32), desc_add(ph, kk * 32), kId, 1);
+                    mma_bf16_ss(tm + cD4, desc_add(uh, kk * 32), desc_add(pl, kk * 32), kId, 1);
+                }
+                mma_commit(bar(kO));
+                mma_commit(bar(kEmptyP + s));
+            }
+            return true;
+        };
+        const auto chunk = [&](int it, auto stage) -> bool {
+            constexpr int s = decltype(stage)::value;
             Stage<D>& st = sm.stage[s];
-            if (!wait(kFull + s, it >> 1)) break;
-            const uint64_t dk = sdesc_sw128(smem_addr(st.k), 16, 1024), dq = sdesc_sw128(smem_addr(st.q), 16, 1024);
-            const uint64_t tk = sdesc_sw128(smem_addr(st.k), kTile, 1024), tq = sdesc_sw128(smem_addr(st.q), kTile, 1024);
-            const uint32_t img = smem_addr(st.img);
+            if (!wait(kFull + s, it >> 1)) return false;
+            const uint32_t kq = smem_addr(st.kq), img = smem_addr(st.img);
+            const uint64_t dk = sdesc_sw128(kq, 16, 1024);
+            const uint64_t tk = sdesc_sw128(kq, 2 * kTile, 1024), tq = sdesc_sw128(kq + kTile, 2 * kTile, 1024);
             if (kRev) {
                 // P^T dO: free of the chain (z of the chunk before has read it out)
                 const uint64_t td = sdesc_sw128(smem_addr(st.v), kTile, 1024);
                 tc_fence_after();
+                if (elect())
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16_ss_w(tm + cD2, desc_add(td, kk * 2048),
-                                      sdesc_sw128(img + (2 + x) * kTile + kk * 2048, kTile, 1024), kIdTT, x + kk > 0, lead);
+                        mma_bf16_ss(tm + cD2, desc_add(td, kk * 2048),
+                                      sdesc_sw128(img + (2 + x) * kTile + kk * 2048, kTile, 1024), kIdTT, x + kk > 0);
             }
-            if (!wait(kState, it)) break;
-            if (!kRev && kMode == kForward && it > 0 && !wait(kO, it - 1)) break;  // P U has read its operand
-            tc_fence_after();
+            // the output warps have read what S Q^T overwrites
+            if (kMode == kForward && it > 0 && !wait(kD2Free, it - 1)) return false;
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t bd = desc_add(dk, (kk >> 2) * kTile + (kk & 3) * 32);
-                mma_bf16_ts_w(tm + cA, tm + cB + op_hi(kk), bd, kId, kk > 0, lead);
-                mma_bf16_ts_w(tm + cA, tm + cB + op_lo(kk), bd, kId, 1, lead);
-            }
-            mma_commit_w(bar(kD1), lead);
-            if (kMode == kForward) {
-                if (it > 0 && !wait(kD2Free, it - 1)) break;
+            for (int y = 0; y < kGroups; ++y) {
+                if (!wait(kState + y, it)) return false;
                 tc_fence_after();
+                if (elect()) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint64_t bd = desc_add(dq, (kk >> 2) * kTile + (kk & 3) * 32);
-                    mma_bf16_ts_w(tm + cD2, tm + cB + op_hi(kk), bd, kId, kk > 0, lead);
-                    mma_bf16_ts_w(tm + cD2, tm + cB + op_lo(kk), bd, kId, 1, lead);
+                for (int z = 0; z < 4; ++z) {
+                    const int kk = 2 * ((z >> 1) * kGroups + y) + (z & 1);
+                    const uint64_t bd = desc_add(dk, (kk >> 2) * 2 * kTile + (kk & 3) * 32);
+                    const uint32_t id = kMode == kForward ? kIdQ : kId;
+                    mma_ts(tm + cA, tm + cB + op_hi(kk), bd, id, y + z > 0);
+                    mma_ts(tm + cA, tm + cB + op_lo(kk), bd, id, 1);
                 }
-                mma_commit_w(bar(kD2), lead);
+                if (y == kGroups - 1) mma_commit(bar(kD1));
+                }
             }
+            if (kMode == kForward && it > 0 && !output(it - 1, std::integral_constant<int, s ^ 1>())) return false;
             if (kRev) {
-                if (!wait(kSide, it)) break;  // e^G dO
+                if (!(wait(kSide, it) && wait(kScaled, it))) return false;  // e^G dO
                 tc_fence_after();
+                if (elect())
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
-                    mma_bf16_ts_w(tm + cS, tm + cD4 + op_hi(kk), desc_add(tq, kk * 2048), kIdS, 1, lead);
-                    mma_bf16_ts_w(tm + cS, tm + cD4 + op_lo(kk), desc_add(tq, kk * 2048), kIdS, 1, lead);
+                    mma_ts(tm + cS, tm + cD4 + op_hi(kk), desc_add(tq, kk * 2048), kIdS, 1);
+                    mma_ts(tm + cS, tm + cD4 + op_lo(kk), desc_add(tq, kk * 2048), kIdS, 1);
                 }
             }
-            if (!wait(kZ, it)) break;
+            if (!wait(kZ, it)) return false;
             tc_fence_after();
-            {
+            if (elect()) {
                 const uint32_t id = kRev ? kIdT : kId;
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     const uint32_t o = kRev ? kk * 2048 : kk * 32;
                     const uint64_t bh = sdesc_sw128(img + o, kRev ? kTile : 16, 1024);
                     const uint64_t bl = sdesc_sw128(img + kTile + o, kRev ? kTile : 16, 1024);
-                    mma_bf16_ts_w(tm + cW, tm + cA + op_hi(kk), bh, id, 1, lead);
-                    mma_bf16_ts_w(tm + cW, tm + cA + op_lo(kk), bh, id, 1, lead);
-                    mma_bf16_ts_w(tm + cW, tm + cA + op_hi(kk), bl, id, 1, lead);
+                    mma_ts(tm + cW, tm + cA + op_hi(kk), bh, id, 1);
+                    mma_ts(tm + cW, tm + cA + op_lo(kk), bh, id, 1);
+                    mma_ts(tm + cW, tm + cA + op_hi(kk), bl, id, 1);
                 }
+                mma_commit(bar(kW));
             }
-            mma_commit_w(bar(kW), lead);
-            if (!wait(kU, it)) break;
+            if (!(wait(kScaled, it) && wait(kU, it))) return false;
             tc_fence_after();
+            if (elect()) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-                mma_bf16_ts_w(tm + cS, tm + cW + op_hi(kk), desc_add(tk, kk * 2048), kIdS, 1, lead);
-                mma_bf16_ts_w(tm + cS, tm + cW + op_lo(kk), desc_add(tk, kk * 2048), kIdS, 1, lead);
+                mma_ts(tm + cS, tm + cW + op_hi(kk), desc_add(tk, kk * 2048), kIdS, 1);
+                mma_ts(tm + cS, tm + cW + op_lo(kk), desc_add(tk, kk * 2048), kIdS, 1);
             }
-            mma_commit_w(bar(kS), lead);
-            if (kMode == kForward) {
-                if (it > 0 && !wait(kOFree, it - 1)) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    const uint64_t bh = sdesc_sw128(img + 2 * kTile + kk * 32, 16, 1024);
-                    const uint64_t bl = sdesc_sw128(img + 3 * kTile + kk * 32, 16, 1024);
-                    mma_bf16_ts_w(tm + cD4, tm + cA + op_hi(kk), bh, kId, kk > 0, lead);
-                    mma_bf16_ts_w(tm + cD4, tm + cA + op_lo(kk), bh, kId, 1, lead);
-                    mma_bf16_ts_w(tm + cD4, tm + cA + op_hi(kk), bl, kId, 1, lead);
-                }
-                mma_commit_w(bar(kO), lead);
+            mma_commit(bar(kS));
             }
-            mma_commit_w(bar(kEmpty + s), lead);
+            if (elect()) mma_commit(bar(kEmpty + s));
+            return true;
+        };
+        for (int it = 0; it < nc; it += 2) {
+            if (!chunk(it, std::integral_constant<int, 0>())) break;
+            if (it + 1 < nc && !chunk(it + 1, std::integral_constant<int, 1>())) break;
+        }
+        if (kMode == kForward && nc > 0 && !sm.abort) {
+            if (nc & 1) output(nc - 1, std::integral_constant<int, 0>());
+            else output(nc - 1, std::integral_constant<int, 1>());
         }
     } else if (warp >= 4 && warp < 12) {
         // ------------------------------------------------------ the chain's epilogue
@@ -311,57 +376,96 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
         if (kMode == kSave) last = nullptr;
         if (last) last += n * page;
         const int r0 = 32 * half;
-        const auto publish = [&](float (&S)[32], int q, float ec) {  // two parts, and e^{G_C} S to accumulate onto
-            uint32_t w[32];
-            split32(S, w);
-            tmem_st32u(row + cB + 32 * q, w);
-#pragma unroll
-            for (int y = 0; y < 32; ++y) S[y] *= ec;
-            tmem_st32(row + cS + 32 * q, S);
-        };
         const auto done = [&](int i) {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive(bar(i));
         };
-        bool ok = nc > 0 && wait(kFull, 0);
-        if (ok || nc == 0) {
-            const float ec = nc > 0 ? sm.stage[0].eg[kC - 1] : 1.f;
+        // x *= f, f 32 consecutive floats of shared memory (the same for the whole warp)
+        const auto times = [](float (&x)[32], const float* f) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 4) {
+                const float4 m = *reinterpret_cast<const float4*>(f + y);
+                const float2 p = mul2(make_float2(m.x, m.y), make_float2(x[y], x[y + 1]));
+                const float2 r = mul2(make_float2(m.z, m.w), make_float2(x[y + 2], x[y + 3]));
+                x[y] = p.x;
+                x[y + 1] = p.y;
+                x[y + 2] = r.x;
+                x[y + 3] = r.y;
+            }
+        };
+        const auto scale = [&](float ec) {  // S -> e^{G_C} S, to accumulate onto
 #pragma unroll 1
             for (int y = 0; y < kGroups; ++y) {
-                const int q = half * kGroups + y;
+                const uint32_t at = row + cS + 32 * (half * kGroups + y);
                 float S[32];
+                tmem_ld32(at, S);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) S[i] = state(first, 32 * q + i);
-                if (nc > 0) publish(S, q, ec);
-                else if (last)
+                for (int i = 0; i < 32; ++i) S[i] *= ec;
+                tmem_st32(at, S);
+            }
+            done(kScaled);
+        };
+        bool ok = nc > 0;
+#pragma unroll 1
+        for (int y = 0; y < kGroups; ++y) {
+            const int q = half * kGroups + y;
+            float S[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) last[static_cast<size_t>(32 * q + i) * kE + e] = S[i];
+            for (int i = 0; i < 32; ++i) S[i] = state(first, 32 * q + i);
+            if (nc > 0) {
+                uint32_t w[32];
+                tmem_st32(row + cS + 32 * q, S);
+                split32(S, w);
+                tmem_st32u(row + cB + 32 * q, w);
+                done(kState + y);
+            } else if (last) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) last[static_cast<size_t>(32 * q + i) * kE + e] = S[i];
             }
         }
-        if (ok) done(kState);
         for (int it = 0; ok && it < nc; ++it) {
             const int s = it & 1, c = kRev ? nc - 1 - it : it;
             Stage<D>& st = sm.stage[s];
+            if (!(ok = wait(kFull + s, it >> 1))) break;
+            scale(st.eg[kC - 1]);
+            uint32_t v[16];  // this column of 32 rows of V, in pairs: read before the product is waited for
+            if (!kRev) {
+                const uint32_t vt = smem_addr(st.v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    v[i] = tile_bits(vt, r0 + 2 * i, e) | tile_bits(vt, r0 + 2 * i + 1, e) << 16;
+            }
             if (!(ok = wait(kD1, it))) break;
             tc_fence_after();
             {
-                float x[32], y[32];
+                float x[32];
                 uint32_t w[32];
                 tmem_ld32(row + cA + r0, x);
                 if (kRev) {
+                    float y[32];
                     tmem_ld32(row + cD2 + r0, y);
+                    times(x, st.rest + r0);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = fmaf(st.rest[r0 + i], x[i], y[i]);
+                    for (int i = 0; i < 32; ++i) x[i] += y[i];
                 } else {
-                    const uint32_t vt = smem_addr(st.v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = fmaf(-st.eg[r0 + i], x[i], tile_at(vt, r0 + i, e));
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(st.neg_eg + r0 + i);
+                        const uint32_t v0 = v[i / 2], v1 = v[i / 2 + 1];
+                        const float2 p = fma2(make_float2(m.x, m.y), make_float2(x[i], x[i + 1]),
+                                              make_float2(low_of(v0), high_of(v0)));
+                        const float2 r = fma2(make_float2(m.z, m.w), make_float2(x[i + 2], x[i + 3]),
+                                              make_float2(low_of(v1), high_of(v1)));
+                        x[i] = p.x;
+                        x[i + 1] = p.y;
+                        x[i + 2] = r.x;
+                        x[i + 3] = r.y;
+                    }
                 }
                 tmem_st32(row + cW + r0, x);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] *= -st.beta[r0 + i];
+                times(x, st.neg_beta + r0);
                 split32(x, w);
                 tmem_st32u(row + cA + r0, w);
             }
@@ -372,44 +476,50 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
                 float x[32];
                 uint32_t w[32];
                 tmem_ld32(row + cW + r0, x);
-                if (kMode != kForward) {  // rows w or x for the gradients
+                {
+                    float u[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) u[i] = x[i];
+                    times(u, (kRev ? st.neg_beta_eg : st.rest_beta) + r0);
+                    split32(u, w);
+                    tmem_st32u(row + cW + r0, w);
+                }
+                done(kU);
+                if (kMode == kForward) {
+                    times(x, st.beta + r0);
+                    split32(x, w);
+                    if (it > 0 && !(ok = wait(kO, it - 1))) break;  // P U of the chunk before has read its operand
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        st_shared_v4(smem_addr(sm.u[y >> 2]) + piece<128>(e, 4 * half + (y & 3)), w[4 * y], w[4 * y + 1],
+                                     w[4 * y + 2], w[4 * y + 3]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive(bar(kUp));
+                } else {  // rows w or x for the gradients
                     float* to = (kRev ? out.X : out.W) + (static_cast<size_t>(n) * A.T + c * kC + r0) * kE + e;
                     const int left = len - c * kC - r0;
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         if (i < left) to[static_cast<size_t>(i) * kE] = x[i];
                 }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] *= st.beta[r0 + i];
-                if (kMode == kForward) {
-                    split32(x, w);
-                    tmem_st32u(row + cA + r0, w);
-                }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] *= kRev ? -st.eg[r0 + i] : st.rest[r0 + i];
-                split32(x, w);
-                tmem_st32u(row + cW + r0, w);
             }
             __syncwarp();
-            if (lane == 0) arrive(bar(kEmpty + s));  // this stage's rows and coefficients are read out
-            done(kU);
-            float ec = 1.f;
-            if (it + 1 < nc) {
-                if (!(ok = wait(kFull + (s ^ 1), (it + 1) >> 1))) break;
-                ec = sm.stage[s ^ 1].eg[kC - 1];
-            }
+            if (lane == 0) arrive(bar(kEmpty + s));  // this stage's rows and factors are read out
             if (kMode != kForward && !(ok = wait(kSaved, it))) break;
             if (!(ok = wait(kS, it))) break;
             tc_fence_after();
             if (it + 1 < nc) {
-#pragma unroll 1
+#pragma unroll
                 for (int y = 0; y < kGroups; ++y) {
                     const int q = half * kGroups + y;
                     float S[32];
+                    uint32_t w[32];
                     tmem_ld32(row + cS + 32 * q, S);
-                    publish(S, q, ec);
+                    split32(S, w);
+                    tmem_st32u(row + cB + 32 * q, w);
+                    done(kState + y);
                 }
-                done(kState);
             } else if (last) {
 #pragma unroll 1
                 for (int y = 0; y < kGroups; ++y) {
@@ -430,18 +540,31 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
             Stage<D>& st = sm.stage[s];
             if (!wait(kFull + s, it >> 1)) break;
             if (kMode == kForward) {
+                // Accumulator fragments (ptx_sm100.cuh): o[x][4 j + y] is row 32 x + 8 j + 2 i + (y & 1) of
+                // value column g + 8 (y >> 1), o[x][16 + ..] of column 16 further.
                 float o[2][32];
-                if (!wait(kD2, it)) break;
+                const int g = lane >> 2, i = lane & 3;
+                if (!wait(kD1, it)) break;
                 tc_fence_after();
-                tmem_ld32(row + cD2, o[0]);
-                tmem_ld32(row + cD2 + 32, o[1]);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    tmem_ld16x256b_x4_pair(row + cD2 + 32 * x, row + cD2 + 32 * x + (16u << 16), o[x]);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(bar(kD2Free));
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[x][i] *= st.eg[32 * x + i];
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 m = *reinterpret_cast<const float2*>(st.eg + 32 * x + 8 * j + 2 * i);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int z = 0; z < 4; z += 2) {
+                                o[x][16 * y + 4 * j + z] *= m.x;
+                                o[x][16 * y + 4 * j + z + 1] *= m.y;
+                            }
+                    }
                 __syncwarp();
                 if (lane == 0) arrive(bar(kEmpty + s));
                 if (!wait(kO, it)) break;
@@ -449,20 +572,53 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     float y[32];
-                    tmem_ld32(row + cD4 + 32 * x, y);
+                    tmem_ld16x256b_x4_pair(row + cD4 + 32 * x, row + cD4 + 32 * x + (16u << 16), y);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[x][i] += y[i];
+                    for (int z = 0; z < 32; ++z) o[x][z] += y[z];
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(bar(kOFree));
-                const size_t step = row_at(A, 0, 0, A.H, 1, kE) - row_at(A, 0, 0, A.H, 0, kE);
-                const size_t at = row_at(A, b, h, A.H, t0, kE) + e;
+                const size_t step = A.bthd ? static_cast<size_t>(A.H) * kE : kE;
+                const size_t at = row_at(A, b, h, A.H, t0, kE) + 32 * (warp & 3);
+                const int left = len - t0;
+                if (A.out_bf16) {
+                    // through shared memory: rows of 64 bytes, their pieces permuted by the row
+                    unsigned char* mine = sm.o[warp & 3];
+                    const uint32_t base = smem_addr(mine);
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                    for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (t0 + 32 * x + i < len) put_row(A, A.o, at + (32 * x + i) * step, o[x][i]);
+                        for (int j = 0; j < 4; ++j) {
+                            const int t = 32 * x + 8 * j + (lane & 7);
+                            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(
+                                             base + t * 64 + (((lane >> 3) ^ ((t >> 1) & 3)) << 4)),
+                                         "r"(pack(o[x][4 * j], o[x][4 * j + 1])),
+                                         "r"(pack(o[x][4 * j + 2], o[x][4 * j + 3])),
+                                         "r"(pack(o[x][16 + 4 * j], o[x][16 + 4 * j + 1])),
+                                         "r"(pack(o[x][16 + 4 * j + 2], o[x][16 + 4 * j + 3]))
+                                         : "memory");
+                        }
+                    __syncwarp();
+                    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(A.o) + at + 8 * i;
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const int t = 8 * y + g;
+                        if (t < left)
+                            *reinterpret_cast<uint4*>(p + t * step) =
+                                *reinterpret_cast<const uint4*>(mine + t * 64 + ((i ^ ((t >> 1) & 3)) << 4));
+                    }
+                    __syncwarp();
+                } else {
+                    float* p = static_cast<float*>(A.o) + at + g;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int z = 0; z < 32; ++z) {
+                            const int t = 32 * x + 8 * (z / 4 % 4) + 2 * i + (z & 1);
+                            if (t < left) p[t * step + 16 * (z >> 4) + 8 * (z >> 1 & 1)] = o[x][z];
+                        }
+                }
                 continue;
             }
             if (kRev) {
@@ -485,21 +641,19 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
             }
             __syncwarp();
             if (lane == 0) arrive(bar(kEmpty + s));
-            // the state (forward: before the chunk, backward: the gradient after it) to memory, [2][e][d]
-            if (!wait(kState, it)) break;
+            // the state (forward: before the chunk, backward: the gradient after it) to memory (Saved's layout)
+            if (!(wait(kState, it) && (D == 64 || wait(kState + 1, it)))) break;
             tc_fence_after();
-            uint32_t* hi = reinterpret_cast<uint32_t*>((kRev ? out.dS1 : out.S0) +
-                                                       (static_cast<size_t>(n) * chunks + c) * 2 * page) + e * (D / 2);
+            __nv_bfloat16* to = (kRev ? out.dS1 : out.S0) + (static_cast<size_t>(n) * chunks + c) * 2 * page + e * 8;
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
                 float w[32];
                 tmem_ld32(row + cB + 32 * q, w);
 #pragma unroll
-                for (int x = 0; x < 32; x += 4) {
-                    uint4 y = make_uint4(__float_as_uint(w[x]), __float_as_uint(w[x + 1]), __float_as_uint(w[x + 2]),
-                                         __float_as_uint(w[x + 3]));
-                    *reinterpret_cast<uint4*>(hi + (x >> 4) * (page / 2) + 16 * q + (x & 15)) = y;
-                }
+                for (int x = 0; x < 32; x += 4)  // 8 columns of d: 16 bytes next to the neighbouring lanes'
+                    *reinterpret_cast<uint4*>(to + (x >> 4) * page + (4 * q + (x & 15) / 4) * (kE * 8)) =
+                        make_uint4(__float_as_uint(w[x]), __float_as_uint(w[x + 1]), __float_as_uint(w[x + 2]),
+                                   __float_as_uint(w[x + 3]));
             }
             tc_fence_before();
             __syncwarp();
@@ -509,7 +663,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
     __syncwarp();
     // MMAs in flight end before TMEM goes: the issuer's last commit is waited for
     if (warp == 1) {
-        mma_commit_w(bar(kEnd), lane == 0);
+        if (elect()) mma_commit(bar(kEnd));
         mbar_wait(bar(kEnd), 0);
     }
     tc_fence_before();
