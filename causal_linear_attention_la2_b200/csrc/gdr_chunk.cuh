@@ -4,8 +4,7 @@
 // With G_t the cumulative gates of a chunk, S0 the state before it and
 // Ah_ts = e^{G_t - G_s} (k_t . k_s) (s < t), P_ts = e^{G_t - G_s} (q_t . k_s) (s <= t),
 // the rows w_t of the chunk solve (I + Ah diag(beta)) W = Z, Z = V - diag(e^G) K S0.
-// With N = (I + Ah diag(beta))^{-1} Ah (strictly lower, one forward substitution
-// per column) both inverses that the two directions need are plain:
+// With N = (I + Ah diag(beta))^{-1} Ah (strictly lower) both inverses that the two directions need are plain:
 //
 //   (I + Ah diag(beta))^{-1} = I - N diag(beta),  (I + diag(beta) Ah)^{-1} = I - diag(beta) N,
 //
@@ -36,6 +35,8 @@
 // from it stay in the registers of one warp from the first row to the last,
 // and the warps of a CTA share only the tiles of K, Q, N and P.
 #pragma once
+#include <type_traits>
+
 #include "gdr_common.cuh"
 
 namespace la2 {
@@ -46,7 +47,7 @@ constexpr int kC = 64;
 // Workspace of one chunk of one value head: N and P, each as a high and a low
 // 64 x 64 bf16 image (row t of 128 bytes, 16-byte pieces permuted by t % 8, as
 // they lie in shared memory), and the factors of each row: e^G, e^{G_C - G}, beta
-// and what the walks multiply by, G itself as two floats.
+// and what the walks multiply by, and G / ln 2 as two floats.
 struct ChunkWs {
     unsigned char img[4][kC * kC * 2];  // N hi, N lo, P hi, P lo
     float eg[kC], rest[kC], beta[kC];
@@ -153,13 +154,17 @@ __device__ __forceinline__ void mma2(float (&c0)[4], float (&c1)[4], const uint3
 template <int W, int kThreads>
 __device__ __forceinline__ void load_tile(uint32_t tile, const Args& A, const void* src, int b, int h, int nh,
                                           int width, int c0, int t0, int len) {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(src);
-    constexpr int kPieces = W / 8;
+    constexpr int kPieces = W / 8, kStep = kThreads / kPieces;
+    static_assert(kThreads % kPieces == 0 && kC % kStep == 0 && kStep % 8 == 0, "whole rows, one permutation per thread");
+    const int r = threadIdx.x / kPieces, c = threadIdx.x % kPieces;
+    const size_t step = static_cast<size_t>(kStep) * width * (A.bthd ? nh : 1);
+    const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(src);
+    const __nv_bfloat16* p = base + row_at(A, b, h, nh, t0 + r, width) + c0 + 8 * c;
+    const uint32_t to = tile + piece<2 * W>(r, c);
 #pragma unroll
-    for (int x = threadIdx.x; x < kC * kPieces; x += kThreads) {
-        const int r = x / kPieces, c = x % kPieces;
-        const bool ok = t0 + r < len;
-        cp16(tile + piece<2 * W>(r, c), p + (ok ? row_at(A, b, h, nh, t0 + r, width) + c0 + 8 * c : 0), ok);
+    for (int x = 0; x < kC / kStep; ++x, p += step) {
+        const bool ok = t0 + r + x * kStep < len;
+        cp16(to + x * kStep * 2 * W, ok ? p : base, ok);
     }
 }
 
@@ -171,18 +176,71 @@ __device__ __forceinline__ void load_bytes(uint32_t dst, const void* src, int by
 
 // ------------------------------------------------------------------ gdr_prep
 
-constexpr int kPrepThreads = 128;
+constexpr int kPrepThreads = 256;
+constexpr int kPitchA = kC + 8, kPitchN = kC + 4;  // floats per row in shared memory
 
 template <int D>
 struct PrepSmem {
-    unsigned char k[kC * D * 2], q[kC * D * 2];
-    float a[kC][kC + 1];   // Ah
-    float ab[kC][kC + 4];  // Ah diag(beta): rows read as float4
+    union {
+        unsigned char kq[2][kC * D * 2];
+        struct {
+            float a[kC][kPitchA];  // Ah
+            float n[kC][kPitchN];  // N
+        };
+    };
     ChunkWs out;
 };
 
-// N and P of one chunk.  Four warps take 16 rows of K K^T and Q K^T each; then a
-// thread takes a column of N:  N_ts = Ah_ts - sum_{s < r < t} Ah_tr beta_r N_rs.
+// (x, y) as three pairs of bf16: all 24 bits of the significand
+__device__ __forceinline__ void split3(float x, float y, uint32_t& h, uint32_t& m, uint32_t& l) {
+    h = pack(x, y);
+    x -= low_of(h);
+    y -= high_of(h);
+    split(x, y, m, l);
+}
+
+// acc (rows tr .., columns sc .. of a 16 x 8 tile) -= M diag(beta) n over r0 ..
+// r0 + 16 kSteps, M and n fp32 in shared memory.  Both are split into three bf16
+// parts (2^-24 is lost, as in fp32): where keys repeat the terms cancel, and what
+// two parts lose of them shows in N.
+template <int kSteps, int kPitchM>
+__device__ __forceinline__ void take(float (&acc)[4], const float (*M)[kPitchM], const float (*n)[kPitchN],
+                                     const float* beta, int tr, int sc, int r0, int lane) {
+    const int g = lane >> 2, i = lane & 3;
+#pragma unroll
+    for (int kk = 0; kk < kSteps; ++kk) {
+        uint32_t ah[4], am[4], al[4], bh[2], bm[2], bl[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int r = r0 + 16 * kk + 8 * x + 2 * i;
+            const float2 b2 = *reinterpret_cast<const float2*>(beta + r);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const float2 m = *reinterpret_cast<const float2*>(&M[tr + g + 8 * y][r]);
+                split3(-b2.x * m.x, -b2.y * m.y, ah[2 * x + y], am[2 * x + y], al[2 * x + y]);
+            }
+            split3(n[r][sc + g], n[r + 1][sc + g], bh[x], bm[x], bl[x]);
+        }
+        mma(acc, al, bh[0], bh[1]);
+        mma(acc, am, bm[0], bm[1]);
+        mma(acc, ah, bl[0], bl[1]);
+        mma(acc, am, bh[0], bh[1]);
+        mma(acc, ah, bm[0], bm[1]);
+        mma(acc, ah, bh[0], bh[1]);
+    }
+}
+
+// N and P of one chunk: warps 0-3 make 16 rows of K K^T each, warps 4-7 of Q K^T.
+//
+// N = (I + Ah diag(beta))^{-1} Ah by halves: with the blocks of the first and
+// second half of the rows,
+//   N11, N22 as for a chunk of half the length,
+//   Y = Ah21 - Ah21 diag(beta1) N11,   N21 = Y - N22 diag(beta2) Y,
+// four blocks of 16 by forward substitution in fp32 (a thread per column,
+// N_ts = Ah_ts - sum_{s < r < t} Ah_tr beta_r N_rs), then 16 -> 32 -> 64 on the
+// tensor cores.  A substitution over all 64 rows is a chain four
+// times as long with most threads idle (7680 chunks of d = 128: 355 us against
+// 257 us with the joins on the SIMT cores, bound by shared memory).
 template <int D>
 __global__ void __launch_bounds__(kPrepThreads)
 gdr_prep(Args A, ChunkWs* ws, int chunks) {
@@ -192,7 +250,7 @@ gdr_prep(Args A, ChunkWs* ws, int chunks) {
     const int len = length_of(A, b), t0 = c * kC;
     if (t0 >= len) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hk = h / (A.H / A.Hk);
-    const uint32_t kt = smem_addr(sm.k), qt = smem_addr(sm.q);
+    const uint32_t kt = smem_addr(sm.kq[0]), qt = smem_addr(sm.kq[1]);
     load_tile<D, kPrepThreads>(kt, A, A.k, b, hk, A.Hk, A.d, 0, t0, len);
     load_tile<D, kPrepThreads>(qt, A, A.q, b, hk, A.Hk, A.d, 0, t0, len);
     cp_commit();
@@ -216,15 +274,17 @@ gdr_prep(Args A, ChunkWs* ws, int chunks) {
             const double y = __shfl_up_sync(0xffffffffu, s, m);
             if (lane >= m) s += y;
         }
+        s *= 1.4426950408889634;  // in powers of two from here on
+        g1 *= 1.4426950408889634;
         const double all = __shfl_sync(0xffffffffu, s, 31), first = s - g1;
         sm.out.g[t] = static_cast<float>(first);
         sm.out.g[t + 1] = static_cast<float>(s);
         sm.out.gl[t] = static_cast<float>(first - sm.out.g[t]);
         sm.out.gl[t + 1] = static_cast<float>(s - sm.out.g[t + 1]);
-        sm.out.eg[t] = expf(sm.out.g[t]) * (1.f + sm.out.gl[t]);
-        sm.out.eg[t + 1] = expf(sm.out.g[t + 1]) * (1.f + sm.out.gl[t + 1]);
-        sm.out.rest[t] = expf(static_cast<float>(all - first));
-        sm.out.rest[t + 1] = expf(static_cast<float>(all - s));
+        sm.out.eg[t] = exp2f(sm.out.g[t]) * (1.f + 0.6931472f * sm.out.gl[t]);
+        sm.out.eg[t + 1] = exp2f(sm.out.g[t + 1]) * (1.f + 0.6931472f * sm.out.gl[t + 1]);
+        sm.out.rest[t] = exp2f(static_cast<float>(all - first));
+        sm.out.rest[t + 1] = exp2f(static_cast<float>(all - s));
         sm.out.beta[t] = b0;
         sm.out.beta[t + 1] = b1;
 #pragma unroll
@@ -238,69 +298,121 @@ gdr_prep(Args A, ChunkWs* ws, int chunks) {
     }
     cp_wait<0>();
     __syncthreads();
-    const int g = lane >> 2, i = lane & 3;
-    {
-        float ck[8][4] = {}, cq[8][4] = {};
+    const int g = lane >> 2, i = lane & 3, rt = warp & 3;
+    const bool isq = warp >= 4;
+    float acc[8][4] = {};
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t ka[4], qa[4], bb[4];
-            ld_a<2 * D>(ka, kt, warp, kk, lane);
-            ld_a<2 * D>(qa, qt, warp, kk, lane);
+    for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t aa[4], bb[4];
+        ld_a<2 * D>(aa, isq ? qt : kt, rt, kk, lane);
 #pragma unroll
-            for (int jp = 0; jp < 4; ++jp) {
-                if (jp <= warp) {
-                    ld_b<2 * D>(bb, kt, jp, kk, lane);
-                    mma2(ck[2 * jp], ck[2 * jp + 1], ka, bb);
-                    mma2(cq[2 * jp], cq[2 * jp + 1], qa, bb);
-                }
+        for (int jp = 0; jp < 4; ++jp) {
+            if (jp <= rt) {
+                ld_b<2 * D>(bb, kt, jp, kk, lane);
+                mma2(acc[2 * jp], acc[2 * jp + 1], aa, bb);
             }
         }
+    }
+    __syncthreads();  // K and Q are read out: a and n take their place
+    const float* beta = sm.out.beta;
+    const float gt[2] = {sm.out.g[16 * rt + g], sm.out.g[16 * rt + g + 8]};
+    const float gtl[2] = {sm.out.gl[16 * rt + g], sm.out.gl[16 * rt + g + 8]};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 8; ++j) {
+        const float2 gs = *reinterpret_cast<const float2*>(&sm.out.g[8 * j + 2 * i]);
+        const float2 gsl = *reinterpret_cast<const float2*>(&sm.out.gl[8 * j + 2 * i]);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int t = 16 * warp + g + 8 * half, s = 8 * j + 2 * i;
-                float p[2], a[2];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const bool low = s + x <= t;
-                    const float M = low ? expf((sm.out.g[t] - sm.out.g[s + x]) + (sm.out.gl[t] - sm.out.gl[s + x])) : 0.f;
-                    p[x] = cq[j][2 * half + x] * M;
-                    a[x] = s + x < t ? ck[j][2 * half + x] * M : 0.f;
-                    sm.a[t][s + x] = a[x];
-                    sm.ab[t][s + x] = a[x] * sm.out.beta[s + x];
-                }
+        for (int half = 0; half < 2; ++half) {
+            const int t = 16 * rt + g + 8 * half, s = 8 * j + 2 * i;
+            float x[2] = {0.f, 0.f};
+            if (j <= 2 * rt + 1) {
+                const int last = isq ? t : t - 1;  // P has its diagonal, Ah has not
+                const float m0 = exp2f((gt[half] - gs.x) + (gtl[half] - gsl.x));
+                const float m1 = exp2f((gt[half] - gs.y) + (gtl[half] - gsl.y));
+                x[0] = s <= last ? acc[j][2 * half] * m0 : 0.f;  // (above the diagonal m may be infinite)
+                x[1] = s + 1 <= last ? acc[j][2 * half + 1] * m1 : 0.f;
+            }
+            if (isq) {
                 uint32_t hi, lo;
-                split(p[0], p[1], hi, lo);
+                split(x[0], x[1], hi, lo);
                 const uint32_t at = piece<128>(t, j) + 4 * i;
                 *reinterpret_cast<uint32_t*>(sm.out.img[2] + at) = hi;
                 *reinterpret_cast<uint32_t*>(sm.out.img[3] + at) = lo;
+            } else {
+                *reinterpret_cast<float2*>(&sm.a[t][s]) = make_float2(x[0], x[1]);
             }
         }
     }
     __syncthreads();
-    if (tid < kC) {
-        float N[kC];
-        N[0] = 0.f;
+    if (tid < kC) {  // blocks of 16: column tid
+        const int r0 = tid & ~15, sl = tid & 15;
+        float bN[16];
+        bN[0] = 0.f;
+        sm.n[r0][tid] = 0.f;
 #pragma unroll
-        for (int t = 1; t < kC; ++t) {
-            float x0 = sm.a[t][tid], x1 = 0.f, x2 = 0.f, x3 = 0.f;
+        for (int t = 1; t < 16; ++t) {
+            float x0 = sm.a[r0 + t][tid], x1 = 0.f;
 #pragma unroll
             for (int r = 0; r < t; r += 4) {
-                const float4 y = *reinterpret_cast<const float4*>(&sm.ab[t][r]);
-                x0 = fmaf(-y.x, N[r], x0);
-                if (r + 1 < t) x1 = fmaf(-y.y, N[r + 1], x1);
-                if (r + 2 < t) x2 = fmaf(-y.z, N[r + 2], x2);
-                if (r + 3 < t) x3 = fmaf(-y.w, N[r + 3], x3);
+                const float4 y = *reinterpret_cast<const float4*>(&sm.a[r0 + t][r0 + r]);
+                x0 = fmaf(-y.x, bN[r], x0);
+                if (r + 1 < t) x1 = fmaf(-y.y, bN[r + 1], x1);
+                if (r + 2 < t) x0 = fmaf(-y.z, bN[r + 2], x0);
+                if (r + 3 < t) x1 = fmaf(-y.w, bN[r + 3], x1);
             }
-            N[t] = tid < t ? (x0 + x1) + (x2 + x3) : 0.f;
+            const float x = t > sl ? x0 + x1 : 0.f;
+            sm.n[r0 + t][tid] = x;
+            bN[t] = beta[r0 + t] * x;
         }
+    } else if (tid < 2 * kC) {  // the blocks right of the diagonal that the last join reads
+        const int r0 = (tid >> 5 & 1) * 32, t = r0 + (tid >> 1 & 15), s = r0 + 16 + 8 * (tid & 1);
+        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(&sm.n[t][s]) = z;
+        *reinterpret_cast<float4*>(&sm.n[t][s + 4]) = z;
+    }
+    __syncthreads();
+    const auto join = [&](auto steps, int r0, int tr, int sc, bool on) {  // halves of `half` rows from r0
+        constexpr int half = 16 * decltype(steps)::value;
+        float y[4] = {};
+        const auto put = [&] {
+            if (on) {
+                *reinterpret_cast<float2*>(&sm.n[tr + g][sc + 2 * i]) = make_float2(y[0], y[1]);
+                *reinterpret_cast<float2*>(&sm.n[tr + g + 8][sc + 2 * i]) = make_float2(y[2], y[3]);
+            }
+            __syncthreads();
+        };
+        if (on) {
+            const float2 y0 = *reinterpret_cast<const float2*>(&sm.a[tr + g][sc + 2 * i]);
+            const float2 y1 = *reinterpret_cast<const float2*>(&sm.a[tr + g + 8][sc + 2 * i]);
+            y[0] = y0.x;
+            y[1] = y0.y;
+            y[2] = y1.x;
+            y[3] = y1.y;
+            take<half / 16>(y, sm.a, sm.n, beta, tr, sc, r0, lane);
+        }
+        put();
+        if (on) take<half / 16>(y, sm.n, sm.n, beta, tr, sc, r0 + half, lane);
+        __syncthreads();
+        put();
+    };
+    join(std::integral_constant<int, 1>(), 32 * (warp & 1), 32 * (warp & 1) + 16, 32 * (warp & 1) + 8 * (warp >> 1 & 1),
+         warp < 4);
+    join(std::integral_constant<int, 2>(), 0, 32 + 16 * (warp & 1), 8 * (warp >> 1), true);
+    {  // N as two images: two pieces of a row per thread, zeros above the blocks of 16 on the diagonal
+        const int t = tid >> 2, p0 = 2 * (tid & 3);
 #pragma unroll
-        for (int t = 0; t < kC; ++t) {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(N[t]);
-            const uint32_t at = piece<128>(t, tid >> 3) + 2 * (tid & 7);
-            *reinterpret_cast<__nv_bfloat16*>(sm.out.img[0] + at) = hi;
-            *reinterpret_cast<__nv_bfloat16*>(sm.out.img[1] + at) = __float2bfloat16_rn(N[t] - __bfloat162float(hi));
+        for (int p = p0; p < p0 + 2; ++p) {
+            uint32_t w[8] = {};
+            if (p0 / 2 <= t / 16) {
+                const float4 x = *reinterpret_cast<const float4*>(&sm.n[t][8 * p]);
+                const float4 y = *reinterpret_cast<const float4*>(&sm.n[t][8 * p + 4]);
+                split(x.x, x.y, w[0], w[4]);
+                split(x.z, x.w, w[1], w[5]);
+                split(y.x, y.y, w[2], w[6]);
+                split(y.z, y.w, w[3], w[7]);
+            }
+            *reinterpret_cast<uint4*>(sm.out.img[0] + piece<128>(t, p)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(sm.out.img[1] + piece<128>(t, p)) = make_uint4(w[4], w[5], w[6], w[7]);
         }
     }
     __syncthreads();
@@ -774,7 +886,7 @@ struct GradTiles {
     unsigned char u[2][kC * E * 2], x[2][kC * E * 2];
     unsigned char S[2][E * D * 2];
     unsigned char dp[2][kC * kC * 2], E_[2][kC * kC * 2];
-    float coef[5][kC];  // e^G, e^{G_C - G}, beta, G, its low part
+    float coef[5][kC];  // e^G, e^{G_C - G}, beta, G / ln 2, its low part
     float db[kC], xr[kC], part[2][kC], dG[kC], red[2 * kGradWarps];
 };
 
@@ -902,7 +1014,7 @@ gdr_grad(Args A, const ChunkWs* ws, Saved in, int chunks) {
                     float pp[2], ee[2];
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const float M = s + y <= t ? expf((G[t] - G[s + y]) + (Gl[t] - Gl[s + y])) : 0.f;
+                        const float M = s + y <= t ? exp2f((G[t] - G[s + y]) + (Gl[t] - Gl[s + y])) : 0.f;
                         pp[y] = p[j][2 * half + y] * M;
                         ee[y] = s + y < t ? -x[j][2 * half + y] * M * beta[t] : 0.f;
                     }
