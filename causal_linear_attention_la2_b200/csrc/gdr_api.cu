@@ -347,7 +347,7 @@ la2_status la2_gdr_decode(const void* q, const void* k, const void* v, const flo
         return LA2_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool vec = e % 4 == 0 && aligned(states, 16);
-    const dim3 grid(B * H, vec ? 1 : cdiv(e, 32));
+    const dim3 grid(B * H, cdiv(e, la2::gdr::kStepUnits * (vec ? 4 : 1)));
     const auto go = [&](auto tag) {
         using Tin = decltype(tag);
         const Tin *qq = static_cast<const Tin*>(q), *kk = static_cast<const Tin*>(k), *vv = static_cast<const Tin*>(v);
@@ -374,11 +374,12 @@ la2_status la2_state_copy(float* states, const int* src, const int* dst, int n, 
     const bool vec = slot_elems % 4 == 0 && aligned(states, 16);
     const size_t item = vec ? 16 : 4;
     const long long page = vec ? slot_elems / 4 : slot_elems;
-    // slices of at most 64 KB of shared memory, so that three CTAs share an SM,
-    // down to 32 bytes of a page
+    // slices of at most 32 KB of shared memory, so that several CTAs share an SM
+    // and one reads while another writes, down to 32 bytes of a page
     int units = la2::gdr::kPoolThreads;
-    while (units > static_cast<int>(32 / item) && static_cast<size_t>(n) * units * item > (64u << 10)) units >>= 1;
-    const size_t smem = static_cast<size_t>(n) * (units * item + 2 * sizeof(int));
+    while (units > static_cast<int>(32 / item) && static_cast<size_t>(n) * units * item > (32u << 10)) units >>= 1;
+    const size_t smem = static_cast<size_t>(n) * (units * item + 2 * sizeof(int)) +
+                        (n_slots <= la2::gdr::kPoolTable ? n_slots * sizeof(int) : 0);
     const long long grid = (page + units - 1) / units;
     if (grid > INT_MAX) return LA2_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -8,7 +8,8 @@ namespace la2 {
 namespace gdr {
 
 constexpr int kStepThreads = 256;
-constexpr int kStepRows = 16;  // rows of the state per thread, at most
+constexpr int kStepUnits = 8;             // column units of a CTA
+constexpr int kStepRows = 128 / 32;       // rows of the state per thread, at most
 
 // One token of row b, head h (gdr_common.cuh).  Both products with the old
 // state, S^T k and S^T q, are taken in one pass while the state sits in
@@ -16,10 +17,12 @@ constexpr int kStepRows = 16;  // rows of the state per thread, at most
 //
 //   u = beta (v - a S^T k),   o = a S^T q + (k . q) u,   S' = a S + k u^T.
 //
-// The state is read and written once (2 d e words of a few flops each: bound
-// by memory bandwidth).  A CTA takes one (row, head) and up to 32 W columns
-// (W = 4: 16-byte loads, e % 4 == 0; W = 1 otherwise); the threads of a group
-// of cu hold one row's columns, the groups take rows in turn.
+// The state is read and written once (2 d e words of a few flops each: bound by
+// memory bandwidth), so what counts is how much of it is on its way: a CTA takes
+// eight column units (W = 4 floats, 16-byte loads, where e % 4 == 0; W = 1
+// otherwise) of one (row, head) with four rows per thread at d = 128, and eight
+// CTAs share an SM.  64 x 40 states of 128 x 128: 116 us with whole states of 256
+// threads (154 registers, one CTA per SM), 85 us with 512 threads.
 //
 // slots[b] outside 0 .. n_slots - 1, or listed for an earlier row already:
 // the row's output is zero and no state changes.
@@ -28,96 +31,102 @@ __global__ void __launch_bounds__(kStepThreads)
 gdr_step(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v,
          const float* __restrict__ g, const float* __restrict__ beta, float* state,
          const int* __restrict__ slots, int n_slots, float* __restrict__ out, int Hk, int H, int d, int e) {
+    constexpr int kWarps = kStepThreads / 32;
     __shared__ float ks[128], qs[128];
-    __shared__ float part[2][kStepThreads * W];
-    const int n = blockIdx.x, b = n / H, h = n % H, tid = threadIdx.x;
-    const int col0 = blockIdx.y * 32 * W;
-    const int cu = min(32, (e - col0) / W);  // column units of this CTA
-    const int groups = kStepThreads / cu, rg = tid / cu, col = col0 + tid % cu * W;
+    __shared__ __align__(16) float part[2][kWarps][kStepUnits * W];
+    const int n = blockIdx.x, b = n / H, h = n % H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cl = lane % kStepUnits, col = (blockIdx.y * kStepUnits + cl) * W;
+    const int i0 = 4 * warp + lane / kStepUnits;  // rows i0, i0 + 32, ..
+    const bool on = col < e;
     const int slot = slots ? slots[b] : b;
     bool live = slot >= 0 && slot < n_slots;
-    float* S = state + ((static_cast<size_t>(live ? slot : 0)) * H + h) * d * e;
+    float* S = state + ((static_cast<size_t>(live ? slot : 0)) * H + h) * d * e + col;
     float sv[kStepRows][W];
-    if (live) {
 #pragma unroll
-        for (int r = 0; r < kStepRows; ++r) {
-            const int i = rg + r * groups;
+    for (int r = 0; r < kStepRows; ++r) {
+        const int i = i0 + 32 * r;
 #pragma unroll
-            for (int w = 0; w < W; ++w) sv[r][w] = 0.f;
-            if (rg < groups && i < d) {
-                const float* row = S + static_cast<size_t>(i) * e + col;
-                if constexpr (W == 4) {
-                    const float4 x = *reinterpret_cast<const float4*>(row);
-                    sv[r][0] = x.x; sv[r][1] = x.y; sv[r][2] = x.z; sv[r][3] = x.w;
-                } else {
-                    sv[r][0] = row[0];
-                }
+        for (int w = 0; w < W; ++w) sv[r][w] = 0.f;
+        if (live && on && i < d) {
+            const float* row = S + static_cast<size_t>(i) * e;
+            if constexpr (W == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(row);
+                sv[r][0] = x.x; sv[r][1] = x.y; sv[r][2] = x.z; sv[r][3] = x.w;
+            } else {
+                sv[r][0] = row[0];
             }
         }
     }
-    const int hk = h / (H / Hk);
     if (tid < d) {
-        const size_t at = (static_cast<size_t>(b) * Hk + hk) * d + tid;
+        const size_t at = (static_cast<size_t>(b) * Hk + h / (H / Hk)) * d + tid;
         ks[tid] = to_float(k[at]);
         qs[tid] = to_float(q[at]);
     }
+    const float a = g ? expf(g[n]) : 1.f, bt = beta[n];
+    float vv[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) vv[w] = on ? to_float(v[static_cast<size_t>(n) * e + col + w]) : 0.f;
     int twice = 0;
     if (slots)
         for (int x = tid; x < b; x += kStepThreads) twice |= slots[x] == slot;
     live = !__syncthreads_or(twice) && live;
-    float* on = out + static_cast<size_t>(n) * e;
+    float* to = out + static_cast<size_t>(n) * e + col;
     if (!live) {
-        if (rg == 0)
+        if (on && tid < kStepUnits)
 #pragma unroll
-            for (int w = 0; w < W; ++w) on[col + w] = 0.f;
+            for (int w = 0; w < W; ++w) to[w] = 0.f;
         return;
     }
-    const float a = g ? expf(g[n]) : 1.f, bt = beta[n];
-    float pk[W], pq[W];
+    float pk[W], pq[W], ki[kStepRows], kq = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) pk[w] = pq[w] = 0.f;
 #pragma unroll
     for (int r = 0; r < kStepRows; ++r) {
-        const int i = rg + r * groups;
-        if (rg < groups && i < d) {
-            const float ki = ks[i], qi = qs[i];
+        const int i = i0 + 32 * r;
+        const float qi = i < d ? qs[i] : 0.f;
+        ki[r] = i < d ? ks[i] : 0.f;
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                pk[w] = fmaf(sv[r][w], ki, pk[w]);
-                pq[w] = fmaf(sv[r][w], qi, pq[w]);
-            }
+        for (int w = 0; w < W; ++w) {
+            pk[w] = fmaf(sv[r][w], ki[r], pk[w]);
+            pq[w] = fmaf(sv[r][w], qi, pq[w]);
         }
     }
+    for (int i = lane; i < d; i += 32) kq = fmaf(ks[i], qs[i], kq);
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-        part[0][tid * W + w] = pk[w];
-        part[1][tid * W + w] = pq[w];
-    }
-    float kq = 0.f;
-    for (int i = tid & 31; i < d; i += 32) kq = fmaf(ks[i], qs[i], kq);
     for (int m = 16; m; m >>= 1) kq += __shfl_xor_sync(0xffffffffu, kq, m);
+#pragma unroll
+    for (int m = kStepUnits; m < 32; m <<= 1)
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            pk[w] += __shfl_xor_sync(0xffffffffu, pk[w], m);
+            pq[w] += __shfl_xor_sync(0xffffffffu, pq[w], m);
+        }
+    if (lane < kStepUnits)
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            part[0][warp][cl * W + w] = pk[w];
+            part[1][warp][cl * W + w] = pq[w];
+        }
     __syncthreads();
     float u[W];
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         float sk = 0.f, sq = 0.f;
-        if (rg < groups)
-            for (int y = 0; y < groups; ++y) {
-                sk += part[0][(y * cu + tid % cu) * W + w];
-                if (rg == 0) sq += part[1][(y * cu + tid % cu) * W + w];
-            }
-        const float vv = rg < groups ? to_float(v[static_cast<size_t>(n) * e + col + w]) : 0.f;
-        u[w] = bt * (vv - a * sk);
-        if (rg == 0) on[col + w] = fmaf(a, sq, kq * u[w]);
+#pragma unroll
+        for (int y = 0; y < kWarps; ++y) {
+            sk += part[0][y][cl * W + w];
+            if (tid < kStepUnits) sq += part[1][y][cl * W + w];
+        }
+        u[w] = bt * (vv[w] - a * sk);
+        if (on && tid < kStepUnits) to[w] = fmaf(a, sq, kq * u[w]);
     }
 #pragma unroll
     for (int r = 0; r < kStepRows; ++r) {
-        const int i = rg + r * groups;
-        if (rg < groups && i < d) {
-            float* row = S + static_cast<size_t>(i) * e + col;
-            const float ki = ks[i];
+        const int i = i0 + 32 * r;
+        if (on && i < d) {
+            float* row = S + static_cast<size_t>(i) * e;
 #pragma unroll
-            for (int w = 0; w < W; ++w) sv[r][w] = fmaf(a, sv[r][w], ki * u[w]);
+            for (int w = 0; w < W; ++w) sv[r][w] = fmaf(a, sv[r][w], ki[r] * u[w]);
             if constexpr (W == 4) *reinterpret_cast<float4*>(row) = make_float4(sv[r][0], sv[r][1], sv[r][2], sv[r][3]);
             else row[0] = sv[r][0];
         }
@@ -129,11 +138,13 @@ gdr_step(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __rest
 // nothing; where a slot is the destination of several pairs the last one
 // counts.  Sources may be destinations of other pairs, so a CTA reads its
 // slice of every source into shared memory before it writes any: slices of
-// different CTAs never meet, and no order between CTAs is needed.  Each place
-// of a destination is written by one thread, in the pairs' order (all pairs of
-// one slot have the same dst % writers).
+// different CTAs never meet, and no order between CTAs is needed.  Which pair is
+// the last one of its destination a table of the slots says (pools of up to
+// kPoolTable slots); in larger pools each place of a destination is written by one
+// thread, in the pairs' order (all pairs of one slot have the same remainder by
+// the number of writers, a power of two).
 constexpr int kPoolThreads = 256;
-constexpr int kPoolMaxPairs = 4096;
+constexpr int kPoolMaxPairs = 4096, kPoolTable = 4096;
 
 // V: float4, or float where the page or the pool's address asks for it.
 // `units` V's of a page per slice, a power of two of at most kPoolThreads.
@@ -145,11 +156,15 @@ pool_copy(V* pool, const int* __restrict__ src, const int* __restrict__ dst, int
     V* buf = reinterpret_cast<V*>(pool_raw);                              // [n][units]
     int* ss = reinterpret_cast<int*>(buf + static_cast<size_t>(n) * units);  // [n]
     int* dd = ss + n;
+    int* last = dd + n;  // [n_slots], where the pool is small enough
+    const bool table = n_slots <= kPoolTable;
     const int tid = threadIdx.x, u = tid % units, w = tid / units, writers = kPoolThreads / units;
     for (int i = tid; i < n; i += kPoolThreads) {
         ss[i] = src[i];
         dd[i] = dst[i];
     }
+    if (table)
+        for (int i = tid; i < n_slots; i += kPoolThreads) last[i] = -1;
     __syncthreads();
     const long long at = static_cast<long long>(blockIdx.x) * units + u;
     const bool on = at < page;
@@ -162,12 +177,22 @@ pool_copy(V* pool, const int* __restrict__ src, const int* __restrict__ dst, int
             buf[i * units + u] = x;
         }
     }
+    if (table)
+        for (int i = tid; i < n; i += kPoolThreads)
+            if (dd[i] >= 0 && dd[i] < n_slots && ss[i] < n_slots) atomicMax(&last[dd[i]], i);
     __syncthreads();
-    if (on) {
-        for (int i = 0; i < n; ++i) {
+    if (!on) return;
+    if (table) {
+#pragma unroll 4
+        for (int i = w; i < n; i += writers) {
             const int t = dd[i];
-            if (t >= 0 && t < n_slots && ss[i] < n_slots && t % writers == w) pool[t * page + at] = buf[i * units + u];
+            if (t >= 0 && t < n_slots && last[t] == i) pool[t * page + at] = buf[i * units + u];
         }
+        return;
+    }
+    for (int i = 0; i < n; ++i) {
+        const int t = dd[i];
+        if (t >= 0 && t < n_slots && ss[i] < n_slots && (t & (writers - 1)) == w) pool[t * page + at] = buf[i * units + u];
     }
 }
 

@@ -598,10 +598,36 @@ def _same_device(device, **tensors) -> None:
             raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _need(t, name, shape, dtype, device) -> None:
+    """_check and the device, with the usual case decided in one expression."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous() and t.is_cuda:
+        return
+    _check(t, name, shape, dtype)
+    _same_device(device, **{name: t})
+
+
+class _On:
+    """The tensors' device made current for a call, where it is not already."""
+
+    def __init__(self, device):
+        if device.type != "cuda":
+            raise ValueError("the tensors must be CUDA tensors")
+        self._guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
 def _stream_on(stream, device) -> int:
     """The caller's stream, or the current stream of the tensors' device."""
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return int(s.cuda_stream)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return int(stream.cuda_stream)
 
 
 def _own_workspace(nbytes: int, device, stream, workspace):
@@ -611,15 +637,16 @@ def _own_workspace(nbytes: int, device, stream, workspace):
     that it runs on, so two calls on two streams, or two captured graphs, never
     share one; the allocator hands the memory on in stream order."""
     if workspace is not None:
-        if workspace.device != device:
-            raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+        _same_device(device, workspace=workspace)
         p, n = _workspace(nbytes, device, workspace)
         return p, n, workspace
     if nbytes <= 0:
         return 0, 0, None
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    with torch.cuda.stream(s):
+    if stream is None:
         buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        with torch.cuda.stream(stream):
+            buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return buf.data_ptr(), nbytes, buf
 
 
@@ -638,20 +665,20 @@ def _gdr_dims(q, v, layout):
 def _gdr_inputs(q, k, v, g, beta, layout, seq_lens, states):
     """Checks what both directions take; returns the sizes and the dtype code."""
     B, Hk, H, T, d, e = _gdr_dims(q, v, layout)
-    dt = _dtype_code(q)
-    _check(q, "q", _shape(layout, B, Hk, T, d), q.dtype)
-    _check(k, "k", _shape(layout, B, Hk, T, d), q.dtype)
-    _check(v, "v", _shape(layout, B, H, T, e), q.dtype)
+    dt, dev = _dtype_code(q), q.device
+    qk = q.shape
+    _need(q, "q", qk, q.dtype, dev)
+    _need(k, "k", qk, q.dtype, dev)
+    _need(v, "v", _shape(layout, B, H, T, e), q.dtype, dev)
     gate = (B, H, T) if layout == "bhtd" else (B, T, H)
-    _check(beta, "beta", gate, torch.float32)
+    _need(beta, "beta", gate, torch.float32, dev)
     if g is not None:
-        _check(g, "g", gate, torch.float32)
+        _need(g, "g", gate, torch.float32, dev)
     if seq_lens is not None:
-        _check(seq_lens, "seq_lens", (B,), torch.int32)
+        _need(seq_lens, "seq_lens", (B,), torch.int32, dev)
     for name, s in states.items():
         if s is not None:
-            _check(s, name, (B, H, d, e), torch.float32)
-    _same_device(q.device, k=k, v=v, g=g, beta=beta, seq_lens=seq_lens, **states)
+            _need(s, name, (B, H, d, e), torch.float32, dev)
     return B, Hk, H, T, d, e, dt
 
 
@@ -675,14 +702,14 @@ def la2_gdr_fwd(q, k, v, g, beta, layout: str = "bhtd", init_state=None, seq_len
                                         {"init_state": init_state, "final_state": final_state})
     odt, oc = _out_dtype(out_dtype)
     shape = _shape(layout, B, H, T, e)
-    with torch.cuda.device(q.device):
+    with _On(q.device):
         sp = _stream_on(stream, q.device)
         if out is None:
             out = (torch.empty if seq_lens is None else torch.zeros)(shape, dtype=odt, device=q.device)
-        _check(out, "out", shape, odt)
+        else:
+            _need(out, "out", shape, odt, q.device)
         if final_state is None and want_final:
             final_state = torch.empty((B, H, d, e), dtype=torch.float32, device=q.device)
-        _same_device(q.device, out=out)
         wp, wn, keep = _own_workspace(la2_gdr_workspace_bytes(B, Hk, H, T, d, e, dt, 0), q.device,
                                       stream, workspace)
         st = la2_gdr_fwd_raw(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), beta.data_ptr(),
@@ -703,12 +730,12 @@ def la2_gdr_bwd(q, k, v, g, beta, dout, layout: str = "bhtd", init_state=None, d
                                         {"init_state": init_state, "d_final_state": d_final_state,
                                          "d_init_state": d_init_state})
     odt, oc = _out_dtype(out_dtype)
-    _check(dout, "dout", _shape(layout, B, H, T, e), q.dtype)
+    _need(dout, "dout", v.shape, q.dtype, q.device)
     if dg is not None and g is None:
         raise ValueError("dg needs a gate g")
     gate = tuple(beta.shape)
     new = torch.empty if seq_lens is None else torch.zeros
-    with torch.cuda.device(q.device):
+    with _On(q.device):
         sp = _stream_on(stream, q.device)
         o = dict(dtype=odt, device=q.device)
         f = dict(dtype=torch.float32, device=q.device)
@@ -720,13 +747,10 @@ def la2_gdr_bwd(q, k, v, g, beta, dout, layout: str = "bhtd", init_state=None, d
             dg = new(gate, **f)
         if d_init_state is None and want_d_init:
             d_init_state = torch.empty((B, H, d, e), **f)
-        _check(dq, "dq", _shape(layout, B, Hk, T, d), odt)
-        _check(dk, "dk", _shape(layout, B, Hk, T, d), odt)
-        _check(dv, "dv", _shape(layout, B, H, T, e), odt)
-        _check(dbeta, "dbeta", gate, torch.float32)
-        if dg is not None:
-            _check(dg, "dg", gate, torch.float32)
-        _same_device(q.device, dout=dout, dq=dq, dk=dk, dv=dv, dg=dg, dbeta=dbeta)
+        for name, t, shape, dtype in (("dq", dq, q.shape, odt), ("dk", dk, q.shape, odt), ("dv", dv, v.shape, odt),
+                                      ("dbeta", dbeta, gate, torch.float32), ("dg", dg, gate, torch.float32)):
+            if t is not None:
+                _need(t, name, shape, dtype, q.device)
         wp, wn, keep = _own_workspace(la2_gdr_workspace_bytes(B, Hk, H, T, d, e, dt, 1), q.device,
                                       stream, workspace)
         st = la2_gdr_bwd_raw(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), beta.data_ptr(),
@@ -751,25 +775,26 @@ def la2_gdr_decode(q, k, v, g, beta, states, slots=None, out=None, stream=None) 
         raise ValueError("q and v must have 3 dimensions, states 4")
     B, Hk, d = q.shape
     H, e = v.shape[1:]
-    dt = _dtype_code(q)
-    _check(q, "q", (B, Hk, d), q.dtype)
-    _check(k, "k", (B, Hk, d), q.dtype)
-    _check(v, "v", (B, H, e), q.dtype)
-    _check(beta, "beta", (B, H), torch.float32)
+    dt, dev, n_slots = _dtype_code(q), q.device, states.shape[0]
+    if (Hk == 0 or H % Hk != 0) and H + Hk:
+        raise ValueError(f"{H} value heads are not a multiple of {Hk} key heads")
+    _need(q, "q", q.shape, q.dtype, dev)
+    _need(k, "k", q.shape, q.dtype, dev)
+    _need(v, "v", (B, H, e), q.dtype, dev)
+    _need(beta, "beta", (B, H), torch.float32, dev)
     if g is not None:
-        _check(g, "g", (B, H), torch.float32)
-    n_slots = states.shape[0]
-    _check(states, "states", (n_slots, H, d, e), torch.float32)
+        _need(g, "g", (B, H), torch.float32, dev)
+    _need(states, "states", (n_slots, H, d, e), torch.float32, dev)
     if slots is not None:
-        _check(slots, "slots", (B,), torch.int32)
+        _need(slots, "slots", (B,), torch.int32, dev)
     elif n_slots < B:
         raise ValueError(f"{B} sequences but {n_slots} slots")
-    with torch.cuda.device(q.device):
-        sp = _stream_on(stream, q.device)
+    with _On(dev):
+        sp = _stream_on(stream, dev)
         if out is None:
-            out = torch.empty((B, H, e), dtype=torch.float32, device=q.device)
-        _check(out, "out", (B, H, e), torch.float32)
-        _same_device(q.device, k=k, v=v, g=g, beta=beta, states=states, slots=slots, out=out)
+            out = torch.empty((B, H, e), dtype=torch.float32, device=dev)
+        else:
+            _need(out, "out", (B, H, e), torch.float32, dev)
         st = la2_gdr_decode_raw(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), beta.data_ptr(),
                                 states.data_ptr(), _ptr(slots), n_slots, out.data_ptr(), B, Hk, H,
                                 d, e, dt, sp)
@@ -784,16 +809,14 @@ def la2_state_copy(states, src, dst, stream=None) -> torch.Tensor:
     the pool do nothing; of several pairs with one destination the last counts.  Returns states."""
     if states.dim() < 1 or src.dim() != 1:
         raise ValueError("states must have a slot dimension, src and dst one dimension")
-    n = src.shape[0]
-    _check(states, "states", states.shape, torch.float32)
-    _check(src, "src", (n,), torch.int32)
-    _check(dst, "dst", (n,), torch.int32)
-    _same_device(states.device, src=src, dst=dst)
-    n_slots = states.shape[0]
-    with torch.cuda.device(states.device):
+    n, n_slots, dev = src.shape[0], states.shape[0], states.device
+    _need(states, "states", states.shape, torch.float32, dev)
+    _need(src, "src", (n,), torch.int32, dev)
+    _need(dst, "dst", (n,), torch.int32, dev)
+    with _On(dev):
         st = la2_state_copy_raw(states.data_ptr(), src.data_ptr(), dst.data_ptr(), n, n_slots,
                                 states.numel() // n_slots if n_slots else 0,
-                                _stream_on(stream, states.device))
+                                _stream_on(stream, dev))
     if st != LA2_OK:
         raise LA2Error(st, "la2_state_copy")
     return states

@@ -524,15 +524,17 @@ def test_state_copy(gpu, shape, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("spare", [0, 5000])
 @pytest.mark.parametrize("n,elems", [(257, 3), (1000, 16), (4096, 40), (4096, 9)])
-def test_state_copy_of_many_pairs(gpu, n, elems):
-    """A rotation of the whole pool, then one destination for all pairs."""
-    flat = torch.randn(n * elems + 1, device=gpu)
-    for pool in (flat[:n * elems].view(n, elems), flat[1:].view(n, elems)):
+def test_state_copy_of_many_pairs(gpu, n, elems, spare):
+    """A rotation of the first n slots, then one destination for all pairs; pools with and without a table of slots."""
+    N = n + spare
+    flat = torch.randn(N * elems + 1, device=gpu)
+    for pool in (flat[:N * elems].view(N, elems), flat[1:].view(N, elems)):
         i = torch.arange(n, dtype=torch.int32, device=gpu)
         before = pool.clone()
         L.la2_state_copy(pool, i, torch.roll(i, 1).contiguous())
-        assert torch.equal(pool[torch.roll(i, 1).long()], before)
+        assert torch.equal(pool[torch.roll(i, 1).long()], before[:n]) and torch.equal(pool[n:], before[n:])
         before = pool.clone()
         L.la2_state_copy(pool, i, torch.full_like(i, 5))
         before[5] = before[n - 1]
