@@ -86,6 +86,8 @@ bool set_smem_attrs() {
     return set_chunk_attrs<64>() && set_chunk_attrs<128>() &&
            set(reinterpret_cast<const void*>(la2::gdr::gdr_grad_rec<float>), sizeof(la2::gdr::GradSmem)) &&
            set(reinterpret_cast<const void*>(la2::gdr::gdr_grad_rec<__nv_bfloat16>), sizeof(la2::gdr::GradSmem)) &&
+           set(reinterpret_cast<const void*>(la2::gdr::gdr_step_bulk<float>), la2::gdr::bulk_smem_bytes(128, 128)) &&
+           set(reinterpret_cast<const void*>(la2::gdr::gdr_step_bulk<__nv_bfloat16>), la2::gdr::bulk_smem_bytes(128, 128)) &&
            set(reinterpret_cast<const void*>(la2::gdr::pool_copy<float4>), 200 << 10) &&
            set(reinterpret_cast<const void*>(la2::gdr::pool_copy<float>), 200 << 10);
 }
@@ -347,11 +349,21 @@ la2_status la2_gdr_decode(const void* q, const void* k, const void* v, const flo
         return LA2_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool vec = e % 4 == 0 && aligned(states, 16);
-    const dim3 grid(B * H, cdiv(e, la2::gdr::kStepUnits * (vec ? 4 : 1)));
+    const long long blocks = static_cast<long long>(B) * H * cdiv(e, la2::gdr::kStepUnits * (vec ? 4 : 1));
+    if (blocks > INT_MAX) return LA2_ERR_UNSUPPORTED;
+    const unsigned grid = static_cast<unsigned>(blocks);
+    // From four states per SM on the pipelined kernel (KERNELTIMES)
+    constexpr int kSMs = 148;
+    const bool bulk = vec && n_slots > 0 && static_cast<long long>(B) * H >= 4 * kSMs && d * e >= 4096;
+    int* status = nullptr;
+    if (bulk && (!device_setup() || !(status = la2::status_word()))) return LA2_ERR_CUDA;
     const auto go = [&](auto tag) {
         using Tin = decltype(tag);
         const Tin *qq = static_cast<const Tin*>(q), *kk = static_cast<const Tin*>(k), *vv = static_cast<const Tin*>(v);
-        if (vec)
+        if (bulk)
+            la2::gdr::gdr_step_bulk<Tin><<<kSMs, la2::gdr::kBulkThreads, la2::gdr::bulk_smem_bytes(d, e), s>>>(
+                qq, kk, vv, g, beta, states, slots, n_slots, out, B * H, Hk, H, d, e, status);
+        else if (vec)
             la2::gdr::gdr_step<Tin, 4><<<grid, la2::gdr::kStepThreads, 0, s>>>(qq, kk, vv, g, beta, states, slots,
                                                                              n_slots, out, Hk, H, d, e);
         else

@@ -3,6 +3,7 @@
 // sequence, and the copies that fork, move and clear slots.
 #pragma once
 #include "gdr_common.cuh"
+#include "ptx_sm100.cuh"
 
 namespace la2 {
 namespace gdr {
@@ -27,15 +28,16 @@ constexpr int kStepRows = 128 / 32;       // rows of the state per thread, at mo
 // slots[b] outside 0 .. n_slots - 1, or listed for an earlier row already:
 // the row's output is zero and no state changes.
 template <typename Tin, int W>
-__global__ void __launch_bounds__(kStepThreads)
+__global__ void __launch_bounds__(kStepThreads, 4)
 gdr_step(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v,
          const float* __restrict__ g, const float* __restrict__ beta, float* state,
          const int* __restrict__ slots, int n_slots, float* __restrict__ out, int Hk, int H, int d, int e) {
     constexpr int kWarps = kStepThreads / 32;
     __shared__ float ks[128], qs[128];
     __shared__ __align__(16) float part[2][kWarps][kStepUnits * W];
-    const int n = blockIdx.x, b = n / H, h = n % H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int cl = lane % kStepUnits, col = (blockIdx.y * kStepUnits + cl) * W;
+    const int blocks = (e + kStepUnits * W - 1) / (kStepUnits * W);  // column blocks of one state run side by side
+    const int n = blockIdx.x / blocks, b = n / H, h = n % H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cl = lane % kStepUnits, col = (blockIdx.x % blocks * kStepUnits + cl) * W;
     const int i0 = 4 * warp + lane / kStepUnits;  // rows i0, i0 + 32, ..
     const bool on = col < e;
     const int slot = slots ? slots[b] : b;
@@ -131,6 +133,163 @@ gdr_step(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __rest
             else row[0] = sv[r][0];
         }
     }
+}
+
+// The same step for many states: a CTA per SM walks over its (row, head)s with
+// three whole states in shared memory, one being loaded (bulk copy), one worked
+// on, one being stored, so that the memory system always has 64 KB to bring and
+// 64 KB to take per SM whatever the arithmetic in between waits for.  States are
+// 16-byte aligned, e a multiple of 4.  Each thread keeps its part of the state in
+// registers between the two products and the update.
+constexpr int kBulkThreads = 512;
+constexpr int kBulkRows = 8;
+constexpr int kBulkStages = 3;
+
+struct BulkSmem {
+    float part[2][kBulkThreads * 4];
+    float ks[2][128], qs[2][128];
+    float u[128], kq;
+    unsigned long long full[kBulkStages];
+};
+
+inline size_t bulk_smem_bytes(int d, int e) {
+    return sizeof(BulkSmem) + 128 + static_cast<size_t>(kBulkStages) * d * e * sizeof(float);
+}
+
+template <typename Tin>
+__global__ void __launch_bounds__(kBulkThreads, 1)
+gdr_step_bulk(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v,
+              const float* __restrict__ g, const float* __restrict__ beta, float* state,
+              const int* __restrict__ slots, int n_slots, float* __restrict__ out, int total, int Hk, int H, int d,
+              int e, int* status) {
+    extern __shared__ __align__(128) unsigned char bulk_raw[];
+    BulkSmem& sm = *reinterpret_cast<BulkSmem*>(bulk_raw);
+    float* stage = reinterpret_cast<float*>(bulk_raw + (sizeof(BulkSmem) + 127) / 128 * 128);
+    const int tid = threadIdx.x, page = d * e;
+    const uint32_t bytes = static_cast<uint32_t>(page) * 4, full = smem_u32(sm.full);
+    const int cu = e / 4, groups = kBulkThreads / cu, rg = tid / cu, ju = tid % cu;
+    const bool on = rg < groups;
+    const int mine = (total - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    const auto index = [&](int y) { return static_cast<int>(blockIdx.x) + y * static_cast<int>(gridDim.x); };
+    const auto slot_of = [&](int y) {
+        const int b = index(y) / H;
+        return slots ? slots[b] : b;
+    };
+    const auto load = [&](int y, int slot) {  // one thread
+        if (slot < 0 || slot >= n_slots) slot = 0;  // read and dropped: a pool without slots is not launched
+        const uint32_t bar = full + 8 * (y % kBulkStages);
+        mbar_arrive_expect_tx(bar, bytes);
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         smem_u32(stage + static_cast<size_t>(y % kBulkStages) * page)),
+                     "l"(state + (static_cast<size_t>(slot) * H + index(y) % H) * page), "r"(bytes), "r"(bar)
+                     : "memory");
+    };
+    const auto row = [&](int y) {  // this thread's element of k or q of one state
+        if (tid >= 2 * d || y >= mine) return 0.f;
+        const int n = index(y), i = tid < d ? tid : tid - d;
+        const size_t at = (static_cast<size_t>(n / H) * Hk + n % H / (H / Hk)) * d + i;
+        return to_float(tid < d ? k[at] : q[at]);
+    };
+    const auto keep = [&](int y, float x) {
+        if (tid < d) sm.ks[y & 1][tid] = x;
+        else if (tid < 2 * d) sm.qs[y & 1][tid - d] = x;
+    };
+    if (tid == 0) {
+        for (int s = 0; s < kBulkStages; ++s) mbar_init(full + 8 * s, 1);
+        fence_mbar_init();
+        for (int y = 0; y < 2 && y < mine; ++y) load(y, slot_of(y));
+    }
+    keep(0, row(0));
+    __syncthreads();
+    for (int y = 0; y < mine; ++y) {
+        const int n = index(y), b = n / H, s = y % kBulkStages;
+        const float next = row(y + 1);
+        const int slot = slot_of(y), ahead = y + 2 < mine && tid == 0 ? slot_of(y + 2) : 0;
+        const float a = g ? expf(g[n]) : 1.f, bt = beta[n];
+        int twice = 0;
+        if (slots)
+            for (int x = tid; x < b; x += kBulkThreads) twice |= slots[x] == slot;
+        const float vv = tid < e ? to_float(v[static_cast<size_t>(n) * e + tid]) : 0.f;
+        const bool ok = mbar_wait(full + 8 * s, (y / kBulkStages) & 1);
+        if (!__syncthreads_and(ok)) {
+            if (tid == 0) atomicCAS(status, 0, 5 | (230 << 8));
+            break;
+        }
+        float4* S = reinterpret_cast<float4*>(stage + static_cast<size_t>(s) * page);
+        const float *ks = sm.ks[y & 1], *qs = sm.qs[y & 1];
+        float4 sv[kBulkRows];
+        float4 pk = make_float4(0.f, 0.f, 0.f, 0.f), pq = pk;
+#pragma unroll
+        for (int r = 0; r < kBulkRows; ++r) {
+            const int i = rg + r * groups;
+            if (on && i < d) {
+                sv[r] = S[i * cu + ju];
+                const float ki = ks[i], qi = qs[i];
+                pk.x = fmaf(sv[r].x, ki, pk.x);
+                pk.y = fmaf(sv[r].y, ki, pk.y);
+                pk.z = fmaf(sv[r].z, ki, pk.z);
+                pk.w = fmaf(sv[r].w, ki, pk.w);
+                pq.x = fmaf(sv[r].x, qi, pq.x);
+                pq.y = fmaf(sv[r].y, qi, pq.y);
+                pq.z = fmaf(sv[r].z, qi, pq.z);
+                pq.w = fmaf(sv[r].w, qi, pq.w);
+            }
+        }
+        if (on) {
+            reinterpret_cast<float4*>(sm.part[0])[tid] = pk;
+            reinterpret_cast<float4*>(sm.part[1])[tid] = pq;
+        }
+        if (tid >= kBulkThreads - 32) {  // k . q
+            float kq = 0.f;
+            for (int i = tid & 31; i < d; i += 32) kq = fmaf(ks[i], qs[i], kq);
+#pragma unroll
+            for (int m = 16; m; m >>= 1) kq += __shfl_xor_sync(0xffffffffu, kq, m);
+            if (tid == kBulkThreads - 1) sm.kq = kq;
+        }
+        const bool live = !__syncthreads_or(twice) && slot >= 0 && slot < n_slots;
+        if (tid < e) {
+            float sk = 0.f, sq = 0.f;
+            const float kq = sm.kq;
+#pragma unroll 16
+            for (int x = 0; x < groups; ++x) {
+                sk += sm.part[0][x * e + tid];
+                sq += sm.part[1][x * e + tid];
+            }
+            const float u = bt * (vv - a * sk);
+            sm.u[tid] = u;
+            out[static_cast<size_t>(n) * e + tid] = live ? fmaf(a, sq, kq * u) : 0.f;
+        }
+        keep(y + 1, next);
+        __syncthreads();
+        if (live && on) {
+            const float4 u = reinterpret_cast<const float4*>(sm.u)[ju];
+#pragma unroll
+            for (int r = 0; r < kBulkRows; ++r) {
+                const int i = rg + r * groups;
+                if (i < d) {
+                    const float ki = ks[i];
+                    S[i * cu + ju] = make_float4(fmaf(a, sv[r].x, ki * u.x), fmaf(a, sv[r].y, ki * u.y),
+                                                 fmaf(a, sv[r].z, ki * u.z), fmaf(a, sv[r].w, ki * u.w));
+                }
+            }
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0) {
+            if (live)
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                                 state + (static_cast<size_t>(slot) * H + n % H) * page),
+                             "r"(smem_u32(S)), "r"(bytes)
+                             : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            if (y + 2 < mine) {
+                // its stage is the one that was stored a step ago
+                asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                load(y + 2, ahead);
+            }
+        }
+    }
+    if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // Pool copies: for every pair i, slot dst[i] takes what slot src[i] held BEFORE

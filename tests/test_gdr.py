@@ -467,6 +467,29 @@ def test_decode_step(gpu, dtype, d, e, Hk, H, gate):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,Hk,H,d,e,dtype", [(40, 20, 20, 128, 128, BF16), (75, 4, 8, 64, 64, F32), (43, 7, 14, 100, 44, BF16),
+                                              (150, 4, 4, 128, 36, F32)])
+def test_decode_of_many_states(gpu, B, Hk, H, d, e, dtype):
+    """More states than the GPU holds at a time, padded and repeated slots among them."""
+    N = B + 3
+    x = R.make(B, Hk, H, 1, d, e, dtype, 3)
+    one = {n: x[n][:, :, 0].contiguous() for n in ("q", "k", "v", "g", "beta")}
+    pool = torch.randn(N, H, d, e, generator=torch.Generator().manual_seed(1))
+    slots = torch.randperm(N, generator=torch.Generator().manual_seed(2))[:B].to(torch.int32)
+    slots[3], slots[B // 2], slots[B - 1] = -1, slots[1], N
+    dead = [3, B // 2, B - 1]
+    live = [i for i in range(B) if i not in dead]
+    dp, dev = pool.to(gpu), {n: t.to(gpu) for n, t in one.items()}
+    o = L.la2_gdr_decode(dev["q"], dev["k"], dev["v"], dev["g"], dev["beta"], dp, slots=slots.to(gpu))
+    at = slots[live].long()
+    ro, rS = R.decode(*(one[n][live] for n in ("q", "k", "v", "g", "beta")), pool[at])
+    _close(o[live].double().cpu(), ro, 1e-5, name="o")
+    _close(dp[at].double().cpu(), rS, 1e-5, name="state")
+    rest = [i for i in range(N) if i not in set(at.tolist())]
+    assert torch.equal(dp[rest].cpu(), pool[rest]) and not o[dead].any()
+
+
+@pytest.mark.gpu
 def test_decode_same_slot_twice(gpu):
     """The first row that names a slot has it; later ones give zeros."""
     x = R.make(4, 1, 2, 1, 64, 64, F32, 2)
