@@ -11,6 +11,7 @@
 
 #include "gdr_chunk.cuh"
 #include "gdr_common.cuh"
+#include "gdr_grad_sm100.cuh"
 #include "gdr_rec.cuh"
 #include "gdr_walk_sm100.cuh"
 #include "la2.h"
@@ -57,6 +58,7 @@ bool row_map(CUtensorMap* m, const void* ptr, int B, int heads, int T, int width
 }
 
 constexpr int kMaxDevices = 64;
+constexpr int kSMs = 148;
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -79,7 +81,7 @@ bool set_chunk_attrs() {
            set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kSave>), sizeof(walk::Smem<D>)) &&
            set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kBackward>), sizeof(walk::Smem<D>)) &&
            set(reinterpret_cast<const void*>(gdr_grad<D, 64>), sizeof(GradTiles<D, 64>)) &&
-           set(reinterpret_cast<const void*>(gdr_grad<D, 128>), sizeof(GradTiles<D, 128>));
+           set(reinterpret_cast<const void*>(grad::gdr_grad_tc<D>), sizeof(grad::Smem<D>));
 }
 
 bool set_smem_attrs() {
@@ -155,7 +157,7 @@ bool by_chunks(la2_dtype dtype, int d, int e) {
 }
 
 struct ChunkLayout {
-    size_t prep, S0, dS1, W, X, bytes;
+    size_t prep, S0, dS1, W, X, dot, sums, bytes;
 };
 
 ChunkLayout chunk_ws(long long BH, int T, int d, int e, bool bwd) {
@@ -166,10 +168,12 @@ ChunkLayout chunk_ws(long long BH, int T, int d, int e, bool bwd) {
         const size_t pages = align256(seqs * chunks * 2 * d * e * 2);  // two bf16 parts
         const size_t rows = align256(seqs * T * e * sizeof(float));
         w.S0 = at;
-        w.dS1 = w.S0 + pages;
+        w.dS1 = w.S0 + pages + align256(seqs * 2 * d * e * 2);
         w.W = w.dS1 + pages;
         w.X = w.W + rows;
-        at = w.X + rows;
+        w.dot = w.X + rows;
+        w.sums = w.dot + align256(seqs * chunks * 4 * sizeof(float));
+        at = w.sums + (e == 128 ? static_cast<size_t>(kSMs) * (64 << 10) : 0);
     }
     w.bytes = at;
     return w;
@@ -187,6 +191,21 @@ la2_status walk_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::S
     if (!status) return LA2_ERR_CUDA;
     walk::gdr_walk<D, kMode><<<A.B * A.H, walk::kThreads, sizeof(walk::Smem<D>), stream>>>(
         A, cw, sv, chunks, mk, mq, mv, status);
+    return LA2_OK;
+}
+
+template <int D>
+la2_status grad_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::Saved& sv, int chunks, cudaStream_t stream) {
+    using namespace la2::gdr;
+    CUtensorMap mk, mq, md;
+    if (!row_map(&mk, A.k, A.B, A.Hk, A.T, D, A.bthd) || !row_map(&mq, A.q, A.B, A.Hk, A.T, D, A.bthd) ||
+        !row_map(&md, A.dout, A.B, A.H, A.T, grad::kE, A.bthd))
+        return LA2_ERR_CUDA;
+    int* status = la2::status_word();
+    if (!status) return LA2_ERR_CUDA;
+    const int units = A.B * A.Hk * chunks;
+    grad::gdr_grad_tc<D><<<units < kSMs ? units : kSMs, grad::kThreads, sizeof(grad::Smem<D>), stream>>>(
+        A, cw, sv, chunks, units * (A.H / A.Hk), mk, mq, md, status);
     return LA2_OK;
 }
 
@@ -218,6 +237,8 @@ la2_status chunk_backward(const Args& A, char* ws, cudaStream_t stream) {
     sv.dS1 = reinterpret_cast<__nv_bfloat16*>(ws + w.dS1);
     sv.W = reinterpret_cast<float*>(ws + w.W);
     sv.X = reinterpret_cast<float*>(ws + w.X);
+    sv.dot = reinterpret_cast<float*>(ws + w.dot);
+    sv.sums = reinterpret_cast<float*>(ws + w.sums);
     const int walks = A.B * A.H * (A.e / kWalkCols);
     if (chunks > 0) {
         gdr_prep<D><<<static_cast<unsigned>(A.B) * A.H * chunks, kPrepThreads, sizeof(PrepSmem<D>), stream>>>(A, cw, chunks);
@@ -226,14 +247,14 @@ la2_status chunk_backward(const Args& A, char* ws, cudaStream_t stream) {
     if (on_tc(A)) {
         la2_status st = walk_tc<D, walk::kSave>(A, cw, sv, chunks, stream);
         if (st == LA2_OK) st = walk_tc<D, walk::kBackward>(A, cw, sv, chunks, stream);
-        if (st != LA2_OK) return st;
+        if (st == LA2_OK) st = grad_tc<D>(A, cw, sv, chunks, stream);
+        return st == LA2_OK ? launched() : st;
     } else {
         gdr_chain_rev<D><<<walks, kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, sv, chunks);
     }
     if (chunks > 0) {
         const unsigned grid = static_cast<unsigned>(A.B) * A.Hk * chunks;
-        if (A.e == 64) gdr_grad<D, 64><<<grid, 32 * kGradWarps, sizeof(GradTiles<D, 64>), stream>>>(A, cw, sv, chunks);
-        else gdr_grad<D, 128><<<grid, 32 * kGradWarps, sizeof(GradTiles<D, 128>), stream>>>(A, cw, sv, chunks);
+        gdr_grad<D, 64><<<grid, 32 * kGradWarps, sizeof(GradTiles<D, 64>), stream>>>(A, cw, sv, chunks);
     }
     return launched();
 }
@@ -353,7 +374,6 @@ la2_status la2_gdr_decode(const void* q, const void* k, const void* v, const flo
     if (blocks > INT_MAX) return LA2_ERR_UNSUPPORTED;
     const unsigned grid = static_cast<unsigned>(blocks);
     // From four states per SM on the pipelined kernel (KERNELTIMES)
-    constexpr int kSMs = 148;
     const bool bulk = vec && n_slots > 0 && static_cast<long long>(B) * H >= 4 * kSMs && d * e >= 4096;
     int* status = nullptr;
     if (bulk && (!device_setup() || !(status = la2::status_word()))) return LA2_ERR_CUDA;

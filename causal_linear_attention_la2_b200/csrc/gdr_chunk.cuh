@@ -431,8 +431,11 @@ constexpr int kWalkCols = 64;
 // d / 8 blocks of [e][8] (one value column's 16 bytes next to the next one's);
 // the rows w and x as fp32 [B*H][T][e].
 struct Saved {
-    __nv_bfloat16 *S0, *dS1;  // [B*H][chunks][2][d / 8][e][8]
+    __nv_bfloat16 *S0;   // [B*H][chunks + 1][2][d / 8][e][8], the last one after the last chunk
+    __nv_bfloat16 *dS1;  // [B*H][chunks][2][d / 8][e][8]
     float *W, *X;
+    float* dot;          // [B*H][chunks][4]: <dS1, S1> in four parts (e = 128)
+    float* sums;         // gdr_grad_tc's sums over the value heads of a key head, 64 KB per CTA
 };
 
 template <int D>
@@ -581,7 +584,7 @@ gdr_chain(Args A, const ChunkWs* ws, Saved out, int chunks) {
                 }
             }
         }
-        if (kSave) save_state<D>(S, out.S0 + (static_cast<size_t>(n) * chunks + c) * 2 * page, A.e, col + g, lane);
+        if (kSave) save_state<D>(S, out.S0 + (static_cast<size_t>(n) * (chunks + 1) + c) * 2 * page, A.e, col + g, lane);
         // Z = V - e^G (K S0), then -beta Z as the operand of N
         uint32_t fh[4][4], fl[4][4];
 #pragma unroll
@@ -927,7 +930,7 @@ gdr_grad(Args A, const ChunkWs* ws, Saved in, int chunks) {
         load_tile<E, kThreads>(dt, A, A.dout, b, h, A.H, E, 0, t0, len);
         load_bytes<kThreads>(smem_addr(sm.coef), ws[cn].eg, 3 * kC * 4);
         load_bytes<kThreads>(smem_addr(sm.coef[3]), ws[cn].g, 2 * kC * 4);
-        load_state(in.S0 + cn * 2 * page);
+        load_state(in.S0 + (seq * (chunks + 1) + c) * 2 * page);
         // rows of w, x, v: u and x as two parts, dbeta and the row sums of x (w - v)
         for (int t = warp; t < kC; t += kGradWarps) {
             constexpr int kPer = E / 32;
@@ -1116,7 +1119,7 @@ gdr_grad(Args A, const ChunkWs* ws, Saved in, int chunks) {
         __syncthreads();
         float dot = 0.f;
         {
-            const uint32_t* s0 = reinterpret_cast<const uint32_t*>(in.S0 + cn * 2 * page);
+            const uint32_t* s0 = reinterpret_cast<const uint32_t*>(in.S0 + (seq * (chunks + 1) + c) * 2 * page);
             constexpr int kWords = D / 2;
             for (int y = tid; y < E * kWords; y += kThreads) {  // word y & 3 of piece y / 4 / E of column r
                 const int r = y / 4 % E, x = y / 4 / E * 4 + y % 4;

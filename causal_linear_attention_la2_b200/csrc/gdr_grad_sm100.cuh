@@ -1,0 +1,577 @@
+// gdr_grad_sm100.cuh -- dq, dk, dv, dg and dbeta of the gated delta rule for
+// e = 128 on the tcgen05 tensor cores, all chunks independently, from what the
+// walks left (gdr_walk_sm100.cuh): per chunk the state S0 before it, the gradient
+// dS1 of the state after it, <dS1, S1>, and the rows w and x.  With U = beta W:
+//
+//   dP = M o (dO U^T),   E_ts = -beta_t M_ts (x_t . u_s)  (s < t)
+//   dq^T = S0 dO^T diag(e^G) + K^T dP^T
+//   dk^T = -S0 X^T diag(beta e^G) + K^T E^T + K^T E + Q^T dP + dS1 U^T diag(e^{G_C - G})
+//   dv = beta x,   dbeta_t = x_t . w_t
+//   dL/dG_t = q_t . dq_t - v_t . dv_t, and <dS1, S1> more in the chunk's last row;
+//   dg: sums of dL/dG from a row to the chunk's end.
+// (dL/dG_t: gating position t scales the state, which dq_t and the outputs read,
+// and nothing but the state enters v_t . dv_t = beta_t v_t . x_t; of the four terms
+// of gdr_rec.cuh's form k_t . row_t - k_t . col_t is -beta_t x_t . v_t.)
+//
+// The products run with d on the TMEM lanes (M = d; 128 rows for dP and E, which
+// are made together as [dO; X] U^T).  The scales of single rows are applied when
+// the accumulators are read.  Every formed operand is a high and a low bf16 part.
+//
+// One persistent CTA per SM walks over (chunk, key head, value head) items.  Per
+// item it reads 2 x 64 KB of states, 64 KB of w and x and 64 KB of rows and writes
+// 80 KB (d = 128), which is what bounds it; warps:
+//   0      loads: dO and factors, K and Q, the four state parts through a ring
+//   1      MMAs
+//   2      TMEM allocation
+//   4-11   epilogues: dP and E as operands; dq, dk, q . dq
+//   12-15  w, x -> operands U, X; dv, dbeta, x . v
+// Waits are bounded as in gdr_walk_sm100.cuh.
+#pragma once
+#include "gdr_walk_sm100.cuh"
+
+namespace la2 {
+namespace gdr {
+namespace grad {
+
+using walk::arrive;
+using walk::bulk_load;
+using walk::elect;
+using walk::Waiter;
+
+constexpr int kE = 128;
+constexpr int kThreads = 512;
+constexpr int kEpiWarps = 8, kRowWarps = 4;
+constexpr int kFactors = 9;  // eg .. gl of ChunkWs
+
+enum Bar { kRows = 0, kRowsFree, kKQ, kKQFree, kXU, kXUFree, kRing, kRingFree = kRing + 2, kPE = kRingFree + 2,
+           kPEFull, kDone, kFree, kSums, kRaw = kSums + 2, kEpi, kEnd, kBars };
+
+template <int D>
+struct Smem {
+    // 64 columns of e: rows of dO, X hi, X lo (the operand [dO; X hi] and, one tile on, [X hi; X lo])
+    unsigned char dx[kE / 64][3][kC * 128];
+    unsigned char u[kE / 64][2][kC * 128];   // U hi, U lo
+    unsigned char k[D / 64][kC * 128], q[D / 64][kC * 128];
+    unsigned char pe[2][2][kC * 128];        // hi, lo: rows of dP, rows of E
+    unsigned char ring[2][D * kE * 2];       // one part of a state: [d / 8][e][8]
+    float f[kFactors][kC];                   // factors of the epilogue's item
+    float dbeta[2][kC], xv[2][kC];           // row sums, by item parity
+    float part[4][kC], dG[kC];
+    unsigned long long bar[kBars];
+    uint32_t tmem;
+    int abort;
+};
+
+// Shared-memory descriptor of an operand stored as blocks of 8 M/N elements
+// (16 bytes) x k, k consecutive, without a swizzle: `mn` bytes from one block of
+// M/N to the next, 128 bytes from 8 k to the next 8.
+__device__ __forceinline__ uint64_t sdesc_blocks(uint32_t addr, uint32_t mn) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(128 >> 4) << 16;
+    d |= static_cast<uint64_t>((mn >> 4) & 0x3FFFu) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    return d;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __grid_constant__ CUtensorMap mk,
+            const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap md, int* status) {
+    extern __shared__ __align__(1024) unsigned char grad_tc_raw[];
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(grad_tc_raw);
+    constexpr uint32_t kTile = kC * 128, kPart = D * kE * 2;
+    constexpr uint32_t cPE = 0, cA = 128, cB = 256, cC = 384;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rep = A.H / A.Hk;
+    const uint32_t bars = smem_addr(sm.bar);
+    const auto bar = [&](int i) { return bars + 8 * i; };
+    const Waiter wait{bars, &sm.abort, status};
+
+    if (tid == 0) {
+        sm.abort = 0;
+        for (int i : {int(kRows), int(kKQ), kRing + 0, kRing + 1, kRingFree + 0, kRingFree + 1, int(kRowsFree), int(kXUFree),
+                      int(kPE), int(kDone), int(kRaw), int(kEnd)})
+            mbar_init(bar(i), 1);
+        mbar_init(bar(kKQFree), kEpiWarps);
+        mbar_init(bar(kXU), kRowWarps);
+        mbar_init(bar(kSums), kRowWarps);
+        mbar_init(bar(kSums + 1), kRowWarps);
+        mbar_init(bar(kPEFull), kEpiWarps);
+        mbar_init(bar(kFree), kEpiWarps);
+        mbar_init(bar(kEpi), kEpiWarps);
+        fence_mbar_init();
+    }
+    if (warp == 2) {
+        tmem_alloc(smem_addr(&sm.tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (sm.tmem != 0) {  // not seen: an allocation of every column starts at the first
+        if (tid == 0) atomicCAS(status, 0, 5 | (198 << 8));
+        __syncthreads();
+        if (warp == 2) tmem_dealloc(sm.tmem, 512);
+        return;
+    }
+
+    // Item -> chunk of a key head (consecutive items of a CTA step through the value heads of one)
+    struct Item {
+        int b, hk, h, c, hh, len;
+    };
+    const int units = items / rep;
+    const int mine = (units - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    const auto item_at = [&](int unit, int hh) {
+        Item x;
+        const int u = static_cast<int>(blockIdx.x) + unit * static_cast<int>(gridDim.x);
+        x.c = u % chunks;
+        x.hk = u / chunks % A.Hk;
+        x.b = u / chunks / A.Hk;
+        x.hh = hh;
+        x.h = x.hk * rep + hh;
+        x.len = length_of(A, x.b);
+        return x;
+    };
+    // Runs body(item, its number) over this CTA's items; chunks behind a sequence's end are passed over
+    const auto each = [&](auto body) {
+        int y = 0;
+        for (int u = 0; u < mine; ++u) {
+            if (item_at(u, 0).c * kC >= item_at(u, 0).len) continue;
+            for (int hh = 0; hh < rep; ++hh, ++y)
+                if (!body(item_at(u, hh), y)) return y;
+        }
+        return y;
+    };
+
+    if (warp == 0) {
+        int cuts = 0, rows = 0, kqs = 0, pieces = 0;
+        each([&](const Item& x, int y) {
+            const int t0 = x.c * kC;
+            const size_t seq = static_cast<size_t>(x.b) * A.H + x.h, cn = seq * chunks + x.c;
+            const auto tile = [&](unsigned char* to, const CUtensorMap& m, int head, int col, int on) {
+                tma_load_4d(smem_addr(to), &m, bar(on), 64 * col, A.bthd ? head : t0, A.bthd ? t0 : head, x.b);
+            };
+            if (y > 0 && !wait(kRowsFree, y - 1)) return false;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar(kRows), 2 * kTile);
+                tile(sm.dx[0][0], md, x.h, 0, kRows);
+                tile(sm.dx[1][0], md, x.h, 1, kRows);
+            }
+            rows = y + 1;
+            const size_t page = static_cast<size_t>(D) * kE;
+            const auto piece_in = [&](int z) {
+                const int s = z & 1, p = 4 * y + z;
+                if (p >= 2 && !wait(kRingFree + s, (p >> 1) - 1)) return false;
+                const __nv_bfloat16* from = z < 2 ? in.S0 + (seq * (chunks + 1) + x.c) * 2 * page + z * page
+                                                  : in.dS1 + cn * 2 * page + (z - 2) * page;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(kRing + s), kPart);
+                    bulk_load(smem_addr(sm.ring[s]), from, kPart, bar(kRing + s));
+                }
+                pieces = p + 1;
+                return true;
+            };
+            if (!piece_in(0) || !piece_in(1)) return false;
+            // K and Q, needed last
+            if (y > 0 && !wait(kKQFree, y - 1)) return false;
+            const bool cut = t0 + kC > x.len && x.len < A.T;  // rows of padding would be summed over
+            if (lane == 0) {
+                const int on = cut ? kRaw : kKQ;
+                mbar_arrive_expect_tx(bar(on), 2 * (D / 64) * kTile);
+                for (int z = 0; z < D / 64; ++z) {
+                    tile(sm.k[z], mk, x.hk, z, on);
+                    tile(sm.q[z], mq, x.hk, z, on);
+                }
+            }
+            if (cut) {
+                if (!wait(kRaw, cuts++)) return false;
+                for (int r = x.len - t0; r < kC; ++r)
+                    if (lane < 8)
+#pragma unroll
+                        for (int z = 0; z < D / 64; ++z) {
+                            *reinterpret_cast<uint4*>(sm.k[z] + r * 128 + lane * 16) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(sm.q[z] + r * 128 + lane * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(bar(kKQ));
+            }
+            kqs = y + 1;
+            return piece_in(2) && piece_in(3);
+        });
+        // the copies in flight have landed before shared memory goes
+        if (rows) mbar_wait(bar(kRows), (rows - 1) & 1);
+        if (kqs) mbar_wait(bar(kKQ), (kqs - 1) & 1);
+        for (int p = max(0, pieces - 2); p < pieces; ++p) mbar_wait(bar(kRing + (p & 1)), (p >> 1) & 1);
+    } else if (warp == 1) {
+        constexpr uint32_t kIdPE = idesc_bf16_f32(128, 128, 0, 0), kIdPE2 = idesc_bf16_f32(128, 64, 0, 0);
+        constexpr uint32_t kIdS = idesc_bf16_f32(D, 64, 1, 0), kIdSU = idesc_bf16_f32(D, 128, 1, 0);
+        constexpr uint32_t kIdK = idesc_bf16_f32(D, 64, 1, 0), kIdKT = idesc_bf16_f32(D, 64, 1, 1);
+        constexpr uint32_t kDx = 3 * kTile, kU = 2 * kTile;  // strides from 64 columns of e to the next
+        const uint32_t dx = smem_addr(sm.dx), u = smem_addr(sm.u);
+        const uint64_t dO = sdesc_sw128(dx, 16, 1024), xh = desc_add(dO, kTile), xl = desc_add(dO, 2 * kTile);
+        const uint64_t uh = sdesc_sw128(u, 16, 1024);
+        each([&](const Item&, int y) {
+            if (!(wait(kRows, y) && wait(kXU, y) && (y == 0 || wait(kFree, y - 1)))) return false;
+            tc_fence_after();
+            if (elect()) {
+#pragma unroll
+                for (int kk = 0; kk < kE / 16; ++kk) {
+                    const uint32_t a = (kk >> 2) * kDx + (kk & 3) * 32, b = (kk >> 2) * kU + (kk & 3) * 32;
+                    mma_bf16_ss(cPE, desc_add(dO, a), desc_add(uh, b), kIdPE, kk > 0);
+                }
+#pragma unroll
+                for (int kk = 0; kk < kE / 16; ++kk) {
+                    const uint32_t a = (kk >> 2) * kDx + (kk & 3) * 32, b = (kk >> 2) * kU + (kk & 3) * 32;
+                    mma_bf16_ss(cB, desc_add(xh, a), desc_add(uh, b), kIdPE2, kk > 0);  // rows 64 ..: X lo U hi
+                }
+                mma_commit(bar(kPE));
+            }
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {  // S0
+                const int s = z & 1, p = 4 * y + z;
+                if (!wait(kRing + s, p >> 1)) return false;
+                tc_fence_after();
+                if (elect()) {
+                    const uint64_t st = sdesc_blocks(smem_addr(sm.ring[s]), kE * 16);
+#pragma unroll
+                    for (int kk = 0; kk < kE / 16; ++kk) {
+                        const uint32_t b = (kk >> 2) * kDx + (kk & 3) * 32;
+                        const uint64_t a = desc_add(st, kk * 256);
+                        mma_bf16_ss(cA, a, desc_add(dO, b), kIdS, z + kk > 0);
+                        mma_bf16_ss(cA + 64, a, desc_add(xh, b), kIdS, z + kk > 0);
+                        if (z == 0) mma_bf16_ss(cA + 64, a, desc_add(xl, b), kIdS, 1);
+                    }
+                    mma_commit(bar(kRingFree + s));
+                }
+            }
+            if (elect()) mma_commit(bar(kRowsFree));  // dO is read out (X and the factors have barriers of their own)
+#pragma unroll
+            for (int z = 2; z < 4; ++z) {  // dS1
+                const int s = z & 1, p = 4 * y + z;
+                if (!wait(kRing + s, p >> 1)) return false;
+                tc_fence_after();
+                if (elect()) {
+                    const uint64_t st = sdesc_blocks(smem_addr(sm.ring[s]), kE * 16);
+#pragma unroll
+                    for (int kk = 0; kk < kE / 16; ++kk)
+                        mma_bf16_ss(cC, desc_add(st, kk * 256), desc_add(uh, (kk >> 2) * kU + (kk & 3) * 32), kIdSU,
+                                    z > 2 || kk > 0);
+                    mma_commit(bar(kRingFree + s));
+                }
+            }
+            if (elect()) mma_commit(bar(kXUFree));
+            if (!(wait(kKQ, y) && wait(kPEFull, y))) return false;
+            tc_fence_after();
+            if (elect()) {
+                const uint64_t kt = sdesc_sw128(smem_addr(sm.k), kTile, 1024), qt = sdesc_sw128(smem_addr(sm.q), kTile, 1024);
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const uint32_t pe = smem_addr(sm.pe[z]);
+                    const uint64_t p0 = sdesc_sw128(pe, 16, 1024), e0 = sdesc_sw128(pe + kTile, 16, 1024);
+                    const uint64_t pt = sdesc_sw128(pe, kTile, 1024), et = sdesc_sw128(pe + kTile, kTile, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        mma_bf16_ss(cB, desc_add(kt, kk * 2048), desc_add(p0, kk * 32), kIdK, z + kk > 0);
+                        mma_bf16_ss(cB + 64, desc_add(kt, kk * 2048), desc_add(e0, kk * 32), kIdK, z + kk > 0);
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        mma_bf16_ss(cB + 64, desc_add(kt, kk * 2048), desc_add(et, kk * 2048), kIdKT, 1);
+                        mma_bf16_ss(cB + 64, desc_add(qt, kk * 2048), desc_add(pt, kk * 2048), kIdKT, 1);
+                    }
+                }
+                mma_commit(bar(kDone));
+            }
+            return true;
+        });
+        if (elect()) mma_commit(bar(kEnd));
+        mbar_wait(bar(kEnd), 0);
+    } else if (warp >= 4 && warp < 12) {
+        const int quad = warp & 3, half = (warp - 4) >> 2, g = lane >> 2, i = lane & 3;
+        const uint32_t row = static_cast<uint32_t>(32 * quad) << 16;
+        constexpr int kHalves = D / 64;  // groups of 16 rows of d in this warp's 32 lanes
+        const int r0 = 32 * half;
+        int met = 0;
+        const auto meet = [&] {  // all epilogue warps, with a bounded wait
+            __syncwarp();
+            if (lane == 0) arrive(bar(kEpi));
+            return wait(kEpi, met++);
+        };
+        // sums over the value heads of a key head, between two of its items: this thread's dq and dk, a value per 256
+        float* sums = in.sums + static_cast<size_t>(blockIdx.x) * (2 * kHalves * 16 * 32 * kEpiWarps) + (tid - 128);
+        each([&](const Item& x, int y) {
+            const int t0 = x.c * kC;
+            const float *eg = sm.f[0], *rest = sm.f[1], *neg_beta = sm.f[4], *neg_beta_eg = sm.f[6];
+            const float *G = sm.f[7], *Gl = sm.f[8];
+            {  // the item before is left behind (the barrier at its end)
+                const float* from = ws[(static_cast<size_t>(x.b) * A.H + x.h) * chunks + x.c].eg;
+                for (int z = tid - 128; z < kFactors * kC; z += 32 * kEpiWarps) sm.f[0][z] = from[z];
+            }
+            if (!(meet() && wait(kPE, y))) return false;
+            tc_fence_after();
+            {  // rows 0 .. 63: dP, 64 .. 127: E; this thread's row, columns r0 ..
+                const int r = 32 * quad + lane, t = r & 63;
+                const bool isE = r >= 64;
+                float v[32], z[32];
+                uint32_t w[32];
+                tmem_ld32(row + cPE + r0, v);
+                tmem_ld32(row + cPE + 64 + r0, z);
+#pragma unroll
+                for (int s = 0; s < 32; ++s) v[s] += z[s];
+                if (quad >= 2) {
+                    tmem_ld32(row + cB + r0, z);
+#pragma unroll
+                    for (int s = 0; s < 32; ++s) v[s] += z[s];
+                }
+                const float gt = G[t], gtl = Gl[t], m = isE ? neg_beta[t] : 1.f;
+                const int last = t0 + t < x.len ? (isE ? t - 1 : t) : -1;  // columns 0 .. last are below the diagonal
+#pragma unroll
+                for (int s = 0; s < 32; ++s)
+                    v[s] = r0 + s <= last ? v[s] * (m * exp2f((gt - G[r0 + s]) + (gtl - Gl[r0 + s]))) : 0.f;
+                walk::split32(v, w);
+#pragma unroll
+                for (int p = 0; p < 8; ++p)
+                    st_shared_v4(smem_addr(sm.pe[p >> 2][isE]) + piece<128>(t, 4 * half + (p & 3)), w[4 * p], w[4 * p + 1],
+                                 w[4 * p + 2], w[4 * p + 3]);
+            }
+            tc_fence_before();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(bar(kPEFull));
+            if (!(wait(kDone, y) && wait(kKQ, y) && wait(kSums + (y & 1), y >> 1))) return false;
+            tc_fence_after();
+            // dq and dk of this item: rows 16 hb + g (+ 8) of d in this quadrant, columns 8 j + 2 i (+ 1) of this half
+            const auto load = [&](uint32_t col, float (&to)[32]) {
+                // D = 64: M = 64 puts 16 rows into each quadrant; the second half is not used
+                tmem_ld16x256b_x4_pair(row + col + r0, row + col + r0 + (kHalves == 2 ? 16u << 16 : 0u), to);
+            };
+            const bool first = x.hh == 0, last_head = x.hh == rep - 1;
+            const size_t step = A.bthd ? static_cast<size_t>(A.Hk) * D : D;
+            const int d_at = (D / 4) * quad, left = x.len - t0;
+            const size_t out_at = row_at(A, x.b, x.hk, A.Hk, t0, D) + d_at;
+            float a[32];
+            float now[kHalves * 16];
+            // `now` (dq: o = 0, dk: o = 1) added to the heads before, and kept or written out
+            const auto finish = [&](int o, void* out) {
+                float* sum = sums + o * (kHalves * 16 * 32 * kEpiWarps);
+                if (!first)
+#pragma unroll
+                    for (int z = 0; z < kHalves * 16; ++z) now[z] += sum[z * 32 * kEpiWarps];
+                if (!last_head) {
+#pragma unroll
+                    for (int z = 0; z < kHalves * 16; ++z) sum[z * 32 * kEpiWarps] = now[z];
+                } else if (A.out_bf16) {
+                    // through this warp's part of the dP, E operand, which the MMAs have read: [32 rows][16 or 32 columns]
+                    constexpr int kRow = 2 * (D / 4), kPc = kRow / 16;  // bytes and pieces of a row
+                    unsigned char* to = sm.pe[0][0] + (2 * (warp - 4) + o) * (2 * kC * 128 / kEpiWarps);
+#pragma unroll
+                    for (int hb = 0; hb < kHalves; ++hb)
+#pragma unroll
+                        for (int jp = 0; jp < 2; ++jp) {
+                            const int m = lane >> 3, t = 8 * (2 * jp + (m >> 1)) + (lane & 7), p = 2 * hb + (m & 1);
+                            const int z = 16 * hb + 8 * jp;
+                            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(
+                                             smem_addr(to) + t * kRow + ((p ^ ((t >> 1) & (kPc - 1))) << 4)),
+                                         "r"(pack(now[z], now[z + 1])), "r"(pack(now[z + 2], now[z + 3])),
+                                         "r"(pack(now[z + 4], now[z + 5])), "r"(pack(now[z + 6], now[z + 7]))
+                                         : "memory");
+                        }
+                    __syncwarp();
+                    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(out) + out_at;
+#pragma unroll
+                    for (int z = lane; z < 32 * kPc; z += 32) {
+                        const int t = z / kPc, c = z % kPc;
+                        if (r0 + t < left)
+                            *reinterpret_cast<uint4*>(p + (r0 + t) * step + 8 * c) =
+                                *reinterpret_cast<const uint4*>(to + t * kRow + ((c ^ ((t >> 1) & (kPc - 1))) << 4));
+                    }
+                } else {
+                    float* p = static_cast<float*>(out) + out_at;
+#pragma unroll
+                    for (int z = 0; z < kHalves * 16; ++z) {
+                        const int t = r0 + 8 * (z / 4 % 4) + 2 * i + (z & 1);
+                        if (t < left) p[t * step + g + 16 * (z >> 4) + 8 * (z >> 1 & 1)] = now[z];
+                    }
+                }
+            };
+            load(cA, a);
+#pragma unroll
+            for (int z = 0; z < kHalves * 16; ++z) {
+                const int t = r0 + 8 * (z / 4 % 4) + 2 * i + (z & 1);
+                now[z] = a[z] * eg[t];
+            }
+            load(cB, a);
+#pragma unroll
+            for (int z = 0; z < kHalves * 16; ++z) now[z] += a[z];
+            {  // q . dq: this warp's rows of d, summed over the lanes that share columns
+                float s[8] = {};
+#pragma unroll
+                for (int hb = 0; hb < kHalves; ++hb)
+#pragma unroll
+                    for (int jp = 0; jp < 2; ++jp) {
+                        // fragments of Q^T: rows of d, columns t, of tiles 2 jp and 2 jp + 1
+                        const int d0 = (D / 4) * quad + 16 * hb, m = lane >> 3;
+                        uint32_t qq[4];
+                        ldsm_t(qq, smem_addr(sm.q[d0 >> 6]) +
+                                       piece<128>(r0 + 8 * (2 * jp + (m >> 1)) + (lane & 7), ((d0 & 63) >> 3) + (m & 1)));
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const int at = 16 * hb + 4 * (2 * jp + z), j = 2 * (2 * jp + z);
+                            s[j] = fmaf(low_of(qq[2 * z]), now[at], fmaf(low_of(qq[2 * z + 1]), now[at + 2], s[j]));
+                            s[j + 1] = fmaf(high_of(qq[2 * z]), now[at + 1], fmaf(high_of(qq[2 * z + 1]), now[at + 3], s[j + 1]));
+                        }
+                    }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                    for (int m = 4; m < 32; m <<= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], m);
+                    if (g == 0) sm.part[quad][r0 + 8 * (j >> 1) + 2 * i + (j & 1)] = s[j];
+                }
+            }
+            finish(0, A.dq);
+            load(cA + 64, a);
+#pragma unroll
+            for (int z = 0; z < kHalves * 16; ++z) {
+                const int t = r0 + 8 * (z / 4 % 4) + 2 * i + (z & 1);
+                now[z] = a[z] * neg_beta_eg[t];
+            }
+            load(cB + 64, a);
+#pragma unroll
+            for (int z = 0; z < kHalves * 16; ++z) now[z] += a[z];
+            load(cC, a);
+#pragma unroll
+            for (int z = 0; z < kHalves * 16; ++z) {
+                const int t = r0 + 8 * (z / 4 % 4) + 2 * i + (z & 1);
+                now[z] = fmaf(a[z], rest[t], now[z]);
+            }
+            load(cC + 64, a);
+#pragma unroll
+            for (int z = 0; z < kHalves * 16; ++z) {
+                const int t = r0 + 8 * (z / 4 % 4) + 2 * i + (z & 1);
+                now[z] = fmaf(a[z], rest[t], now[z]);
+            }
+            finish(1, A.dk);
+            tc_fence_before();
+            if (!meet()) return false;  // q . dq is complete
+            if (warp == 4) {  // sums of dL/dG from each row to the chunk's end: two rows per lane
+                const int t = 2 * lane;
+                const size_t seq = static_cast<size_t>(x.b) * A.H + x.h;
+                const float* xv = sm.xv[y & 1];
+                float y0 = sm.part[0][t] + sm.part[1][t] + sm.part[2][t] + sm.part[3][t] - xv[t];
+                float y1 = sm.part[0][t + 1] + sm.part[1][t + 1] + sm.part[2][t + 1] + sm.part[3][t + 1] - xv[t + 1];
+                // (the rows of dO behind the end are whatever lies there)
+                if (t0 + t >= x.len) y0 = 0.f;
+                if (t0 + t + 1 >= x.len) y1 = 0.f;
+                if (lane == 31) {
+                    const float* dot = in.dot + (seq * chunks + x.c) * 4;
+                    y1 += (dot[0] + dot[1]) + (dot[2] + dot[3]);
+                }
+                float s = y0 + y1;
+#pragma unroll
+                for (int m = 1; m < 32; m <<= 1) {
+                    const float z = __shfl_down_sync(0xffffffffu, s, m);
+                    if (lane + m < 32) s += z;
+                }
+                const size_t at = row_at(A, x.b, x.h, A.H, t0 + t, 1), next = row_at(A, x.b, x.h, A.H, t0 + t + 1, 1);
+                if (t0 + t < x.len) {
+                    if (A.dg) A.dg[at] = s;
+                    A.dbeta[at] = sm.dbeta[y & 1][t];
+                }
+                if (t0 + t + 1 < x.len) {
+                    if (A.dg) A.dg[next] = s - y0;
+                    A.dbeta[next] = sm.dbeta[y & 1][t + 1];
+                }
+            }
+            // accumulators, K, Q, dP and E, the factors and the row sums of this item are read out
+            if (!meet()) return false;
+            if (lane == 0) {
+                arrive(bar(kKQFree));
+                arrive(bar(kFree));
+            }
+            return true;
+        });
+    } else if (warp >= 12) {
+        const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(A.v);
+        each([&](const Item& x, int y) {
+            const int t0 = x.c * kC, col = 4 * lane;
+            const size_t seq = static_cast<size_t>(x.b) * A.H + x.h;
+            const ChunkWs& cw = ws[seq * chunks + x.c];
+#pragma unroll 1
+            for (int z = 0; z < 2; ++z) {  // 8 rows at a time, all loads first
+                float4 w[8], xx[8];
+                uint2 vv[8];
+                float bt[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const int t = 16 * (warp - 12) + 8 * z + r;
+                    w[r] = xx[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    vv[r] = make_uint2(0, 0);
+                    bt[r] = 0.f;
+                    if (t0 + t < x.len) {
+                        const size_t at = (seq * A.T + t0 + t) * kE + col;
+                        w[r] = *reinterpret_cast<const float4*>(in.W + at);
+                        xx[r] = *reinterpret_cast<const float4*>(in.X + at);
+                        vv[r] = *reinterpret_cast<const uint2*>(v + row_at(A, x.b, x.h, A.H, t0 + t, kE) + col);
+                        bt[r] = cw.beta[t];
+                    }
+                }
+                // The MMAs have read the operands of the item before.  They began when the epilogue had left the item
+                // before that one, whose buffer of row sums is written now.
+                if (z == 0 && y > 0 && !wait(kXUFree, y - 1)) return false;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const int t = 16 * (warp - 12) + 8 * z + r;
+                    const uint32_t at = piece<128>(t, (col & 63) >> 3) + 2 * (col & 7);
+                    uint32_t h0, h1, l0, l1;
+                    split(bt[r] * w[r].x, bt[r] * w[r].y, h0, l0);
+                    split(bt[r] * w[r].z, bt[r] * w[r].w, h1, l1);
+                    *reinterpret_cast<uint2*>(sm.u[col >> 6][0] + at) = make_uint2(h0, h1);
+                    *reinterpret_cast<uint2*>(sm.u[col >> 6][1] + at) = make_uint2(l0, l1);
+                    split(xx[r].x, xx[r].y, h0, l0);
+                    split(xx[r].z, xx[r].w, h1, l1);
+                    *reinterpret_cast<uint2*>(sm.dx[col >> 6][1] + at) = make_uint2(h0, h1);
+                    *reinterpret_cast<uint2*>(sm.dx[col >> 6][2] + at) = make_uint2(l0, l1);
+                    float db = fmaf(xx[r].x, w[r].x, fmaf(xx[r].y, w[r].y, fmaf(xx[r].z, w[r].z, xx[r].w * w[r].w)));
+                    float xv = fmaf(xx[r].x, low_of(vv[r].x), fmaf(xx[r].y, high_of(vv[r].x),
+                               fmaf(xx[r].z, low_of(vv[r].y), xx[r].w * high_of(vv[r].y))));
+#pragma unroll
+                    for (int m = 16; m; m >>= 1) {
+                        db += __shfl_xor_sync(0xffffffffu, db, m);
+                        xv += __shfl_xor_sync(0xffffffffu, xv, m);
+                    }
+                    if (lane == 0) {
+                        sm.dbeta[y & 1][t] = db;
+                        sm.xv[y & 1][t] = bt[r] * xv;
+                    }
+                    if (t0 + t < x.len) {
+                        const size_t io = row_at(A, x.b, x.h, A.H, t0 + t, kE) + col;
+                        const float b0 = bt[r] * xx[r].x, b1 = bt[r] * xx[r].y, b2 = bt[r] * xx[r].z, b3 = bt[r] * xx[r].w;
+                        if (A.out_bf16)
+                            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.dv) + io) =
+                                make_uint2(pack(b0, b1), pack(b2, b3));
+                        else
+                            *reinterpret_cast<float4*>(static_cast<float*>(A.dv) + io) = make_float4(b0, b1, b2, b3);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                arrive(bar(kSums + (y & 1)));
+                arrive(bar(kXU));
+            }
+            return true;
+        });
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 2) tmem_dealloc(sm.tmem, 512);
+}
+
+}  // namespace grad
+}  // namespace gdr
+}  // namespace la2

@@ -520,6 +520,20 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
                     tmem_st32u(row + cB + 32 * q, w);
                     done(kState + y);
                 }
+            } else if (kMode == kSave) {
+                __nv_bfloat16* to = out.S0 + (static_cast<size_t>(n) * (chunks + 1) + nc) * 2 * page + e * 8;
+#pragma unroll 1
+                for (int y = 0; y < kGroups; ++y) {
+                    const int q = half * kGroups + y;
+                    float S[32];
+                    uint32_t w[32];
+                    tmem_ld32(row + cS + 32 * q, S);
+                    split32(S, w);
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4)
+                        *reinterpret_cast<uint4*>(to + (x >> 4) * page + (4 * q + (x & 15) / 4) * (kE * 8)) =
+                            make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
+                }
             } else if (last) {
 #pragma unroll 1
                 for (int y = 0; y < kGroups; ++y) {
@@ -642,9 +656,19 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
             __syncwarp();
             if (lane == 0) arrive(bar(kEmpty + s));
             // the state (forward: before the chunk, backward: the gradient after it) to memory (Saved's layout)
+            uint4 s1[8];  // 32 columns of d of S1, high and low
+            const __nv_bfloat16* after = out.S0 + (static_cast<size_t>(n) * (chunks + 1) + c + 1) * 2 * page + e * 8;
+            const auto load_s1 = [&](int q) {
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    s1[x] = *reinterpret_cast<const uint4*>(after + (x >> 2) * page + (4 * q + (x & 3)) * (kE * 8));
+            };
+            if (kRev) load_s1(0);
             if (!(wait(kState, it) && (D == 64 || wait(kState + 1, it)))) break;
             tc_fence_after();
-            __nv_bfloat16* to = (kRev ? out.dS1 : out.S0) + (static_cast<size_t>(n) * chunks + c) * 2 * page + e * 8;
+            __nv_bfloat16* to = (kRev ? out.dS1 + (static_cast<size_t>(n) * chunks + c) * 2 * page
+                                      : out.S0 + (static_cast<size_t>(n) * (chunks + 1) + c) * 2 * page) + e * 8;
+            float dot = 0.f;
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
                 float w[32];
@@ -654,6 +678,25 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
                     *reinterpret_cast<uint4*>(to + (x >> 4) * page + (4 * q + (x & 15) / 4) * (kE * 8)) =
                         make_uint4(__float_as_uint(w[x]), __float_as_uint(w[x + 1]), __float_as_uint(w[x + 2]),
                                    __float_as_uint(w[x + 3]));
+                if (kRev) {  // <dS1, S1>: the state after this chunk as the forward walk left it
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint4 yh = s1[x], yl = s1[4 + x];
+                        const uint32_t h4[4] = {yh.x, yh.y, yh.z, yh.w}, l4[4] = {yl.x, yl.y, yl.z, yl.w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const uint32_t dh = __float_as_uint(w[4 * x + y]), dl = __float_as_uint(w[16 + 4 * x + y]);
+                            dot = fmaf(low_of(dh) + low_of(dl), low_of(h4[y]) + low_of(l4[y]), dot);
+                            dot = fmaf(high_of(dh) + high_of(dl), high_of(h4[y]) + high_of(l4[y]), dot);
+                        }
+                    }
+                    if (q + 1 < D / 32) load_s1(q + 1);
+                }
+            }
+            if (kRev) {
+#pragma unroll
+                for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+                if (lane == 0) out.dot[(static_cast<size_t>(n) * chunks + c) * 4 + (warp & 3)] = dot;
             }
             tc_fence_before();
             __syncwarp();
