@@ -327,8 +327,8 @@ gdr_prep(Args A, ChunkWs* ws, int chunks) {
             float x[2] = {0.f, 0.f};
             if (j <= 2 * rt + 1) {
                 const int last = isq ? t : t - 1;  // P has its diagonal, Ah has not
-                const float m0 = exp2f((gt[half] - gs.x) + (gtl[half] - gsl.x));
-                const float m1 = exp2f((gt[half] - gs.y) + (gtl[half] - gsl.y));
+                const float m0 = exp2_flat((gt[half] - gs.x) + (gtl[half] - gsl.x));
+                const float m1 = exp2_flat((gt[half] - gs.y) + (gtl[half] - gsl.y));
                 x[0] = s <= last ? acc[j][2 * half] * m0 : 0.f;  // (above the diagonal m may be infinite)
                 x[1] = s + 1 <= last ? acc[j][2 * half + 1] * m1 : 0.f;
             }

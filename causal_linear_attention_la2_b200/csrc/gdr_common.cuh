@@ -52,6 +52,14 @@ __device__ __forceinline__ float gate_at(const Args& a, size_t i) {
     return a.g ? fmaxf(a.g[i], kMinGate) : 0.f;
 }
 
+// 2^x, off by at most 2 units in the last place (results below 2^-126 are zero);
+// without a branch, so that it can be computed where it is not used.
+__device__ __forceinline__ float exp2_flat(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 

@@ -207,7 +207,7 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
     } else if (warp == 1) {
         constexpr uint32_t kIdPE = idesc_bf16_f32(128, 128, 0, 0), kIdPE2 = idesc_bf16_f32(128, 64, 0, 0);
         constexpr uint32_t kIdS = idesc_bf16_f32(D, 64, 1, 0), kIdSU = idesc_bf16_f32(D, 128, 1, 0);
-        constexpr uint32_t kIdK = idesc_bf16_f32(D, 64, 1, 0), kIdKT = idesc_bf16_f32(D, 64, 1, 1);
+        constexpr uint32_t kIdKT = idesc_bf16_f32(D, 64, 1, 1);
         constexpr uint32_t kDx = 3 * kTile, kU = 2 * kTile;  // strides from 64 columns of e to the next
         const uint32_t dx = smem_addr(sm.dx), u = smem_addr(sm.u);
         const uint64_t dO = sdesc_sw128(dx, 16, 1024), xh = desc_add(dO, kTile), xl = desc_add(dO, 2 * kTile);
@@ -268,18 +268,19 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                 const uint64_t kt = sdesc_sw128(smem_addr(sm.k), kTile, 1024), qt = sdesc_sw128(smem_addr(sm.q), kTile, 1024);
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
+                    const uint64_t p0 = sdesc_sw128(smem_addr(sm.pe[z]), 16, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)  // rows of dP and E are one operand of 128 rows
+                        mma_bf16_ss(cB, desc_add(kt, kk * 2048), desc_add(p0, kk * 32), kIdSU, z + kk > 0);
+                }
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
                     const uint32_t pe = smem_addr(sm.pe[z]);
-                    const uint64_t p0 = sdesc_sw128(pe, 16, 1024), e0 = sdesc_sw128(pe + kTile, 16, 1024);
                     const uint64_t pt = sdesc_sw128(pe, kTile, 1024), et = sdesc_sw128(pe + kTile, kTile, 1024);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
-                        mma_bf16_ss(cB, desc_add(kt, kk * 2048), desc_add(p0, kk * 32), kIdK, z + kk > 0);
-                        mma_bf16_ss(cB + 64, desc_add(kt, kk * 2048), desc_add(e0, kk * 32), kIdK, z + kk > 0);
-                    }
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        mma_bf16_ss(cB + 64, desc_add(kt, kk * 2048), desc_add(et, kk * 2048), kIdKT, 1);
-                        mma_bf16_ss(cB + 64, desc_add(qt, kk * 2048), desc_add(pt, kk * 2048), kIdKT, 1);
+                        mma_bf16_ss(cPE, desc_add(kt, kk * 2048), desc_add(et, kk * 2048), kIdKT, z + kk > 0);
+                        mma_bf16_ss(cPE, desc_add(qt, kk * 2048), desc_add(pt, kk * 2048), kIdKT, 1);
                     }
                 }
                 mma_commit(bar(kDone));
@@ -328,8 +329,18 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                 const float gt = G[t], gtl = Gl[t], m = isE ? neg_beta[t] : 1.f;
                 const int last = t0 + t < x.len ? (isE ? t - 1 : t) : -1;  // columns 0 .. last are below the diagonal
 #pragma unroll
-                for (int s = 0; s < 32; ++s)
-                    v[s] = r0 + s <= last ? v[s] * (m * exp2f((gt - G[r0 + s]) + (gtl - Gl[r0 + s]))) : 0.f;
+                for (int s = 0; s < 32; s += 4) {
+                    const float4 gs = *reinterpret_cast<const float4*>(G + r0 + s);
+                    const float4 gl = *reinterpret_cast<const float4*>(Gl + r0 + s);
+                    const float e4[4] = {(gt - gs.x) + (gtl - gl.x), (gt - gs.y) + (gtl - gl.y), (gt - gs.z) + (gtl - gl.z),
+                                         (gt - gs.w) + (gtl - gl.w)};
+#pragma unroll
+                    for (int y4 = 0; y4 < 4; ++y4) {
+                        // (above the diagonal the power may be infinite, and is not used)
+                        const float on = v[s + y4] * (m * exp2_flat(e4[y4]));
+                        v[s + y4] = r0 + s + y4 <= last ? on : 0.f;
+                    }
+                }
                 walk::split32(v, w);
 #pragma unroll
                 for (int p = 0; p < 8; ++p)
@@ -440,6 +451,9 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             load(cB + 64, a);
 #pragma unroll
             for (int z = 0; z < kHalves * 16; ++z) now[z] += a[z];
+            load(cPE, a);
+#pragma unroll
+            for (int z = 0; z < kHalves * 16; ++z) now[z] += a[z];
             load(cC, a);
 #pragma unroll
             for (int z = 0; z < kHalves * 16; ++z) {
@@ -520,10 +534,11 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                 // The MMAs have read the operands of the item before.  They began when the epilogue had left the item
                 // before that one, whose buffer of row sums is written now.
                 if (z == 0 && y > 0 && !wait(kXUFree, y - 1)) return false;
+                float sum[16];  // of each row: x . w, x . v
+                const int row0 = 16 * (warp - 12) + 8 * z;
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                    const int t = 16 * (warp - 12) + 8 * z + r;
-                    const uint32_t at = piece<128>(t, (col & 63) >> 3) + 2 * (col & 7);
+                    const uint32_t at = piece<128>(row0 + r, (col & 63) >> 3) + 2 * (col & 7);
                     uint32_t h0, h1, l0, l1;
                     split(bt[r] * w[r].x, bt[r] * w[r].y, h0, l0);
                     split(bt[r] * w[r].z, bt[r] * w[r].w, h1, l1);
@@ -533,27 +548,39 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                     split(xx[r].z, xx[r].w, h1, l1);
                     *reinterpret_cast<uint2*>(sm.dx[col >> 6][1] + at) = make_uint2(h0, h1);
                     *reinterpret_cast<uint2*>(sm.dx[col >> 6][2] + at) = make_uint2(l0, l1);
-                    float db = fmaf(xx[r].x, w[r].x, fmaf(xx[r].y, w[r].y, fmaf(xx[r].z, w[r].z, xx[r].w * w[r].w)));
-                    float xv = fmaf(xx[r].x, low_of(vv[r].x), fmaf(xx[r].y, high_of(vv[r].x),
-                               fmaf(xx[r].z, low_of(vv[r].y), xx[r].w * high_of(vv[r].y))));
+                    sum[2 * r] = fmaf(xx[r].x, w[r].x, fmaf(xx[r].y, w[r].y, fmaf(xx[r].z, w[r].z, xx[r].w * w[r].w)));
+                    sum[2 * r + 1] = bt[r] * fmaf(xx[r].x, low_of(vv[r].x), fmaf(xx[r].y, high_of(vv[r].x),
+                                                  fmaf(xx[r].z, low_of(vv[r].y), xx[r].w * high_of(vv[r].y))));
+                }
+                // 16 sums over 32 lanes, halving what a lane holds with each exchange: lane l ends with sum l / 2
 #pragma unroll
-                    for (int m = 16; m; m >>= 1) {
-                        db += __shfl_xor_sync(0xffffffffu, db, m);
-                        xv += __shfl_xor_sync(0xffffffffu, xv, m);
-                    }
-                    if (lane == 0) {
-                        sm.dbeta[y & 1][t] = db;
-                        sm.xv[y & 1][t] = bt[r] * xv;
-                    }
-                    if (t0 + t < x.len) {
-                        const size_t io = row_at(A, x.b, x.h, A.H, t0 + t, kE) + col;
-                        const float b0 = bt[r] * xx[r].x, b1 = bt[r] * xx[r].y, b2 = bt[r] * xx[r].z, b3 = bt[r] * xx[r].w;
-                        if (A.out_bf16)
-                            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.dv) + io) =
-                                make_uint2(pack(b0, b1), pack(b2, b3));
-                        else
-                            *reinterpret_cast<float4*>(static_cast<float*>(A.dv) + io) = make_float4(b0, b1, b2, b3);
-                    }
+                for (int m = 16, held = 8; m > 1; m >>= 1, held >>= 1)
+#pragma unroll
+                    for (int y2 = 0; y2 < 8; ++y2)
+                        if (y2 < held) {
+                            const bool up = lane & m;
+                            const float give = up ? sum[y2] : sum[held + y2], keep = up ? sum[held + y2] : sum[y2];
+                            sum[y2] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+                        }
+                sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
+                if ((lane & 1) == 0) (lane & 2 ? sm.xv : sm.dbeta)[y & 1][row0 + (lane >> 2)] = sum[0];
+                const size_t out0 = row_at(A, x.b, x.h, A.H, t0 + row0, kE) + col;
+                const size_t step = A.bthd ? static_cast<size_t>(A.H) * kE : kE;
+                const int left = x.len - t0 - row0;
+                if (A.out_bf16) {
+                    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(A.dv) + out0;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        if (r < left)
+                            *reinterpret_cast<uint2*>(p + r * step) = make_uint2(pack(bt[r] * xx[r].x, bt[r] * xx[r].y),
+                                                                                 pack(bt[r] * xx[r].z, bt[r] * xx[r].w));
+                } else {
+                    float* p = static_cast<float*>(A.dv) + out0;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        if (r < left)
+                            *reinterpret_cast<float4*>(p + r * step) =
+                                make_float4(bt[r] * xx[r].x, bt[r] * xx[r].y, bt[r] * xx[r].z, bt[r] * xx[r].w);
                 }
             }
             fence_proxy_async_smem();

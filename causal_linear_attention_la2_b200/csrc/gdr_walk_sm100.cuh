@@ -656,20 +656,23 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
             __syncwarp();
             if (lane == 0) arrive(bar(kEmpty + s));
             // the state (forward: before the chunk, backward: the gradient after it) to memory (Saved's layout)
-            uint4 s1[8];  // 32 columns of d of S1, high and low
+            uint4 s1[2][8];  // 32 columns of d of S1, high and low, and the 32 after them
             const __nv_bfloat16* after = out.S0 + (static_cast<size_t>(n) * (chunks + 1) + c + 1) * 2 * page + e * 8;
             const auto load_s1 = [&](int q) {
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
-                    s1[x] = *reinterpret_cast<const uint4*>(after + (x >> 2) * page + (4 * q + (x & 3)) * (kE * 8));
+                    s1[q & 1][x] = *reinterpret_cast<const uint4*>(after + (x >> 2) * page + (4 * q + (x & 3)) * (kE * 8));
             };
-            if (kRev) load_s1(0);
+            if (kRev) {
+                load_s1(0);
+                load_s1(1);
+            }
             if (!(wait(kState, it) && (D == 64 || wait(kState + 1, it)))) break;
             tc_fence_after();
             __nv_bfloat16* to = (kRev ? out.dS1 + (static_cast<size_t>(n) * chunks + c) * 2 * page
                                       : out.S0 + (static_cast<size_t>(n) * (chunks + 1) + c) * 2 * page) + e * 8;
             float dot = 0.f;
-#pragma unroll 1
+#pragma unroll
             for (int q = 0; q < D / 32; ++q) {
                 float w[32];
                 tmem_ld32(row + cB + 32 * q, w);
@@ -681,7 +684,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
                 if (kRev) {  // <dS1, S1>: the state after this chunk as the forward walk left it
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const uint4 yh = s1[x], yl = s1[4 + x];
+                        const uint4 yh = s1[q & 1][x], yl = s1[q & 1][4 + x];
                         const uint32_t h4[4] = {yh.x, yh.y, yh.z, yh.w}, l4[4] = {yl.x, yl.y, yl.z, yl.w};
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
@@ -690,7 +693,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
                             dot = fmaf(high_of(dh) + high_of(dl), high_of(h4[y]) + high_of(l4[y]), dot);
                         }
                     }
-                    if (q + 1 < D / 32) load_s1(q + 1);
+                    if (q + 2 < D / 32) load_s1(q + 2);
                 }
             }
             if (kRev) {
