@@ -157,7 +157,7 @@ bool by_chunks(la2_dtype dtype, int d, int e) {
 }
 
 struct ChunkLayout {
-    size_t prep, S0, dS1, W, X, dot, sums, bytes;
+    size_t prep, S0, dS1, W, X, sums, bytes;
 };
 
 ChunkLayout chunk_ws(long long BH, int T, int d, int e, bool bwd) {
@@ -171,8 +171,7 @@ ChunkLayout chunk_ws(long long BH, int T, int d, int e, bool bwd) {
         w.dS1 = w.S0 + pages + align256(seqs * 2 * d * e * 2);
         w.W = w.dS1 + pages;
         w.X = w.W + rows;
-        w.dot = w.X + rows;
-        w.sums = w.dot + align256(seqs * chunks * 4 * sizeof(float));
+        w.sums = w.X + rows;
         at = w.sums + (e == 128 ? static_cast<size_t>(kSMs) * (64 << 10) : 0);
     }
     w.bytes = at;
@@ -237,7 +236,6 @@ la2_status chunk_backward(const Args& A, char* ws, cudaStream_t stream) {
     sv.dS1 = reinterpret_cast<__nv_bfloat16*>(ws + w.dS1);
     sv.W = reinterpret_cast<float*>(ws + w.W);
     sv.X = reinterpret_cast<float*>(ws + w.X);
-    sv.dot = reinterpret_cast<float*>(ws + w.dot);
     sv.sums = reinterpret_cast<float*>(ws + w.sums);
     const int walks = A.B * A.H * (A.e / kWalkCols);
     if (chunks > 0) {

@@ -434,7 +434,6 @@ struct Saved {
     __nv_bfloat16 *S0;   // [B*H][chunks + 1][2][d / 8][e][8], the last one after the last chunk
     __nv_bfloat16 *dS1;  // [B*H][chunks][2][d / 8][e][8]
     float *W, *X;
-    float* dot;          // [B*H][chunks][4]: <dS1, S1> in four parts (e = 128)
     float* sums;         // gdr_grad_tc's sums over the value heads of a key head, 64 KB per CTA
 };
 

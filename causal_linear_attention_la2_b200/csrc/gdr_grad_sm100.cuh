@@ -1,7 +1,7 @@
 // gdr_grad_sm100.cuh -- dq, dk, dv, dg and dbeta of the gated delta rule for
 // e = 128 on the tcgen05 tensor cores, all chunks independently, from what the
 // walks left (gdr_walk_sm100.cuh): per chunk the state S0 before it, the gradient
-// dS1 of the state after it, <dS1, S1>, and the rows w and x.  With U = beta W:
+// dS1 of the state after it, and the rows w and x.  With U = beta W:
 //
 //   dP = M o (dO U^T),   E_ts = -beta_t M_ts (x_t . u_s)  (s < t)
 //   dq^T = S0 dO^T diag(e^G) + K^T dP^T
@@ -22,9 +22,9 @@
 // 80 KB (d = 128), which is what bounds it; warps:
 //   0      loads: dO and factors, K and Q, the four state parts through a ring
 //   1      MMAs
-//   2      TMEM allocation
+//   2, 3   <dS1, S1> (both states out of L2); 3: dg, dbeta; 2: TMEM allocation
 //   4-11   epilogues: dP and E as operands; dq, dk, q . dq
-//   12-15  w, x -> operands U, X; dv, dbeta, x . v
+//   12-15  w, x -> operands U, X; dv, and the sums of rows for dbeta and dg
 // Waits are bounded as in gdr_walk_sm100.cuh.
 #pragma once
 #include "gdr_walk_sm100.cuh"
@@ -44,7 +44,8 @@ constexpr int kEpiWarps = 8, kRowWarps = 4;
 constexpr int kFactors = 9;  // eg .. gl of ChunkWs
 
 enum Bar { kRows = 0, kRowsFree, kKQ, kKQFree, kXU, kXUFree, kRing, kRingFree = kRing + 2, kPE = kRingFree + 2,
-           kPEFull, kDone, kFree, kSums, kRaw = kSums + 2, kEpi, kEnd, kBars };
+           kPEFull, kDone, kFree, kSums, kSumsFree = kSums + 2, kPart = kSumsFree + 2, kDot = kPart + 2,
+           kRaw = kDot + 2, kEpi, kEnd, kBars };
 
 template <int D>
 struct Smem {
@@ -54,9 +55,10 @@ struct Smem {
     unsigned char k[D / 64][kC * 128], q[D / 64][kC * 128];
     unsigned char pe[2][2][kC * 128];        // hi, lo: rows of dP, rows of E
     unsigned char ring[2][D * kE * 2];       // one part of a state: [d / 8][e][8]
-    float f[kFactors][kC];                   // factors of the epilogue's item
+    float f[2][kFactors][kC];                // factors, by item parity
     float dbeta[2][kC], xv[2][kC];           // row sums, by item parity
-    float part[4][kC], dG[kC];
+    float part[2][4][kC];                    // q . dq of a quadrant's rows of d, by item parity
+    float dot[2];                            // warp 2's half of <dS1, S1>, by item parity
     unsigned long long bar[kBars];
     uint32_t tmem;
     int abort;
@@ -80,7 +82,7 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap md, int* status) {
     extern __shared__ __align__(1024) unsigned char grad_tc_raw[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(grad_tc_raw);
-    constexpr uint32_t kTile = kC * 128, kPart = D * kE * 2;
+    constexpr uint32_t kTile = kC * 128, kPiece = D * kE * 2;
     constexpr uint32_t cPE = 0, cA = 128, cB = 256, cC = 384;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rep = A.H / A.Hk;
@@ -97,6 +99,12 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
         mbar_init(bar(kXU), kRowWarps);
         mbar_init(bar(kSums), kRowWarps);
         mbar_init(bar(kSums + 1), kRowWarps);
+        mbar_init(bar(kSumsFree), 1);
+        mbar_init(bar(kSumsFree + 1), 1);
+        for (int z = 0; z < 2; ++z) {
+            mbar_init(bar(kPart + z), kEpiWarps);
+            mbar_init(bar(kDot + z), 1);
+        }
         mbar_init(bar(kPEFull), kEpiWarps);
         mbar_init(bar(kFree), kEpiWarps);
         mbar_init(bar(kEpi), kEpiWarps);
@@ -118,7 +126,7 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
 
     // Item -> chunk of a key head (consecutive items of a CTA step through the value heads of one)
     struct Item {
-        int b, hk, h, c, hh, len;
+        int b, hk, h, c, hh, len, u;
     };
     const int units = items / rep;
     const int mine = (units - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
@@ -129,6 +137,7 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
         x.hk = u / chunks % A.Hk;
         x.b = u / chunks / A.Hk;
         x.hh = hh;
+        x.u = unit;
         x.h = x.hk * rep + hh;
         x.len = length_of(A, x.b);
         return x;
@@ -166,8 +175,8 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                 const __nv_bfloat16* from = z < 2 ? in.S0 + (seq * (chunks + 1) + x.c) * 2 * page + z * page
                                                   : in.dS1 + cn * 2 * page + (z - 2) * page;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(bar(kRing + s), kPart);
-                    bulk_load(smem_addr(sm.ring[s]), from, kPart, bar(kRing + s));
+                    mbar_arrive_expect_tx(bar(kRing + s), kPiece);
+                    bulk_load(smem_addr(sm.ring[s]), from, kPiece, bar(kRing + s));
                 }
                 pieces = p + 1;
                 return true;
@@ -289,6 +298,80 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
         });
         if (elect()) mma_commit(bar(kEnd));
         mbar_wait(bar(kEnd), 0);
+    } else if (warp < 4) {
+        each([&](const Item& x, int y) {
+            const int t0 = x.c * kC, t = 2 * lane;
+            const size_t seq = static_cast<size_t>(x.b) * A.H + x.h, page = static_cast<size_t>(D) * kE;
+            // <dS1, S1>, half of the 16-byte pieces: warp 2 and warp 3 take turns of 32
+            const uint4* s1 = reinterpret_cast<const uint4*>(in.S0 + (seq * (chunks + 1) + x.c + 1) * 2 * page);
+            const uint4* d1 = reinterpret_cast<const uint4*>(in.dS1 + (seq * chunks + x.c) * 2 * page);
+            constexpr int kPieces = D * kE / 8;  // of one part
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+            for (int z = (warp - 2) * 32 + lane; z < kPieces; z += 4 * 64) {
+                uint4 v[4][4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    v[r][0] = s1[z + 64 * r];
+                    v[r][1] = s1[z + 64 * r + kPieces];
+                    v[r][2] = d1[z + 64 * r];
+                    v[r][3] = d1[z + 64 * r + kPieces];
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const auto take = [&](uint32_t sh, uint32_t sl, uint32_t dh, uint32_t dl) {
+                        const float2 s2 = make_float2(low_of(sh) + low_of(sl), high_of(sh) + high_of(sl));
+                        const float2 d2 = make_float2(low_of(dh) + low_of(dl), high_of(dh) + high_of(dl));
+                        sum = fma2(s2, d2, sum);
+                    };
+                    take(v[r][0].x, v[r][1].x, v[r][2].x, v[r][3].x);
+                    take(v[r][0].y, v[r][1].y, v[r][2].y, v[r][3].y);
+                    take(v[r][0].z, v[r][1].z, v[r][2].z, v[r][3].z);
+                    take(v[r][0].w, v[r][1].w, v[r][2].w, v[r][3].w);
+                }
+            }
+            float dot = sum.x + sum.y;
+#pragma unroll
+            for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+            if (warp == 2) {
+                // (warp 3 has left the item before the last one: kSumsFree)
+                if (y >= 2 && !wait(kSumsFree + (y & 1), (y >> 1) - 1)) return false;
+                if (lane == 0) {
+                    sm.dot[y & 1] = dot;
+                    arrive(bar(kDot + (y & 1)));
+                }
+                return true;
+            }
+            if (!(wait(kPart + (y & 1), y >> 1) && wait(kDot + (y & 1), y >> 1) && wait(kSums + (y & 1), y >> 1))) return false;
+            // sums of dL/dG from each row to the chunk's end: two rows per lane
+            const float(*part)[kC] = sm.part[y & 1];
+            const float* xv = sm.xv[y & 1];
+            float y0 = part[0][t] + part[1][t] + part[2][t] + part[3][t] - xv[t];
+            float y1 = part[0][t + 1] + part[1][t + 1] + part[2][t + 1] + part[3][t + 1] - xv[t + 1];
+            // (the rows of dO behind the end are whatever lies there)
+            if (t0 + t >= x.len) y0 = 0.f;
+            if (t0 + t + 1 >= x.len) y1 = 0.f;
+            if (lane == 31) y1 += dot + sm.dot[y & 1];
+            float s = y0 + y1;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const float z = __shfl_down_sync(0xffffffffu, s, m);
+                if (lane + m < 32) s += z;
+            }
+            const float db0 = sm.dbeta[y & 1][t], db1 = sm.dbeta[y & 1][t + 1];
+            __syncwarp();
+            if (lane == 0) arrive(bar(kSumsFree + (y & 1)));
+            const size_t at = row_at(A, x.b, x.h, A.H, t0 + t, 1), next = at + (A.bthd ? A.H : 1);
+            if (t0 + t < x.len) {
+                if (A.dg) A.dg[at] = s;
+                A.dbeta[at] = db0;
+            }
+            if (t0 + t + 1 < x.len) {
+                if (A.dg) A.dg[next] = s - y0;
+                A.dbeta[next] = db1;
+            }
+            return true;
+        });
     } else if (warp >= 4 && warp < 12) {
         const int quad = warp & 3, half = (warp - 4) >> 2, g = lane >> 2, i = lane & 3;
         const uint32_t row = static_cast<uint32_t>(32 * quad) << 16;
@@ -302,15 +385,31 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
         };
         // sums over the value heads of a key head, between two of its items: this thread's dq and dk, a value per 256
         float* sums = in.sums + static_cast<size_t>(blockIdx.x) * (2 * kHalves * 16 * 32 * kEpiWarps) + (tid - 128);
-        each([&](const Item& x, int y) {
+        // factors of the item that begins at or behind (u, hh), into registers and from there into f[y & 1]
+        float fac[3];
+        const auto fetch = [&](int u, int hh) {
+            while (u < mine && item_at(u, 0).c * kC >= item_at(u, 0).len) ++u;
+            if (u >= mine) return;
+            const Item x = item_at(u, hh);
+            const float* from = ws[(static_cast<size_t>(x.b) * A.H + x.h) * chunks + x.c].eg;
+#pragma unroll
+            for (int z = 0; z < 3; ++z)
+                if (tid - 128 + z * 32 * kEpiWarps < kFactors * kC) fac[z] = from[tid - 128 + z * 32 * kEpiWarps];
+        };
+        const auto store = [&](int y) {
+#pragma unroll
+            for (int z = 0; z < 3; ++z)
+                if (tid - 128 + z * 32 * kEpiWarps < kFactors * kC) sm.f[y & 1][0][tid - 128 + z * 32 * kEpiWarps] = fac[z];
+        };
+        fetch(0, 0);
+        store(0);
+        if (meet()) each([&](const Item& x, int y) {
             const int t0 = x.c * kC;
-            const float *eg = sm.f[0], *rest = sm.f[1], *neg_beta = sm.f[4], *neg_beta_eg = sm.f[6];
-            const float *G = sm.f[7], *Gl = sm.f[8];
-            {  // the item before is left behind (the barrier at its end)
-                const float* from = ws[(static_cast<size_t>(x.b) * A.H + x.h) * chunks + x.c].eg;
-                for (int z = tid - 128; z < kFactors * kC; z += 32 * kEpiWarps) sm.f[0][z] = from[z];
-            }
-            if (!(meet() && wait(kPE, y))) return false;
+            const float(*f)[kC] = sm.f[y & 1];
+            const float *eg = f[0], *rest = f[1], *neg_beta = f[4], *neg_beta_eg = f[6], *G = f[7], *Gl = f[8];
+            if (x.hh + 1 < rep) fetch(x.u, x.hh + 1);
+            else fetch(x.u + 1, 0);
+            if (!wait(kPE, y)) return false;
             tc_fence_after();
             {  // rows 0 .. 63: dP, 64 .. 127: E; this thread's row, columns r0 ..
                 const int r = 32 * quad + lane, t = r & 63;
@@ -351,7 +450,7 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) arrive(bar(kPEFull));
-            if (!(wait(kDone, y) && wait(kKQ, y) && wait(kSums + (y & 1), y >> 1))) return false;
+            if (!(wait(kDone, y) && wait(kKQ, y) && (y < 2 || wait(kSumsFree + (y & 1), (y >> 1) - 1)))) return false;
             tc_fence_after();
             // dq and dk of this item: rows 16 hb + g (+ 8) of d in this quadrant, columns 8 j + 2 i (+ 1) of this half
             const auto load = [&](uint32_t col, float (&to)[32]) {
@@ -363,9 +462,9 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             const int d_at = (D / 4) * quad, left = x.len - t0;
             const size_t out_at = row_at(A, x.b, x.hk, A.Hk, t0, D) + d_at;
             float a[32];
-            float now[kHalves * 16];
-            // `now` (dq: o = 0, dk: o = 1) added to the heads before, and kept or written out
-            const auto finish = [&](int o, void* out) {
+            float nq[kHalves * 16], nk[kHalves * 16];  // dq and dk of this item
+            // dq (o = 0) or dk (o = 1) added to the heads before, and kept or written out
+            const auto finish = [&](float (&now)[kHalves * 16], int o, void* out) {
                 float* sum = sums + o * (kHalves * 16 * 32 * kEpiWarps);
                 if (!first)
 #pragma unroll
@@ -407,15 +506,31 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                     }
                 }
             };
+            const auto factor = [&](const float* of, int z) { return of[r0 + 8 * (z / 4 % 4) + 2 * i + (z & 1)]; };
             load(cA, a);
 #pragma unroll
-            for (int z = 0; z < kHalves * 16; ++z) {
-                const int t = r0 + 8 * (z / 4 % 4) + 2 * i + (z & 1);
-                now[z] = a[z] * eg[t];
-            }
+            for (int z = 0; z < kHalves * 16; ++z) nq[z] = a[z] * factor(eg, z);
             load(cB, a);
 #pragma unroll
-            for (int z = 0; z < kHalves * 16; ++z) now[z] += a[z];
+            for (int z = 0; z < kHalves * 16; ++z) nq[z] += a[z];
+            load(cC, a);
+#pragma unroll
+            for (int z = 0; z < kHalves * 16; ++z) nk[z] = a[z] * factor(rest, z);
+            load(cC + 64, a);
+#pragma unroll
+            for (int z = 0; z < kHalves * 16; ++z) nk[z] = fmaf(a[z], factor(rest, z), nk[z]);
+            load(cA + 64, a);
+#pragma unroll
+            for (int z = 0; z < kHalves * 16; ++z) nk[z] = fmaf(a[z], factor(neg_beta_eg, z), nk[z]);
+            load(cB + 64, a);
+#pragma unroll
+            for (int z = 0; z < kHalves * 16; ++z) nk[z] += a[z];
+            load(cPE, a);
+#pragma unroll
+            for (int z = 0; z < kHalves * 16; ++z) nk[z] += a[z];
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(bar(kFree));  // the accumulators are read out: the next item's products may begin
             {  // q . dq: this warp's rows of d, summed over the lanes that share columns
                 float s[8] = {};
 #pragma unroll
@@ -423,88 +538,39 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
 #pragma unroll
                     for (int jp = 0; jp < 2; ++jp) {
                         // fragments of Q^T: rows of d, columns t, of tiles 2 jp and 2 jp + 1
-                        const int d0 = (D / 4) * quad + 16 * hb, m = lane >> 3;
+                        const int d0 = d_at + 16 * hb, m = lane >> 3;
                         uint32_t qq[4];
                         ldsm_t(qq, smem_addr(sm.q[d0 >> 6]) +
                                        piece<128>(r0 + 8 * (2 * jp + (m >> 1)) + (lane & 7), ((d0 & 63) >> 3) + (m & 1)));
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
                             const int at = 16 * hb + 4 * (2 * jp + z), j = 2 * (2 * jp + z);
-                            s[j] = fmaf(low_of(qq[2 * z]), now[at], fmaf(low_of(qq[2 * z + 1]), now[at + 2], s[j]));
-                            s[j + 1] = fmaf(high_of(qq[2 * z]), now[at + 1], fmaf(high_of(qq[2 * z + 1]), now[at + 3], s[j + 1]));
+                            s[j] = fmaf(low_of(qq[2 * z]), nq[at], fmaf(low_of(qq[2 * z + 1]), nq[at + 2], s[j]));
+                            s[j + 1] = fmaf(high_of(qq[2 * z]), nq[at + 1], fmaf(high_of(qq[2 * z + 1]), nq[at + 3], s[j + 1]));
                         }
                     }
+                // 8 sums over the 8 lanes of equal i, halving what a lane holds: lane g ends with sum g
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int m = 16, held = 4; m >= 4; m >>= 1, held >>= 1)
 #pragma unroll
-                    for (int m = 4; m < 32; m <<= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], m);
-                    if (g == 0) sm.part[quad][r0 + 8 * (j >> 1) + 2 * i + (j & 1)] = s[j];
-                }
+                    for (int z = 0; z < 4; ++z)
+                        if (z < held) {
+                            const bool up = lane & m;
+                            const float give = up ? s[z] : s[held + z], keep = up ? s[held + z] : s[z];
+                            s[z] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+                        }
+                sm.part[y & 1][quad][r0 + 8 * (g >> 1) + 2 * i + (g & 1)] = s[0];
             }
-            finish(0, A.dq);
-            load(cA + 64, a);
-#pragma unroll
-            for (int z = 0; z < kHalves * 16; ++z) {
-                const int t = r0 + 8 * (z / 4 % 4) + 2 * i + (z & 1);
-                now[z] = a[z] * neg_beta_eg[t];
-            }
-            load(cB + 64, a);
-#pragma unroll
-            for (int z = 0; z < kHalves * 16; ++z) now[z] += a[z];
-            load(cPE, a);
-#pragma unroll
-            for (int z = 0; z < kHalves * 16; ++z) now[z] += a[z];
-            load(cC, a);
-#pragma unroll
-            for (int z = 0; z < kHalves * 16; ++z) {
-                const int t = r0 + 8 * (z / 4 % 4) + 2 * i + (z & 1);
-                now[z] = fmaf(a[z], rest[t], now[z]);
-            }
-            load(cC + 64, a);
-#pragma unroll
-            for (int z = 0; z < kHalves * 16; ++z) {
-                const int t = r0 + 8 * (z / 4 % 4) + 2 * i + (z & 1);
-                now[z] = fmaf(a[z], rest[t], now[z]);
-            }
-            finish(1, A.dk);
-            tc_fence_before();
-            if (!meet()) return false;  // q . dq is complete
-            if (warp == 4) {  // sums of dL/dG from each row to the chunk's end: two rows per lane
-                const int t = 2 * lane;
-                const size_t seq = static_cast<size_t>(x.b) * A.H + x.h;
-                const float* xv = sm.xv[y & 1];
-                float y0 = sm.part[0][t] + sm.part[1][t] + sm.part[2][t] + sm.part[3][t] - xv[t];
-                float y1 = sm.part[0][t + 1] + sm.part[1][t + 1] + sm.part[2][t + 1] + sm.part[3][t + 1] - xv[t + 1];
-                // (the rows of dO behind the end are whatever lies there)
-                if (t0 + t >= x.len) y0 = 0.f;
-                if (t0 + t + 1 >= x.len) y1 = 0.f;
-                if (lane == 31) {
-                    const float* dot = in.dot + (seq * chunks + x.c) * 4;
-                    y1 += (dot[0] + dot[1]) + (dot[2] + dot[3]);
-                }
-                float s = y0 + y1;
-#pragma unroll
-                for (int m = 1; m < 32; m <<= 1) {
-                    const float z = __shfl_down_sync(0xffffffffu, s, m);
-                    if (lane + m < 32) s += z;
-                }
-                const size_t at = row_at(A, x.b, x.h, A.H, t0 + t, 1), next = row_at(A, x.b, x.h, A.H, t0 + t + 1, 1);
-                if (t0 + t < x.len) {
-                    if (A.dg) A.dg[at] = s;
-                    A.dbeta[at] = sm.dbeta[y & 1][t];
-                }
-                if (t0 + t + 1 < x.len) {
-                    if (A.dg) A.dg[next] = s - y0;
-                    A.dbeta[next] = sm.dbeta[y & 1][t + 1];
-                }
-            }
-            // accumulators, K, Q, dP and E, the factors and the row sums of this item are read out
-            if (!meet()) return false;
+            __syncwarp();
             if (lane == 0) {
+                arrive(bar(kPart + (y & 1)));
                 arrive(bar(kKQFree));
-                arrive(bar(kFree));
             }
-            return true;
+            finish(nq, 0, A.dq);
+            finish(nk, 1, A.dk);
+            store(y + 1);
+            // what was staged in the place of dP and E is read out, and the next item's factors are there
+            return meet();
         });
     } else if (warp >= 12) {
         const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(A.v);
@@ -531,9 +597,9 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                         bt[r] = cw.beta[t];
                     }
                 }
-                // The MMAs have read the operands of the item before.  They began when the epilogue had left the item
-                // before that one, whose buffer of row sums is written now.
+                // the MMAs have read the operands of the item before, warp 3 the row sums of the one before that
                 if (z == 0 && y > 0 && !wait(kXUFree, y - 1)) return false;
+                if (z == 0 && y > 1 && !wait(kSumsFree + (y & 1), (y >> 1) - 1)) return false;
                 float sum[16];  // of each row: x . w, x . v
                 const int row0 = 16 * (warp - 12) + 8 * z;
 #pragma unroll

@@ -22,8 +22,8 @@
 //
 // Warps (16): 0 loads (TMA tiles, bulk copies of what gdr_prep left), 1 issues
 // the MMAs, 2 owns the TMEM allocation; 4-7 and 8-11 are the chain's epilogue,
-// half of the columns each; 12-15 do what is off the chain (the output; the copy
-// of the state for the backward; the operand e^G dO).
+// half of the columns each; 12-15 do what is off the chain (the output; the operand
+// e^G dO).
 //
 // Every wait is bounded (two seconds); a role that gives up raises the CTA's
 // abort flag, all leave their loops, copies and MMAs in flight are waited for
@@ -53,7 +53,7 @@ struct Stage {  // 1024-byte aligned; tiles of 64 rows x 64 columns (128 bytes, 
     unsigned char pad[2048 - kCoefs * kC * 4];
 };
 
-enum Bar { kFull = 0, kEmpty = 2, kState = 4, kFullP = 6, kEmptyP = 8, kD1 = 10, kZ, kW, kU, kUp, kS, kScaled, kD2Free, kO, kOFree, kSide, kSaved, kRaw, kEnd, kBars };
+enum Bar { kFull = 0, kEmpty = 2, kState = 4, kFullP = 6, kEmptyP = 8, kD1 = 10, kZ, kW, kU, kUp, kS, kScaled, kD2Free, kO, kOFree, kSide, kRaw, kEnd, kBars };
 
 template <int D>
 struct Smem {
@@ -168,7 +168,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
         }
         for (int i : {kD1, kW, kS, kO, kRaw, kEnd}) mbar_init(bar(i), 1);
         for (int i : {kState + 0, kState + 1, int(kZ), int(kU), int(kUp), int(kScaled)}) mbar_init(bar(i), kChainWarps);
-        for (int i : {kD2Free, kOFree, kSide, kSaved}) mbar_init(bar(i), kSideWarps);
+        for (int i : {kD2Free, kOFree, kSide}) mbar_init(bar(i), kSideWarps);
         fence_mbar_init();
     }
     if (warp == 2) {
@@ -407,6 +407,16 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
             }
             done(kScaled);
         };
+        // 32 columns of d of the state (its two parts) to memory, in Saved's layout: each lane's 16 bytes next to the
+        // neighbouring lanes'.  `at`: forward, the chunk that the state enters; backward, the one whose dS1 it is.
+        const auto keep = [&](const uint32_t (&w)[32], int q, int at) {
+            __nv_bfloat16* to = (kRev ? out.dS1 + (static_cast<size_t>(n) * chunks + at) * 2 * page
+                                      : out.S0 + (static_cast<size_t>(n) * (chunks + 1) + at) * 2 * page) + e * 8;
+#pragma unroll
+            for (int x = 0; x < 32; x += 4)
+                *reinterpret_cast<uint4*>(to + (x >> 4) * page + (4 * q + (x & 15) / 4) * (kE * 8)) =
+                    make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
+        };
         bool ok = nc > 0;
 #pragma unroll 1
         for (int y = 0; y < kGroups; ++y) {
@@ -420,6 +430,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
                 split32(S, w);
                 tmem_st32u(row + cB + 32 * q, w);
                 done(kState + y);
+                if (kMode != kForward) keep(w, q, kRev ? nc - 1 : 0);
             } else if (last) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) last[static_cast<size_t>(32 * q + i) * kE + e] = S[i];
@@ -506,10 +517,9 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
             }
             __syncwarp();
             if (lane == 0) arrive(bar(kEmpty + s));  // this stage's rows and factors are read out
-            if (kMode != kForward && !(ok = wait(kSaved, it))) break;
             if (!(ok = wait(kS, it))) break;
             tc_fence_after();
-            if (it + 1 < nc) {
+            if (it + 1 < nc || kMode == kSave) {
 #pragma unroll
                 for (int y = 0; y < kGroups; ++y) {
                     const int q = half * kGroups + y;
@@ -517,22 +527,11 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
                     uint32_t w[32];
                     tmem_ld32(row + cS + 32 * q, S);
                     split32(S, w);
-                    tmem_st32u(row + cB + 32 * q, w);
-                    done(kState + y);
-                }
-            } else if (kMode == kSave) {
-                __nv_bfloat16* to = out.S0 + (static_cast<size_t>(n) * (chunks + 1) + nc) * 2 * page + e * 8;
-#pragma unroll 1
-                for (int y = 0; y < kGroups; ++y) {
-                    const int q = half * kGroups + y;
-                    float S[32];
-                    uint32_t w[32];
-                    tmem_ld32(row + cS + 32 * q, S);
-                    split32(S, w);
-#pragma unroll
-                    for (int x = 0; x < 32; x += 4)
-                        *reinterpret_cast<uint4*>(to + (x >> 4) * page + (4 * q + (x & 15) / 4) * (kE * 8)) =
-                            make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
+                    if (it + 1 < nc) {
+                        tmem_st32u(row + cB + 32 * q, w);
+                        done(kState + y);
+                    }
+                    if (kMode != kForward) keep(w, q, kRev ? c - 1 : c + 1);
                 }
             } else if (last) {
 #pragma unroll 1
@@ -655,55 +654,6 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
             }
             __syncwarp();
             if (lane == 0) arrive(bar(kEmpty + s));
-            // the state (forward: before the chunk, backward: the gradient after it) to memory (Saved's layout)
-            uint4 s1[2][8];  // 32 columns of d of S1, high and low, and the 32 after them
-            const __nv_bfloat16* after = out.S0 + (static_cast<size_t>(n) * (chunks + 1) + c + 1) * 2 * page + e * 8;
-            const auto load_s1 = [&](int q) {
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    s1[q & 1][x] = *reinterpret_cast<const uint4*>(after + (x >> 2) * page + (4 * q + (x & 3)) * (kE * 8));
-            };
-            if (kRev) {
-                load_s1(0);
-                load_s1(1);
-            }
-            if (!(wait(kState, it) && (D == 64 || wait(kState + 1, it)))) break;
-            tc_fence_after();
-            __nv_bfloat16* to = (kRev ? out.dS1 + (static_cast<size_t>(n) * chunks + c) * 2 * page
-                                      : out.S0 + (static_cast<size_t>(n) * (chunks + 1) + c) * 2 * page) + e * 8;
-            float dot = 0.f;
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-                float w[32];
-                tmem_ld32(row + cB + 32 * q, w);
-#pragma unroll
-                for (int x = 0; x < 32; x += 4)  // 8 columns of d: 16 bytes next to the neighbouring lanes'
-                    *reinterpret_cast<uint4*>(to + (x >> 4) * page + (4 * q + (x & 15) / 4) * (kE * 8)) =
-                        make_uint4(__float_as_uint(w[x]), __float_as_uint(w[x + 1]), __float_as_uint(w[x + 2]),
-                                   __float_as_uint(w[x + 3]));
-                if (kRev) {  // <dS1, S1>: the state after this chunk as the forward walk left it
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint4 yh = s1[q & 1][x], yl = s1[q & 1][4 + x];
-                        const uint32_t h4[4] = {yh.x, yh.y, yh.z, yh.w}, l4[4] = {yl.x, yl.y, yl.z, yl.w};
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const uint32_t dh = __float_as_uint(w[4 * x + y]), dl = __float_as_uint(w[16 + 4 * x + y]);
-                            dot = fmaf(low_of(dh) + low_of(dl), low_of(h4[y]) + low_of(l4[y]), dot);
-                            dot = fmaf(high_of(dh) + high_of(dl), high_of(h4[y]) + high_of(l4[y]), dot);
-                        }
-                    }
-                    if (q + 2 < D / 32) load_s1(q + 2);
-                }
-            }
-            if (kRev) {
-#pragma unroll
-                for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-                if (lane == 0) out.dot[(static_cast<size_t>(n) * chunks + c) * 4 + (warp & 3)] = dot;
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive(bar(kSaved));
         }
     }
     __syncwarp();
