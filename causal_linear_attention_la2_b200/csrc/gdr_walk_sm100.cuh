@@ -91,6 +91,22 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 
+// The timer is read every 64 tries only: reading it takes longer than most waits.
+__device__ __noinline__ bool wait_slow(uint32_t b, uint32_t parity, int where, volatile int* abort, int* status) {
+    uint64_t t0 = 0;
+    for (uint32_t tries = 1;; ++tries) {
+        if (mbar_try_wait(b, parity)) return true;
+        if (tries % 64) continue;
+        if (*abort) return false;
+        if (!t0) t0 = global_ns();
+        if (global_ns() - t0 > 2000000000ull) {
+            *abort = 1;
+            atomicCAS(status, 0, 5 | ((200 + where) << 8));
+            return false;
+        }
+    }
+}
+
 struct Waiter {
     uint32_t bars;
     volatile int* abort;
@@ -99,23 +115,8 @@ struct Waiter {
     __device__ __forceinline__ bool operator()(int bar, uint32_t parity) const {
         const uint32_t b = bars + 8 * bar;
         bool ok = mbar_try_wait(b, parity & 1);
-        if (!__all_sync(0xffffffffu, ok)) ok = slow(b, parity & 1, bar);
+        if (!__all_sync(0xffffffffu, ok)) ok = wait_slow(b, parity & 1, bar, abort, status);
         return __all_sync(0xffffffffu, ok);
-    }
-    // The timer is read every 64 tries only: reading it takes longer than most waits.
-    __device__ __noinline__ bool slow(uint32_t b, uint32_t parity, int where) const {
-        uint64_t t0 = 0;
-        for (uint32_t tries = 1;; ++tries) {
-            if (mbar_try_wait(b, parity)) return true;
-            if (tries % 64) continue;
-            if (*abort) return false;
-            if (!t0) t0 = global_ns();
-            if (global_ns() - t0 > 2000000000ull) {
-                *abort = 1;
-                atomicCAS(status, 0, 5 | ((200 + where) << 8));
-                return false;
-            }
-        }
     }
 };
 
@@ -520,7 +521,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
             if (!(ok = wait(kS, it))) break;
             tc_fence_after();
             if (it + 1 < nc || kMode == kSave) {
-#pragma unroll
+#pragma unroll 1
                 for (int y = 0; y < kGroups; ++y) {
                     const int q = half * kGroups + y;
                     float S[32];
