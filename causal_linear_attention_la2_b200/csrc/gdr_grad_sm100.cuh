@@ -7,11 +7,10 @@
 //   dq^T = S0 dO^T diag(e^G) + K^T dP^T
 //   dk^T = -S0 X^T diag(beta e^G) + K^T E^T + K^T E + Q^T dP + dS1 U^T diag(e^{G_C - G})
 //   dv = beta x,   dbeta_t = x_t . w_t
-//   dL/dG_t = q_t . dq_t - v_t . dv_t, and <dS1, S1> more in the chunk's last row;
-//   dg: sums of dL/dG from a row to the chunk's end.
-// (dL/dG_t: gating position t scales the state, which dq_t and the outputs read,
-// and nothing but the state enters v_t . dv_t = beta_t v_t . x_t; of the four terms
-// of gdr_rec.cuh's form k_t . row_t - k_t . col_t is -beta_t x_t . v_t.)
+//   dL/dG_t = q_t . dq_t + beta_t x_t . (w_t - v_t) - k_t . col_t, col the last three terms of dk,
+//   and <dS1, S1> more in the chunk's last row; dg: sums of dL/dG from a row to the chunk's end.
+// (k_t . col_t is x_t . u_t, so dL/dG_t = q_t . dq_t - v_t . dv_t; but computed from that, what
+// x_t is off by is not taken out again, and dg is off by 1.5e-5 instead of 6e-6 of its norm.)
 //
 // The products run with d on the TMEM lanes (M = d; 128 rows for dP and E, which
 // are made together as [dO; X] U^T).  The scales of single rows are applied when
@@ -57,7 +56,7 @@ struct Smem {
     unsigned char ring[2][D * kE * 2];       // one part of a state: [d / 8][e][8]
     float f[2][kFactors][kC];                // factors, by item parity
     float dbeta[2][kC], xv[2][kC];           // row sums, by item parity
-    float part[2][4][kC];                    // q . dq of a quadrant's rows of d, by item parity
+    float part[2][4][kC];                    // q . dq - k . col of a quadrant's rows of d, by item parity
     float dot[2];                            // warp 2's half of <dS1, S1>, by item parity
     unsigned long long bar[kBars];
     uint32_t tmem;
@@ -74,6 +73,22 @@ __device__ __forceinline__ uint64_t sdesc_blocks(uint32_t addr, uint32_t mn) {
     d |= static_cast<uint64_t>((mn >> 4) & 0x3FFFu) << 32;
     d |= static_cast<uint64_t>(1) << 46;
     return d;
+}
+
+// 16 lanes x 32 columns of TMEM as fragments (the layout of ptx_sm100.cuh's pair of
+// such loads), waited for in the same statement
+__device__ __forceinline__ void tmem_frag(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 template <int D>
@@ -346,8 +361,8 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             // sums of dL/dG from each row to the chunk's end: two rows per lane
             const float(*part)[kC] = sm.part[y & 1];
             const float* xv = sm.xv[y & 1];
-            float y0 = part[0][t] + part[1][t] + part[2][t] + part[3][t] - xv[t];
-            float y1 = part[0][t + 1] + part[1][t + 1] + part[2][t + 1] + part[3][t + 1] - xv[t + 1];
+            float y0 = part[0][t] + part[1][t] + part[2][t] + part[3][t] + xv[t];
+            float y1 = part[0][t + 1] + part[1][t + 1] + part[2][t + 1] + part[3][t + 1] + xv[t + 1];
             // (the rows of dO behind the end are whatever lies there)
             if (t0 + t >= x.len) y0 = 0.f;
             if (t0 + t + 1 >= x.len) y1 = 0.f;
@@ -453,16 +468,30 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             if (!(wait(kDone, y) && wait(kKQ, y) && (y < 2 || wait(kSumsFree + (y & 1), (y >> 1) - 1)))) return false;
             tc_fence_after();
             // dq and dk of this item: rows 16 hb + g (+ 8) of d in this quadrant, columns 8 j + 2 i (+ 1) of this half
-            const auto load = [&](uint32_t col, float (&to)[32]) {
-                // D = 64: M = 64 puts 16 rows into each quadrant; the second half is not used
-                tmem_ld16x256b_x4_pair(row + col + r0, row + col + r0 + (kHalves == 2 ? 16u << 16 : 0u), to);
+            // (D = 64: M = 64 puts 16 rows into each quadrant)
+            // of += (factor of the column) accumulator, column block `col`
+            const auto add = [&](uint32_t col, float (&of)[kHalves * 16], const float* f2) {
+#pragma unroll
+                for (int hb = 0; hb < kHalves; ++hb) {
+                    float a[16];
+                    tmem_frag(row + col + r0 + (static_cast<uint32_t>(16 * hb) << 16), a);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float2 m = make_float2(1.f, 1.f);
+                        if (f2) m = *reinterpret_cast<const float2*>(f2 + r0 + 8 * j + 2 * i);
+#pragma unroll
+                        for (int z = 4 * j; z < 4 * j + 4; z += 2) {
+                            of[16 * hb + z] = fmaf(a[z], m.x, of[16 * hb + z]);
+                            of[16 * hb + z + 1] = fmaf(a[z + 1], m.y, of[16 * hb + z + 1]);
+                        }
+                    }
+                }
             };
             const bool first = x.hh == 0, last_head = x.hh == rep - 1;
             const size_t step = A.bthd ? static_cast<size_t>(A.Hk) * D : D;
             const int d_at = (D / 4) * quad, left = x.len - t0;
             const size_t out_at = row_at(A, x.b, x.hk, A.Hk, t0, D) + d_at;
-            float a[32];
-            float nq[kHalves * 16], nk[kHalves * 16];  // dq and dk of this item
+            float nq[kHalves * 16] = {}, nk[kHalves * 16] = {};  // dq and dk of this item
             // dq (o = 0) or dk (o = 1) added to the heads before, and kept or written out
             const auto finish = [&](float (&now)[kHalves * 16], int o, void* out) {
                 float* sum = sums + o * (kHalves * 16 * 32 * kEpiWarps);
@@ -506,49 +535,39 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                     }
                 }
             };
-            const auto factor = [&](const float* of, int z) { return of[r0 + 8 * (z / 4 % 4) + 2 * i + (z & 1)]; };
-            load(cA, a);
-#pragma unroll
-            for (int z = 0; z < kHalves * 16; ++z) nq[z] = a[z] * factor(eg, z);
-            load(cB, a);
-#pragma unroll
-            for (int z = 0; z < kHalves * 16; ++z) nq[z] += a[z];
-            load(cC, a);
-#pragma unroll
-            for (int z = 0; z < kHalves * 16; ++z) nk[z] = a[z] * factor(rest, z);
-            load(cC + 64, a);
-#pragma unroll
-            for (int z = 0; z < kHalves * 16; ++z) nk[z] = fmaf(a[z], factor(rest, z), nk[z]);
-            load(cA + 64, a);
-#pragma unroll
-            for (int z = 0; z < kHalves * 16; ++z) nk[z] = fmaf(a[z], factor(neg_beta_eg, z), nk[z]);
-            load(cB + 64, a);
-#pragma unroll
-            for (int z = 0; z < kHalves * 16; ++z) nk[z] += a[z];
-            load(cPE, a);
-#pragma unroll
-            for (int z = 0; z < kHalves * 16; ++z) nk[z] += a[z];
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive(bar(kFree));  // the accumulators are read out: the next item's products may begin
-            {  // q . dq: this warp's rows of d, summed over the lanes that share columns
-                float s[8] = {};
+            add(cC, nk, rest);
+            add(cC + 64, nk, rest);
+            add(cPE, nk, nullptr);
+            float s[8] = {};  // of columns 8 (j / 2) + 2 i + j % 2: this warp's rows of d of q . dq - k . col
+            const auto along = [&](const unsigned char (*rows)[kC * 128], const float (&of)[kHalves * 16], float sign) {
 #pragma unroll
                 for (int hb = 0; hb < kHalves; ++hb)
 #pragma unroll
                     for (int jp = 0; jp < 2; ++jp) {
-                        // fragments of Q^T: rows of d, columns t, of tiles 2 jp and 2 jp + 1
+                        // fragments of the transposed tile: rows of d, columns t, of tiles 2 jp and 2 jp + 1
                         const int d0 = d_at + 16 * hb, m = lane >> 3;
                         uint32_t qq[4];
-                        ldsm_t(qq, smem_addr(sm.q[d0 >> 6]) +
+                        ldsm_t(qq, smem_addr(rows[d0 >> 6]) +
                                        piece<128>(r0 + 8 * (2 * jp + (m >> 1)) + (lane & 7), ((d0 & 63) >> 3) + (m & 1)));
 #pragma unroll
                         for (int z = 0; z < 2; ++z) {
                             const int at = 16 * hb + 4 * (2 * jp + z), j = 2 * (2 * jp + z);
-                            s[j] = fmaf(low_of(qq[2 * z]), nq[at], fmaf(low_of(qq[2 * z + 1]), nq[at + 2], s[j]));
-                            s[j + 1] = fmaf(high_of(qq[2 * z]), nq[at + 1], fmaf(high_of(qq[2 * z + 1]), nq[at + 3], s[j + 1]));
+                            s[j] = fmaf(sign * low_of(qq[2 * z]), of[at], fmaf(sign * low_of(qq[2 * z + 1]), of[at + 2], s[j]));
+                            s[j + 1] = fmaf(sign * high_of(qq[2 * z]), of[at + 1],
+                                            fmaf(sign * high_of(qq[2 * z + 1]), of[at + 3], s[j + 1]));
                         }
                     }
+            };
+            along(sm.k, nk, -1.f);
+            add(cA + 64, nk, neg_beta_eg);
+            add(cB + 64, nk, nullptr);
+            add(cA, nq, eg);
+            add(cB, nq, nullptr);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(bar(kFree));  // the accumulators are read out: the next item's products may begin
+            {
+                along(sm.q, nq, 1.f);
                 // 8 sums over the 8 lanes of equal i, halving what a lane holds: lane g ends with sum g
 #pragma unroll
                 for (int m = 16, held = 4; m >= 4; m >>= 1, held >>= 1)
@@ -600,7 +619,7 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                 // the MMAs have read the operands of the item before, warp 3 the row sums of the one before that
                 if (z == 0 && y > 0 && !wait(kXUFree, y - 1)) return false;
                 if (z == 0 && y > 1 && !wait(kSumsFree + (y & 1), (y >> 1) - 1)) return false;
-                float sum[16];  // of each row: x . w, x . v
+                float sum[16];  // of each row: x . w, beta x . (w - v)
                 const int row0 = 16 * (warp - 12) + 8 * z;
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
@@ -615,8 +634,8 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                     *reinterpret_cast<uint2*>(sm.dx[col >> 6][1] + at) = make_uint2(h0, h1);
                     *reinterpret_cast<uint2*>(sm.dx[col >> 6][2] + at) = make_uint2(l0, l1);
                     sum[2 * r] = fmaf(xx[r].x, w[r].x, fmaf(xx[r].y, w[r].y, fmaf(xx[r].z, w[r].z, xx[r].w * w[r].w)));
-                    sum[2 * r + 1] = bt[r] * fmaf(xx[r].x, low_of(vv[r].x), fmaf(xx[r].y, high_of(vv[r].x),
-                                                  fmaf(xx[r].z, low_of(vv[r].y), xx[r].w * high_of(vv[r].y))));
+                    sum[2 * r + 1] = bt[r] * fmaf(xx[r].x, w[r].x - low_of(vv[r].x), fmaf(xx[r].y, w[r].y - high_of(vv[r].x),
+                                                  fmaf(xx[r].z, w[r].z - low_of(vv[r].y), xx[r].w * (w[r].w - high_of(vv[r].y)))));
                 }
                 // 16 sums over 32 lanes, halving what a lane holds with each exchange: lane l ends with sum l / 2
 #pragma unroll
