@@ -569,18 +569,22 @@ gdr_chain(Args A, const ChunkWs* ws, Saved out, int chunks) {
         float z[8][4] = {}, o[8][4] = {};
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t ah[4], al[4], bb[4];
+            uint32_t ah[4], al[4], bb[4][4];
             frag_split(S[2 * kk], S[2 * kk + 1], ah, al);
+            // a tile's products lie eight MMAs apart, so that none waits for the one before it
 #pragma unroll
-            for (int jp = 0; jp < 4; ++jp) {
-                ld_b<2 * D>(bb, kt, jp, kk, lane);
-                mma2(z[2 * jp], z[2 * jp + 1], ah, bb);
-                mma2(z[2 * jp], z[2 * jp + 1], al, bb);
-                if (!kSave) {
-                    ld_b<2 * D>(bb, qt, jp, kk, lane);
-                    mma2(o[2 * jp], o[2 * jp + 1], ah, bb);
-                    mma2(o[2 * jp], o[2 * jp + 1], al, bb);
-                }
+            for (int jp = 0; jp < 4; ++jp) ld_b<2 * D>(bb[jp], kt, jp, kk, lane);
+#pragma unroll
+            for (int jp = 0; jp < 4; ++jp) mma2(z[2 * jp], z[2 * jp + 1], ah, bb[jp]);
+#pragma unroll
+            for (int jp = 0; jp < 4; ++jp) mma2(z[2 * jp], z[2 * jp + 1], al, bb[jp]);
+            if (!kSave) {
+#pragma unroll
+                for (int jp = 0; jp < 4; ++jp) ld_b<2 * D>(bb[jp], qt, jp, kk, lane);
+#pragma unroll
+                for (int jp = 0; jp < 4; ++jp) mma2(o[2 * jp], o[2 * jp + 1], ah, bb[jp]);
+#pragma unroll
+                for (int jp = 0; jp < 4; ++jp) mma2(o[2 * jp], o[2 * jp + 1], al, bb[jp]);
             }
         }
         if (kSave) save_state<D>(S, out.S0 + (static_cast<size_t>(n) * (chunks + 1) + c) * 2 * page, A.e, col + g, lane);
@@ -618,15 +622,17 @@ gdr_chain(Args A, const ChunkWs* ws, Saved out, int chunks) {
         const uint32_t nh = smem_addr(sm.np[0]), nl = smem_addr(sm.np[1]);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
+            uint32_t bb[4][4];
 #pragma unroll
-            for (int jp = kk; jp < 4; ++jp) {
-                uint32_t bb[4];
-                ld_b<128>(bb, nh, jp, kk, lane);
-                mma2(z[2 * jp], z[2 * jp + 1], fh[kk], bb);
-                mma2(z[2 * jp], z[2 * jp + 1], fl[kk], bb);
-                ld_b<128>(bb, nl, jp, kk, lane);
-                mma2(z[2 * jp], z[2 * jp + 1], fh[kk], bb);
-            }
+            for (int jp = kk; jp < 4; ++jp) ld_b<128>(bb[jp], nh, jp, kk, lane);
+#pragma unroll
+            for (int jp = kk; jp < 4; ++jp) mma2(z[2 * jp], z[2 * jp + 1], fh[kk], bb[jp]);
+#pragma unroll
+            for (int jp = kk; jp < 4; ++jp) mma2(z[2 * jp], z[2 * jp + 1], fl[kk], bb[jp]);
+#pragma unroll
+            for (int jp = kk; jp < 4; ++jp) ld_b<128>(bb[jp], nl, jp, kk, lane);
+#pragma unroll
+            for (int jp = kk; jp < 4; ++jp) mma2(z[2 * jp], z[2 * jp + 1], fh[kk], bb[jp]);
         }
         if (kSave) {
 #pragma unroll
@@ -656,15 +662,17 @@ gdr_chain(Args A, const ChunkWs* ws, Saved out, int chunks) {
             for (int kk = 0; kk < 4; ++kk) {
                 uint32_t uh[4], ul[4];
                 frag_split(z[2 * kk], z[2 * kk + 1], uh, ul);
+                uint32_t bb[4][4];
 #pragma unroll
-                for (int jp = kk; jp < 4; ++jp) {
-                    uint32_t bb[4];
-                    ld_b<128>(bb, ph, jp, kk, lane);
-                    mma2(o[2 * jp], o[2 * jp + 1], uh, bb);
-                    mma2(o[2 * jp], o[2 * jp + 1], ul, bb);
-                    ld_b<128>(bb, pl, jp, kk, lane);
-                    mma2(o[2 * jp], o[2 * jp + 1], uh, bb);
-                }
+                for (int jp = kk; jp < 4; ++jp) ld_b<128>(bb[jp], ph, jp, kk, lane);
+#pragma unroll
+                for (int jp = kk; jp < 4; ++jp) mma2(o[2 * jp], o[2 * jp + 1], uh, bb[jp]);
+#pragma unroll
+                for (int jp = kk; jp < 4; ++jp) mma2(o[2 * jp], o[2 * jp + 1], ul, bb[jp]);
+#pragma unroll
+                for (int jp = kk; jp < 4; ++jp) ld_b<128>(bb[jp], pl, jp, kk, lane);
+#pragma unroll
+                for (int jp = kk; jp < 4; ++jp) mma2(o[2 * jp], o[2 * jp + 1], uh, bb[jp]);
             }
             store_rows(A, A.o, A.out_bf16, o, b, h, c * kC, len, col, sm.v[s], wcol, lane);
         }
@@ -691,11 +699,14 @@ gdr_chain(Args A, const ChunkWs* ws, Saved out, int chunks) {
             uint32_t uh[4], ul[4];
             frag_split(y[0], y[1], uh, ul);
 #pragma unroll
-            for (int jp = 0; jp < D / 16; ++jp) {
-                uint32_t bb[4];
-                ld_bt<2 * D>(bb, kt, jp, kk, lane);
-                mma2(S[2 * jp], S[2 * jp + 1], uh, bb);
-                mma2(S[2 * jp], S[2 * jp + 1], ul, bb);
+            for (int j4 = 0; j4 < D / 16; j4 += 4) {
+                uint32_t bb[4][4];
+#pragma unroll
+                for (int jp = 0; jp < 4; ++jp) ld_bt<2 * D>(bb[jp], kt, j4 + jp, kk, lane);
+#pragma unroll
+                for (int jp = 0; jp < 4; ++jp) mma2(S[2 * (j4 + jp)], S[2 * (j4 + jp) + 1], uh, bb[jp]);
+#pragma unroll
+                for (int jp = 0; jp < 4; ++jp) mma2(S[2 * (j4 + jp)], S[2 * (j4 + jp) + 1], ul, bb[jp]);
             }
         }
         __syncthreads();
@@ -748,14 +759,14 @@ gdr_chain_rev(Args A, const ChunkWs* ws, Saved out, int chunks) {
         float x[8][4] = {};
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t ah[4], al[4], bb[4];
+            uint32_t ah[4], al[4], bb[4][4];
             frag_split(S[2 * kk], S[2 * kk + 1], ah, al);
 #pragma unroll
-            for (int jp = 0; jp < 4; ++jp) {
-                ld_b<2 * D>(bb, kt, jp, kk, lane);
-                mma2(x[2 * jp], x[2 * jp + 1], ah, bb);
-                mma2(x[2 * jp], x[2 * jp + 1], al, bb);
-            }
+            for (int jp = 0; jp < 4; ++jp) ld_b<2 * D>(bb[jp], kt, jp, kk, lane);
+#pragma unroll
+            for (int jp = 0; jp < 4; ++jp) mma2(x[2 * jp], x[2 * jp + 1], ah, bb[jp]);
+#pragma unroll
+            for (int jp = 0; jp < 4; ++jp) mma2(x[2 * jp], x[2 * jp + 1], al, bb[jp]);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -774,14 +785,15 @@ gdr_chain_rev(Args A, const ChunkWs* ws, Saved out, int chunks) {
         for (int kk = 0; kk < 4; ++kk) {
             uint32_t da[4];
             ld_at<128>(da, vt, warp, kk, lane);
+            uint32_t bb[4][4];
 #pragma unroll
-            for (int jp = 0; jp <= kk; ++jp) {
-                uint32_t bb[4];
-                ld_bt<128>(bb, ph, jp, kk, lane);
-                mma2(x[2 * jp], x[2 * jp + 1], da, bb);
-                ld_bt<128>(bb, pl, jp, kk, lane);
-                mma2(x[2 * jp], x[2 * jp + 1], da, bb);
-            }
+            for (int jp = 0; jp <= kk; ++jp) ld_bt<128>(bb[jp], ph, jp, kk, lane);
+#pragma unroll
+            for (int jp = 0; jp <= kk; ++jp) mma2(x[2 * jp], x[2 * jp + 1], da, bb[jp]);
+#pragma unroll
+            for (int jp = 0; jp <= kk; ++jp) ld_bt<128>(bb[jp], pl, jp, kk, lane);
+#pragma unroll
+            for (int jp = 0; jp <= kk; ++jp) mma2(x[2 * jp], x[2 * jp + 1], da, bb[jp]);
         }
         // X = dU - N^T (beta dU)
         {
@@ -802,15 +814,17 @@ gdr_chain_rev(Args A, const ChunkWs* ws, Saved out, int chunks) {
             }
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
+                uint32_t bb[4][4];
 #pragma unroll
-                for (int jp = 0; jp <= kk; ++jp) {
-                    uint32_t bb[4];
-                    ld_bt<128>(bb, nh, jp, kk, lane);
-                    mma2(x[2 * jp], x[2 * jp + 1], fh[kk], bb);
-                    mma2(x[2 * jp], x[2 * jp + 1], fl[kk], bb);
-                    ld_bt<128>(bb, nl, jp, kk, lane);
-                    mma2(x[2 * jp], x[2 * jp + 1], fh[kk], bb);
-                }
+                for (int jp = 0; jp <= kk; ++jp) ld_bt<128>(bb[jp], nh, jp, kk, lane);
+#pragma unroll
+                for (int jp = 0; jp <= kk; ++jp) mma2(x[2 * jp], x[2 * jp + 1], fh[kk], bb[jp]);
+#pragma unroll
+                for (int jp = 0; jp <= kk; ++jp) mma2(x[2 * jp], x[2 * jp + 1], fl[kk], bb[jp]);
+#pragma unroll
+                for (int jp = 0; jp <= kk; ++jp) ld_bt<128>(bb[jp], nl, jp, kk, lane);
+#pragma unroll
+                for (int jp = 0; jp <= kk; ++jp) mma2(x[2 * jp], x[2 * jp + 1], fh[kk], bb[jp]);
             }
         }
 #pragma unroll
@@ -859,14 +873,18 @@ gdr_chain_rev(Args A, const ChunkWs* ws, Saved out, int chunks) {
             frag_split(y[0], y[1], h1, l1);
             frag_split(u[0], u[1], h2, l2);
 #pragma unroll
-            for (int jp = 0; jp < D / 16; ++jp) {
-                uint32_t bb[4];
-                ld_bt<2 * D>(bb, qt, jp, kk, lane);
-                mma2(S[2 * jp], S[2 * jp + 1], h1, bb);
-                mma2(S[2 * jp], S[2 * jp + 1], l1, bb);
-                ld_bt<2 * D>(bb, kt, jp, kk, lane);
-                mma2(S[2 * jp], S[2 * jp + 1], h2, bb);
-                mma2(S[2 * jp], S[2 * jp + 1], l2, bb);
+            for (int j4 = 0; j4 < D / 16; j4 += 4) {
+                uint32_t bb[4][4];
+                const auto both = [&](uint32_t tile, const uint32_t (&h)[4], const uint32_t (&l)[4]) {
+#pragma unroll
+                    for (int jp = 0; jp < 4; ++jp) ld_bt<2 * D>(bb[jp], tile, j4 + jp, kk, lane);
+#pragma unroll
+                    for (int jp = 0; jp < 4; ++jp) mma2(S[2 * (j4 + jp)], S[2 * (j4 + jp) + 1], h, bb[jp]);
+#pragma unroll
+                    for (int jp = 0; jp < 4; ++jp) mma2(S[2 * (j4 + jp)], S[2 * (j4 + jp) + 1], l, bb[jp]);
+                };
+                both(qt, h1, l1);
+                both(kt, h2, l2);
             }
         }
         // dv = beta X, through this warp's columns of the dO tile, which it has read
