@@ -180,15 +180,23 @@ constexpr int kPrepThreads = 256;
 constexpr int kPitchA = kC + 8, kPitchN = kC + 4;  // floats per row in shared memory
 
 template <int D>
-struct PrepSmem {
+struct PrepSmem {  // four CTAs per SM
     union {
         unsigned char kq[2][kC * D * 2];
         struct {
-            float a[kC][kPitchA];  // Ah
+            union {
+                float a[kC][kPitchA];                // Ah
+                unsigned char nimg[2][kC * kC * 2];  // N as two images, when Ah is read out
+            };
             float n[kC][kPitchN];  // N
         };
     };
-    ChunkWs out;
+    unsigned char pimg[2][kC * kC * 2];
+    struct {
+        float eg[kC], rest[kC], beta[kC];
+        float neg_eg[kC], neg_beta[kC], rest_beta[kC], neg_beta_eg[kC];
+        float g[kC], gl[kC], unused[3 * kC];
+    } out;  // as at the end of ChunkWs
 };
 
 // (x, y) as three pairs of bf16: all 24 bits of the significand
@@ -242,7 +250,7 @@ __device__ __forceinline__ void take(float (&acc)[4], const float (*M)[kPitchM],
 // times as long with most threads idle (7680 chunks of d = 128: 355 us against
 // 257 us with the joins on the SIMT cores, bound by shared memory).
 template <int D>
-__global__ void __launch_bounds__(kPrepThreads)
+__global__ void __launch_bounds__(kPrepThreads, 4)
 gdr_prep(Args A, ChunkWs* ws, int chunks) {
     extern __shared__ __align__(128) unsigned char prep_raw[];
     PrepSmem<D>& sm = *reinterpret_cast<PrepSmem<D>*>(prep_raw);
@@ -336,8 +344,8 @@ gdr_prep(Args A, ChunkWs* ws, int chunks) {
                 uint32_t hi, lo;
                 split(x[0], x[1], hi, lo);
                 const uint32_t at = piece<128>(t, j) + 4 * i;
-                *reinterpret_cast<uint32_t*>(sm.out.img[2] + at) = hi;
-                *reinterpret_cast<uint32_t*>(sm.out.img[3] + at) = lo;
+                *reinterpret_cast<uint32_t*>(sm.pimg[0] + at) = hi;
+                *reinterpret_cast<uint32_t*>(sm.pimg[1] + at) = lo;
             } else {
                 *reinterpret_cast<float2*>(&sm.a[t][s]) = make_float2(x[0], x[1]);
             }
@@ -411,14 +419,18 @@ gdr_prep(Args A, ChunkWs* ws, int chunks) {
                 split(y.x, y.y, w[2], w[6]);
                 split(y.z, y.w, w[3], w[7]);
             }
-            *reinterpret_cast<uint4*>(sm.out.img[0] + piece<128>(t, p)) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(sm.out.img[1] + piece<128>(t, p)) = make_uint4(w[4], w[5], w[6], w[7]);
+            *reinterpret_cast<uint4*>(sm.nimg[0] + piece<128>(t, p)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(sm.nimg[1] + piece<128>(t, p)) = make_uint4(w[4], w[5], w[6], w[7]);
         }
     }
     __syncthreads();
-    const uint4* from = reinterpret_cast<const uint4*>(&sm.out);
-    uint4* to = reinterpret_cast<uint4*>(ws + static_cast<size_t>(n) * chunks + c);
-    for (int x = tid; x < static_cast<int>(sizeof(ChunkWs) / 16); x += kPrepThreads) to[x] = from[x];
+    ChunkWs& to = ws[static_cast<size_t>(n) * chunks + c];
+    const auto copy = [&](void* dst, const void* src, int bytes) {
+        for (int x = tid; x < bytes / 16; x += kPrepThreads) static_cast<uint4*>(dst)[x] = static_cast<const uint4*>(src)[x];
+    };
+    copy(to.img[0], sm.nimg, sizeof(sm.nimg));
+    copy(to.img[2], sm.pimg, sizeof(sm.pimg));
+    copy(to.eg, &sm.out, sizeof(sm.out));
 }
 
 // ----------------------------------------------------------------- gdr_chain
