@@ -80,6 +80,8 @@ bool set_chunk_attrs() {
            set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kForward>), sizeof(walk::Smem<D>)) &&
            set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kSave>), sizeof(walk::Smem<D>)) &&
            set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kBackward>), sizeof(walk::Smem<D>)) &&
+           set(reinterpret_cast<const void*>(walk::gdr_join<D>), sizeof(walk::JoinSmem<D>)) &&
+           set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kTransfer>), sizeof(walk::Smem<D>)) &&
            set(reinterpret_cast<const void*>(gdr_grad<D, 64>), sizeof(GradTiles<D, 64>)) &&
            set(reinterpret_cast<const void*>(grad::gdr_grad_tc<D>), sizeof(grad::Smem<D>));
 }
@@ -156,8 +158,32 @@ bool by_chunks(la2_dtype dtype, int d, int e) {
     return dtype == LA2_DTYPE_BF16 && (d == 64 || d == 128) && (e == 64 || e == 128);
 }
 
+// Segments of the forward walk (gdr_walk_sm100.cuh) for `seqs` sequences of
+// `chunks` chunks, by the chunks that the busiest SM walks: a segment's own and,
+// with segments, those of the two walks that make its entering state; a join takes
+// about a chunk's time.  16 sequences of 1024 chunks (T = 65,536): 9 segments,
+// JOINTIMES.
+struct SegPlan {
+    int segs, per;
+};
+
+SegPlan seg_plan(long long seqs, int chunks) {
+    SegPlan best = {1, chunks};
+    long long cost = static_cast<long long>(chunks) * ((seqs + kSMs - 1) / kSMs);
+    for (int g = 2; g <= 32 && chunks / g >= 8; ++g) {
+        const int per = cdiv(chunks, g), segs = cdiv(chunks, per);
+        const long long waves = (seqs * segs + kSMs - 1) / kSMs + (seqs * (2 * (segs - 1) - 1) + kSMs - 1) / kSMs;
+        const long long c = waves * per + segs + 8;
+        if (c < cost) {
+            cost = c;
+            best = {segs, per};
+        }
+    }
+    return best;
+}
+
 struct ChunkLayout {
-    size_t prep, S0, dS1, W, X, sums, bytes;
+    size_t prep, S0, dS1, W, X, sums, segs, bytes;
 };
 
 ChunkLayout chunk_ws(long long BH, int T, int d, int e, bool bwd) {
@@ -174,13 +200,18 @@ ChunkLayout chunk_ws(long long BH, int T, int d, int e, bool bwd) {
         w.sums = w.X + rows;
         at = w.sums + (e == 128 ? static_cast<size_t>(kSMs) * (64 << 10) : 0);
     }
+    if (!bwd && e == la2::gdr::walk::kE) {
+        w.segs = at;
+        at += static_cast<size_t>(seg_plan(BH, static_cast<int>(chunks)).segs - 1) * seqs * 3 * d * e * sizeof(float);
+    }
     w.bytes = at;
     return w;
 }
 
 // One walk along every sequence: e = 128 on tcgen05 (T = 0 has no rows to map).
 template <int D, int kMode>
-la2_status walk_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::Saved& sv, int chunks, cudaStream_t stream) {
+la2_status walk_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::Saved& sv,
+                   const la2::gdr::walk::Segments& sg, int chunks, cudaStream_t stream) {
     using namespace la2::gdr;
     CUtensorMap mk, mq, mv;
     if (!row_map(&mk, A.k, A.B, A.Hk, A.T, D, A.bthd) || !row_map(&mq, A.q, A.B, A.Hk, A.T, D, A.bthd) ||
@@ -188,8 +219,9 @@ la2_status walk_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::S
         return LA2_ERR_CUDA;
     int* status = la2::status_word();
     if (!status) return LA2_ERR_CUDA;
-    walk::gdr_walk<D, kMode><<<A.B * A.H, walk::kThreads, sizeof(walk::Smem<D>), stream>>>(
-        A, cw, sv, chunks, mk, mq, mv, status);
+    const int parts = kMode == walk::kTransfer ? 2 * (sg.segs - 1) - 1 : kMode == walk::kForward ? sg.segs : 1;
+    walk::gdr_walk<D, kMode><<<A.B * A.H * parts, walk::kThreads, sizeof(walk::Smem<D>), stream>>>(
+        A, cw, sv, sg, chunks, mk, mq, mv, status);
     return LA2_OK;
 }
 
@@ -218,7 +250,16 @@ la2_status chunk_forward(const Args& A, char* ws, cudaStream_t stream) {
     if (chunks > 0)
         gdr_prep<D><<<static_cast<unsigned>(A.B) * A.H * chunks, kPrepThreads, sizeof(PrepSmem<D>), stream>>>(A, cw, chunks);
     if (on_tc(A)) {
-        const la2_status st = walk_tc<D, walk::kForward>(A, cw, Saved{}, chunks, stream);
+        const long long seqs = static_cast<long long>(A.B) * A.H;
+        const SegPlan pl = seg_plan(seqs, chunks);
+        const walk::Segments sg = {pl.segs, pl.per, reinterpret_cast<float*>(ws + chunk_ws(seqs, A.T, A.d, A.e, false).segs)};
+        la2_status st = LA2_OK;
+        if (pl.segs > 1) {
+            st = walk_tc<D, walk::kTransfer>(A, cw, Saved{}, sg, chunks, stream);
+            if (st != LA2_OK) return st;
+            walk::gdr_join<D><<<dim3(A.B * A.H, walk::kE / 32), walk::kJoinThreads, sizeof(walk::JoinSmem<D>), stream>>>(A, sg);
+        }
+        st = walk_tc<D, walk::kForward>(A, cw, Saved{}, sg, chunks, stream);
         return st == LA2_OK ? launched() : st;
     }
     gdr_chain<D, false><<<A.B * A.H * (A.e / kWalkCols), kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, Saved{}, chunks);
@@ -243,8 +284,9 @@ la2_status chunk_backward(const Args& A, char* ws, cudaStream_t stream) {
         if (!on_tc(A)) gdr_chain<D, true><<<walks, kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, sv, chunks);
     }
     if (on_tc(A)) {
-        la2_status st = walk_tc<D, walk::kSave>(A, cw, sv, chunks, stream);
-        if (st == LA2_OK) st = walk_tc<D, walk::kBackward>(A, cw, sv, chunks, stream);
+        const walk::Segments whole = {1, chunks, nullptr};
+        la2_status st = walk_tc<D, walk::kSave>(A, cw, sv, whole, chunks, stream);
+        if (st == LA2_OK) st = walk_tc<D, walk::kBackward>(A, cw, sv, whole, chunks, stream);
         if (st == LA2_OK) st = grad_tc<D>(A, cw, sv, chunks, stream);
         return st == LA2_OK ? launched() : st;
     } else {

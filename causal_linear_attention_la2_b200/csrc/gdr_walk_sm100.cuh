@@ -42,7 +42,18 @@ constexpr int kE = 128;
 constexpr int kThreads = 512;
 constexpr int kChainWarps = 8, kSideWarps = 4;
 
-enum Mode { kForward = 0, kSave = 1, kBackward = 2 };
+enum Mode { kForward = 0, kSave = 1, kBackward = 2, kTransfer = 3 };
+
+// Few sequences: each is cut into `segs` segments of `per` chunks that are walked
+// at the same time.  What a segment does to the state that enters it is
+// S -> M S + B; kTransfer walks all segments but the first and the last twice,
+// from zero for B and from the identity with v = 0 for M (d columns), the first
+// one once, from where it starts; gdr_join applies them in turn, and the forward
+// walk of each segment starts from its result.
+struct Segments {
+    int segs, per;  // 1: whole sequences
+    float* pages;   // [segs - 1][B*H][3][d][128]: B, M, the state that enters segment s + 1
+};
 
 template <int D>
 struct Stage {  // 1024-byte aligned; tiles of 64 rows x 64 columns (128 bytes, swizzled)
@@ -141,7 +152,7 @@ __device__ __forceinline__ float tile_at(uint32_t tile, int r, int c) { return _
 
 template <int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
-gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant__ CUtensorMap mk,
+gdr_walk(Args A, const ChunkWs* ws, Saved out, Segments sg, int chunks, const __grid_constant__ CUtensorMap mk,
          const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mv, int* status) {
     extern __shared__ __align__(1024) unsigned char walk_tc_raw[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(walk_tc_raw);
@@ -149,10 +160,18 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
     constexpr uint32_t kTile = kC * 128;
     // TMEM columns
     constexpr uint32_t cS = 0, cB = D, cA = 2 * D, cD2 = cA + 64, cW = cD2 + 64, cD4 = cW + 64;
-    const int n = blockIdx.x, b = n / A.H, h = n % A.H, hk = h / (A.H / A.Hk);
+    // kForward: segment by segment; kTransfer: B of the first one, B and M of the others
+    const int seqs = A.B * A.H, n = blockIdx.x % seqs, part = blockIdx.x / seqs;
+    const int seg = kMode == kTransfer ? (part + 1) >> 1 : kMode == kForward ? part : 0;
+    const bool unit = kMode == kTransfer && part > 0 && !(part & 1);  // from the identity, with v = 0
+    const int b = n / A.H, h = n % A.H, hk = h / (A.H / A.Hk);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int len = length_of(A, b), nc = (len + kC - 1) / kC;
+    const int len = length_of(A, b), all = (len + kC - 1) / kC;
+    // chunks c0 .. c0 + nc - 1 of the sequence
+    const int c0 = (kMode == kForward || kMode == kTransfer) && sg.segs > 1 ? seg * sg.per : 0;
+    const int nc = sg.segs > 1 ? max(0, min(sg.per, all - c0)) : all;
     const size_t page = static_cast<size_t>(D) * kE;
+    const auto pages = [&](int s, int which) { return sg.pages + ((static_cast<size_t>(s) * seqs + n) * 3 + which) * page; };
     const ChunkWs* cw = ws + static_cast<size_t>(n) * chunks;
     const uint32_t bars = smem_addr(sm.bar);
     volatile int* abort = &sm.abort;
@@ -189,11 +208,12 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
 
     if (warp == 0) {
         // ---------------------------------------------------------------- loads
-        constexpr uint32_t kRows = (kMode == kSave ? D / 64 : 2 * (D / 64)) * kTile + (kE / 64) * kTile;
+        constexpr bool kNoQ = kMode == kSave || kMode == kTransfer;
+        constexpr uint32_t kRows = (kNoQ ? D / 64 : 2 * (D / 64)) * kTile + (kE / 64) * kTile;
         constexpr uint32_t kImg = (kRev ? 4 : 2) * kC * kC * 2, kCoef = kCoefs * kC * 4;
         int issued = 0;
         for (int it = 0; it < nc; ++it) {
-            const int s = it & 1, c = kRev ? nc - 1 - it : it, t0 = c * kC;
+            const int s = it & 1, c = kRev ? nc - 1 - it : c0 + it, t0 = c * kC;
             if (it >= 2 && !wait(kEmpty + s, (it >> 1) - 1)) break;
             Stage<D>& st = sm.stage[s];
             const bool cut = t0 + kC > len && len < A.T;  // rows of this sequence's padding would be loaded
@@ -205,7 +225,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
                 };
                 for (int x = 0; x < D / 64; ++x) {
                     rows(st.kq[x][0], mk, hk, x);
-                    if (kMode != kSave) rows(st.kq[x][1], mq, hk, x);
+                    if (!kNoQ) rows(st.kq[x][1], mq, hk, x);
                 }
                 for (int x = 0; x < kE / 64; ++x) rows(st.v[x], mv, h, x);
                 bulk_load(smem_addr(st.img), cw[c].img, kImg, bar(on));
@@ -230,7 +250,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
 #pragma unroll
                         for (int y = 0; y < D / 64; ++y) {
                             *reinterpret_cast<uint4*>(st.kq[y][0] + r * 128 + x * 16) = z;
-                            if (kMode != kSave) *reinterpret_cast<uint4*>(st.kq[y][1] + r * 128 + x * 16) = z;
+                            if (!kNoQ) *reinterpret_cast<uint4*>(st.kq[y][1] + r * 128 + x * 16) = z;
                         }
 #pragma unroll
                         for (int y = 0; y < kE / 64; ++y) *reinterpret_cast<uint4*>(st.v[y] + r * 128 + x * 16) = z;
@@ -242,7 +262,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
         }
         // the copies in flight have landed before the CTA's shared memory goes
         for (int it = max(0, issued - 2); it < issued; ++it) {
-            const int c = kRev ? nc - 1 - it : it;
+            const int c = kRev ? nc - 1 - it : c0 + it;
             const bool cut = c * kC + kC > len && len < A.T;
             mbar_wait(cut ? bar(kRaw) : bar(kFull + (it & 1)), cut ? 0 : (it >> 1) & 1);
             // (a P that was never asked for, after an abort, costs this wait its two seconds)
@@ -370,12 +390,24 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
         const int half = (warp - 4) >> 2, e = 32 * (warp & 3) + lane;
         const uint32_t row = tm + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         constexpr int kGroups = D / 64;  // groups of 32 state columns of this half
-        const auto state = [&](const float* p, int i) { return p ? p[static_cast<size_t>(i) * kE + e] : 0.f; };
+        const auto state = [&](const float* p, int i) {
+            if (unit) return e == i ? 1.f : 0.f;
+            return p ? p[static_cast<size_t>(i) * kE + e] : 0.f;
+        };
         const float* first = kRev ? A.dfinal : A.init;
         if (first) first += n * page;
         float* last = kRev ? A.dinit : A.fin;
         if (kMode == kSave) last = nullptr;
         if (last) last += n * page;
+        if (kMode == kForward && sg.segs > 1) {
+            if (seg > 0) first = pages(seg - 1, 2);
+            // the final state is that of the segment with the sequence's last row (the first one of an empty sequence)
+            if (all > 0 ? c0 >= all || c0 + nc < all : seg > 0) last = nullptr;
+        }
+        if (kMode == kTransfer) {
+            if (seg > 0) first = nullptr;
+            last = pages(seg, unit ? 1 : 0);
+        }
         const int r0 = 32 * half;
         const auto done = [&](int i) {
             tmem_wait_st();
@@ -431,14 +463,14 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
                 split32(S, w);
                 tmem_st32u(row + cB + 32 * q, w);
                 done(kState + y);
-                if (kMode != kForward) keep(w, q, kRev ? nc - 1 : 0);
+                if (kMode == kSave || kRev) keep(w, q, kRev ? nc - 1 : 0);
             } else if (last) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) last[static_cast<size_t>(32 * q + i) * kE + e] = S[i];
             }
         }
         for (int it = 0; ok && it < nc; ++it) {
-            const int s = it & 1, c = kRev ? nc - 1 - it : it;
+            const int s = it & 1, c = kRev ? nc - 1 - it : c0 + it;
             Stage<D>& st = sm.stage[s];
             if (!(ok = wait(kFull + s, it >> 1))) break;
             scale(st.eg[kC - 1]);
@@ -447,7 +479,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
                 const uint32_t vt = smem_addr(st.v);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    v[i] = tile_bits(vt, r0 + 2 * i, e) | tile_bits(vt, r0 + 2 * i + 1, e) << 16;
+                    v[i] = unit ? 0u : tile_bits(vt, r0 + 2 * i, e) | tile_bits(vt, r0 + 2 * i + 1, e) << 16;
             }
             if (!(ok = wait(kD1, it))) break;
             tc_fence_after();
@@ -508,7 +540,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) arrive(bar(kUp));
-                } else {  // rows w or x for the gradients
+                } else if (kMode != kTransfer) {  // rows w or x for the gradients
                     float* to = (kRev ? out.X : out.W) + (static_cast<size_t>(n) * A.T + c * kC + r0) * kE + e;
                     const int left = len - c * kC - r0;
 #pragma unroll
@@ -532,7 +564,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
                         tmem_st32u(row + cB + 32 * q, w);
                         done(kState + y);
                     }
-                    if (kMode != kForward) keep(w, q, kRev ? c - 1 : c + 1);
+                    if (kMode == kSave || kRev) keep(w, q, kRev ? c - 1 : c + 1);
                 }
             } else if (last) {
 #pragma unroll 1
@@ -550,7 +582,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
         const int e = 32 * (warp & 3) + lane;
         const uint32_t row = tm + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         for (int it = 0; it < nc; ++it) {
-            const int s = it & 1, c = kRev ? nc - 1 - it : it, t0 = c * kC;
+            const int s = it & 1, c = kRev ? nc - 1 - it : c0 + it, t0 = c * kC;
             Stage<D>& st = sm.stage[s];
             if (!wait(kFull + s, it >> 1)) break;
             if (kMode == kForward) {
@@ -667,6 +699,63 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant
     __syncthreads();
     tc_fence_after();
     if (warp == 2) tmem_dealloc(tm, 512);
+}
+
+// The states that enter segments 1, 2, ..: S_{s+1} = M_s S_s + B_s in fp32, 32
+// value columns per CTA (a lane each), d / 8 rows per warp; the next segment's M is
+// on its way (each warp its own rows) while this one's is used.
+constexpr int kJoinThreads = 256;
+
+template <int D>
+struct JoinSmem {
+    float M[2][D][kE];
+    float S[D][32];
+};
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads)
+gdr_join(Args A, Segments sg) {
+    extern __shared__ __align__(128) unsigned char join_raw[];
+    JoinSmem<D>& sm = *reinterpret_cast<JoinSmem<D>*>(join_raw);
+    const int seqs = A.B * A.H, n = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e = 32 * blockIdx.y + lane;
+    constexpr int kRows = D / (kJoinThreads / 32);
+    const size_t page = static_cast<size_t>(D) * kE;
+    const auto pages = [&](int s) { return sg.pages + (static_cast<size_t>(s) * seqs + n) * 3 * page; };
+    const auto fetch = [&](int s) {  // M of segment s: this warp's rows
+        if (s > 0 && s + 1 < sg.segs)
+            for (int r = warp * kRows; r < (warp + 1) * kRows; ++r)
+                cp16(smem_addr(&sm.M[s & 1][r][4 * lane]), pages(s) + page + static_cast<size_t>(r) * kE + 4 * lane, true);
+        cp_commit();
+    };
+    fetch(0);
+    for (int s = 0; s + 1 < sg.segs; ++s) {
+        fetch(s + 1);
+        float* at = pages(s);
+        float acc[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) acc[r] = at[static_cast<size_t>(warp * kRows + r) * kE + e];
+        cp_wait<1>();
+        __syncthreads();
+        if (s > 0) {  // the first segment's walk began with the initial state
+        const float(*M)[kE] = &sm.M[s & 1][warp * kRows];
+#pragma unroll 4
+        for (int k = 0; k < D; k += 4) {
+            const float s0 = sm.S[k][lane], s1 = sm.S[k + 1][lane], s2 = sm.S[k + 2][lane], s3 = sm.S[k + 3][lane];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const float4 m = *reinterpret_cast<const float4*>(&M[r][k]);
+                acc[r] = fmaf(m.x, s0, fmaf(m.y, s1, fmaf(m.z, s2, fmaf(m.w, s3, acc[r]))));
+            }
+        }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            sm.S[warp * kRows + r][lane] = acc[r];
+            at[2 * page + static_cast<size_t>(warp * kRows + r) * kE + e] = acc[r];
+        }
+    }
 }
 
 }  // namespace walk

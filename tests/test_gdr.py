@@ -418,6 +418,16 @@ def test_pieces_are_the_whole(gpu, dtype, d, cut):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,Hk,H,T,d,lens", [(1, 1, 1, 2100, 128, None), (1, 1, 2, 1030, 64, None),
+                                             (3, 1, 2, 1500, 128, [1500, 0, 700])])
+def test_long_sequences_in_segments(gpu, B, Hk, H, T, d, lens):
+    """Few long sequences, which the forward walks in segments: ragged ends, an empty sequence, carried states."""
+    x = R.make(B, Hk, H, T, d, 128, BF16, 23, init=True, lens=lens)
+    x["g"] *= 0.1  # states that last over many chunks
+    _check_fwd(gpu, x)
+
+
+@pytest.mark.gpu
 def test_empty_sequences_hand_states_on(gpu):
     s = torch.randn(2, 2, 8, 8, device=gpu)
     z = torch.zeros(2, 2, 0, 8, device=gpu)
