@@ -8,6 +8,7 @@
 #include <climits>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "gdr_chunk.cuh"
 #include "gdr_common.cuh"
@@ -132,7 +133,8 @@ RecWs rec_ws(long long BH, int T, int d, int e) {
 template <typename Tin>
 la2_status rec_forward(const Args& A, cudaStream_t stream) {
     const dim3 grid(A.B * A.H, cdiv(A.e, la2::gdr::kRecCols));
-    la2::gdr::gdr_rec_fwd<Tin, false><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, nullptr, nullptr);
+    if (A.d <= 64) la2::gdr::gdr_rec_fwd<Tin, false, 8><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, nullptr, nullptr);
+    else la2::gdr::gdr_rec_fwd<Tin, false, 16><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, nullptr, nullptr);
     return launched();
 }
 
@@ -144,9 +146,14 @@ la2_status rec_backward(const Args& A, char* ws, cudaStream_t stream) {
     float* W = reinterpret_cast<float*>(ws + w.W);
     float* X = reinterpret_cast<float*>(ws + w.X);
     const dim3 grid(A.B * A.H, cdiv(A.e, la2::gdr::kRecCols));
-    if (A.T > 0)
-        la2::gdr::gdr_rec_fwd<Tin, true><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, S0, W);
-    la2::gdr::gdr_rec_rev<Tin><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, dS1, X);
+    const auto walks = [&](auto rows) {
+        constexpr int kRows = decltype(rows)::value;
+        if (A.T > 0)
+            la2::gdr::gdr_rec_fwd<Tin, true, kRows><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, S0, W);
+        la2::gdr::gdr_rec_rev<Tin, kRows><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, dS1, X);
+    };
+    if (A.d <= 64) walks(std::integral_constant<int, 8>());
+    else walks(std::integral_constant<int, 16>());
     if (A.T > 0)
         la2::gdr::gdr_grad_rec<Tin><<<static_cast<unsigned>(A.B) * A.Hk * cdiv(A.T, la2::gdr::kRecChunk),
                                       la2::gdr::kGradThreads, sizeof(la2::gdr::GradSmem), stream>>>(A, S0, dS1, W, X);

@@ -21,7 +21,6 @@ namespace gdr {
 constexpr int kMaxDim = 128;
 constexpr int kRecThreads = 128;  // 4 warps of 4 columns
 constexpr int kRecCols = 16;
-constexpr int kRecRows = 16;      // rows of the state per lane: kMaxDim / 8
 constexpr int kRecStep = 16;      // tokens staged in shared memory at a time
 constexpr int kRecChunk = 32;     // chunk length of gdr_grad_rec
 
@@ -33,30 +32,55 @@ struct RecSmem {
     float b[kRecStep];
 };
 
-// Rows t0 .. t0 + n - 1 of k, q and 16 columns of `vals` (v or dout) into
-// shared memory; rows i >= d are zero.
+// Rows t0 .. t0 + n - 1 of k, q and 16 columns of `vals` (v or dout) on their way
+// to shared memory (rows i >= d are zero): a thread's column of k and q, loaded
+// while the rows before are worked on.
+static_assert(kRecThreads == kMaxDim, "a thread per column of k and q");
+
 template <typename Tin>
-__device__ __forceinline__ void rec_stage(const Args& A, RecSmem& sm, const Tin* vals, int b, int h,
-                                          int t0, int n, int col0) {
-    const int tid = threadIdx.x, hk = h / (A.H / A.Hk);
-    const Tin* k = static_cast<const Tin*>(A.k);
-    const Tin* q = static_cast<const Tin*>(A.q);
-    for (int x = tid; x < n * kMaxDim; x += kRecThreads) {
-        const int r = x / kMaxDim, i = x % kMaxDim;
-        const size_t at = row_at(A, b, hk, A.Hk, t0 + r, A.d) + i;
-        sm.k[r][i] = i < A.d ? to_float(k[at]) : 0.f;
-        sm.q[r][i] = i < A.d ? to_float(q[at]) : 0.f;
+struct RecRows {
+    float k[kRecStep], q[kRecStep], v[2], a, b;
+
+    __device__ __forceinline__ void load(const Args& A, const Tin* vals, int b0, int h, int t0, int n, int col0) {
+        const int tid = threadIdx.x, hk = h / (A.H / A.Hk);
+        const Tin* kp = static_cast<const Tin*>(A.k);
+        const Tin* qp = static_cast<const Tin*>(A.q);
+#pragma unroll
+        for (int r = 0; r < kRecStep; ++r) {
+            k[r] = q[r] = 0.f;
+            if (r < n && tid < A.d) {
+                const size_t at = row_at(A, b0, hk, A.Hk, t0 + r, A.d) + tid;
+                k[r] = to_float(kp[at]);
+                q[r] = to_float(qp[at]);
+            }
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int r = (tid + y * kRecThreads) / kRecCols, j = col0 + tid % kRecCols;
+            v[y] = r < n && j < A.e ? to_float(vals[row_at(A, b0, h, A.H, t0 + r, A.e) + j]) : 0.f;
+        }
+        a = b = 0.f;
+        if (tid < n) {
+            const size_t at = row_at(A, b0, h, A.H, t0 + tid, 1);
+            a = expf(gate_at(A, at));
+            b = A.beta[at];
+        }
     }
-    for (int x = tid; x < n * kRecCols; x += kRecThreads) {
-        const int r = x / kRecCols, j = col0 + x % kRecCols;
-        sm.v[r][x % kRecCols] = j < A.e ? to_float(vals[row_at(A, b, h, A.H, t0 + r, A.e) + j]) : 0.f;
+    __device__ __forceinline__ void store(RecSmem& sm) const {
+        const int tid = threadIdx.x;
+#pragma unroll
+        for (int r = 0; r < kRecStep; ++r) {
+            sm.k[r][tid] = k[r];
+            sm.q[r][tid] = q[r];
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) sm.v[(tid + y * kRecThreads) / kRecCols][tid % kRecCols] = v[y];
+        if (tid < kRecStep) {
+            sm.a[tid] = a;
+            sm.b[tid] = b;
+        }
     }
-    if (tid < n) {
-        const size_t at = row_at(A, b, h, A.H, t0 + tid, 1);
-        sm.a[tid] = expf(gate_at(A, at));
-        sm.b[tid] = A.beta[at];
-    }
-}
+};
 
 __device__ __forceinline__ float sum8(float x) {
     x += __shfl_xor_sync(0xffffffffu, x, 1);
@@ -65,9 +89,9 @@ __device__ __forceinline__ float sum8(float x) {
     return x;
 }
 
-// Forward.  kSave: no output; the state entering each chunk goes to S0
+// Forward.  kRecRows: rows of the state per lane, 8 (d <= 64) or 16.  kSave: no output; the state entering each chunk goes to S0
 // [B*H][chunks][d][e] and the rows w to W [B*H][T][e], for the backward.
-template <typename Tin, bool kSave>
+template <typename Tin, bool kSave, int kRecRows>
 __global__ void __launch_bounds__(kRecThreads)
 gdr_rec_fwd(Args A, float* S0, float* W) {
     __shared__ RecSmem sm;
@@ -85,38 +109,46 @@ gdr_rec_fwd(Args A, float* S0, float* W) {
         const int i = r + 8 * m;
         S[m] = A.init && on && i < A.d ? A.init[n * page + static_cast<size_t>(i) * A.e + j] : 0.f;
     }
+    const size_t step = A.bthd ? static_cast<size_t>(A.H) * A.e : A.e;  // from one row of v, out, dv to the next
+    const size_t row0 = row_at(A, b, h, A.H, 0, A.e) + j;
+    RecRows<Tin> next;
+    if (len > 0) next.load(A, static_cast<const Tin*>(A.v), b, h, 0, min(kRecStep, len), col0);
     for (int t0 = 0; t0 < len; t0 += kRecStep) {
         const int m16 = min(kRecStep, len - t0);
         __syncthreads();
-        rec_stage<Tin>(A, sm, static_cast<const Tin*>(A.v), b, h, t0, m16, col0);
+        next.store(sm);
         __syncthreads();
+        if (t0 + kRecStep < len)
+            next.load(A, static_cast<const Tin*>(A.v), b, h, t0 + kRecStep, min(kRecStep, len - t0 - kRecStep), col0);
         if (kSave && t0 % kRecChunk == 0 && on) {
             float* to = S0 + (static_cast<size_t>(n) * chunks + t0 / kRecChunk) * page + j;
 #pragma unroll
             for (int m = 0; m < kRecRows; ++m)
                 if (r + 8 * m < A.d) to[static_cast<size_t>(r + 8 * m) * A.e] = S[m];
         }
+#pragma unroll 2
         for (int t = 0; t < m16; ++t) {
             const float a = sm.a[t];
-            float p = 0.f;
+            float p[4] = {};
 #pragma unroll
             for (int m = 0; m < kRecRows; ++m) {
                 S[m] *= a;
-                p = fmaf(S[m], sm.k[t][r + 8 * m], p);
+                p[m & 3] = fmaf(S[m], sm.k[t][r + 8 * m], p[m & 3]);
             }
-            const float w = sm.v[t][lc] - sum8(p);
+            const float w = sm.v[t][lc] - sum8((p[0] + p[1]) + (p[2] + p[3]));
             const float u = sm.b[t] * w;
-            float o = 0.f;
+            float o4[4] = {};
 #pragma unroll
             for (int m = 0; m < kRecRows; ++m) {
                 S[m] = fmaf(sm.k[t][r + 8 * m], u, S[m]);
-                if (!kSave) o = fmaf(S[m], sm.q[t][r + 8 * m], o);
+                if (!kSave) o4[m & 3] = fmaf(S[m], sm.q[t][r + 8 * m], o4[m & 3]);
             }
+            float o = (o4[0] + o4[1]) + (o4[2] + o4[3]);
             if (kSave) {
                 if (on && r == 0) W[(static_cast<size_t>(n) * A.T + t0 + t) * A.e + j] = w;
             } else {
                 o = sum8(o);
-                if (on && r == 0) put(A.o, row_at(A, b, h, A.H, t0 + t, A.e) + j, o, A.out_bf16);
+                if (on && r == 0) put(A.o, row0 + (t0 + t) * step, o, A.out_bf16);
             }
         }
     }
@@ -129,7 +161,7 @@ gdr_rec_fwd(Args A, float* S0, float* W) {
 
 // Backward in time: dv, d_init_state, the rows x to X [B*H][T][e] and the
 // gradient of the state after each chunk to dS1 [B*H][chunks][d][e].
-template <typename Tin>
+template <typename Tin, int kRecRows>
 __global__ void __launch_bounds__(kRecThreads)
 gdr_rec_rev(Args A, float* dS1, float* X) {
     __shared__ RecSmem sm;
@@ -147,11 +179,17 @@ gdr_rec_rev(Args A, float* dS1, float* X) {
         const int i = r + 8 * m;
         D[m] = A.dfinal && on && i < A.d ? A.dfinal[n * page + static_cast<size_t>(i) * A.e + j] : 0.f;
     }
-    for (int t0 = len > 0 ? (len - 1) / kRecStep * kRecStep : -1; t0 >= 0; t0 -= kRecStep) {
+    const size_t step = A.bthd ? static_cast<size_t>(A.H) * A.e : A.e;
+    const size_t row0 = row_at(A, b, h, A.H, 0, A.e) + j;
+    RecRows<Tin> next;
+    const int tail = len > 0 ? (len - 1) / kRecStep * kRecStep : -1;
+    if (len > 0) next.load(A, static_cast<const Tin*>(A.dout), b, h, tail, len - tail, col0);
+    for (int t0 = tail; t0 >= 0; t0 -= kRecStep) {
         const int m16 = min(kRecStep, len - t0);
         __syncthreads();
-        rec_stage<Tin>(A, sm, static_cast<const Tin*>(A.dout), b, h, t0, m16, col0);
+        next.store(sm);
         __syncthreads();
+        if (t0 > 0) next.load(A, static_cast<const Tin*>(A.dout), b, h, t0 - kRecStep, kRecStep, col0);
         // the last rows of a chunk: its dS1 is what arrives here
         if (on && ((t0 + kRecStep) % kRecChunk == 0 || t0 + m16 == len)) {
             float* to = dS1 + (static_cast<size_t>(n) * chunks + t0 / kRecChunk) * page + j;
@@ -159,20 +197,21 @@ gdr_rec_rev(Args A, float* dS1, float* X) {
             for (int m = 0; m < kRecRows; ++m)
                 if (r + 8 * m < A.d) to[static_cast<size_t>(r + 8 * m) * A.e] = D[m];
         }
+#pragma unroll 2
         for (int t = m16 - 1; t >= 0; --t) {
             const float dout = sm.v[t][lc];
-            float p = 0.f;
+            float p[4] = {};
 #pragma unroll
             for (int m = 0; m < kRecRows; ++m) {
                 D[m] = fmaf(sm.q[t][r + 8 * m], dout, D[m]);
-                p = fmaf(D[m], sm.k[t][r + 8 * m], p);
+                p[m & 3] = fmaf(D[m], sm.k[t][r + 8 * m], p[m & 3]);
             }
-            const float x = sum8(p), dw = sm.b[t] * x, a = sm.a[t];
+            const float x = sum8((p[0] + p[1]) + (p[2] + p[3])), dw = sm.b[t] * x, a = sm.a[t];
 #pragma unroll
             for (int m = 0; m < kRecRows; ++m) D[m] = a * fmaf(-sm.k[t][r + 8 * m], dw, D[m]);
             if (on && r == 0) {
                 X[(static_cast<size_t>(n) * A.T + t0 + t) * A.e + j] = x;
-                put(A.dv, row_at(A, b, h, A.H, t0 + t, A.e) + j, dw, A.out_bf16);
+                put(A.dv, row0 + (t0 + t) * step, dw, A.out_bf16);
             }
         }
     }
