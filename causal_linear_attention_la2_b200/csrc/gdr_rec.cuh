@@ -39,7 +39,8 @@ static_assert(kRecThreads == kMaxDim, "a thread per column of k and q");
 
 template <typename Tin>
 struct RecRows {
-    float k[kRecStep], q[kRecStep], v[2], a, b;
+    Tin k[kRecStep], q[kRecStep], v[2];  // as loaded: a conversion would wait for them
+    float g, b;
 
     __device__ __forceinline__ void load(const Args& A, const Tin* vals, int b0, int h, int t0, int n, int col0) {
         const int tid = threadIdx.x, hk = h / (A.H / A.Hk);
@@ -47,22 +48,22 @@ struct RecRows {
         const Tin* qp = static_cast<const Tin*>(A.q);
 #pragma unroll
         for (int r = 0; r < kRecStep; ++r) {
-            k[r] = q[r] = 0.f;
+            k[r] = q[r] = Tin(0.f);
             if (r < n && tid < A.d) {
                 const size_t at = row_at(A, b0, hk, A.Hk, t0 + r, A.d) + tid;
-                k[r] = to_float(kp[at]);
-                q[r] = to_float(qp[at]);
+                k[r] = kp[at];
+                q[r] = qp[at];
             }
         }
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
             const int r = (tid + y * kRecThreads) / kRecCols, j = col0 + tid % kRecCols;
-            v[y] = r < n && j < A.e ? to_float(vals[row_at(A, b0, h, A.H, t0 + r, A.e) + j]) : 0.f;
+            v[y] = r < n && j < A.e ? vals[row_at(A, b0, h, A.H, t0 + r, A.e) + j] : Tin(0.f);
         }
-        a = b = 0.f;
+        g = b = 0.f;
         if (tid < n) {
             const size_t at = row_at(A, b0, h, A.H, t0 + tid, 1);
-            a = expf(gate_at(A, at));
+            if (A.g) g = A.g[at];
             b = A.beta[at];
         }
     }
@@ -70,13 +71,13 @@ struct RecRows {
         const int tid = threadIdx.x;
 #pragma unroll
         for (int r = 0; r < kRecStep; ++r) {
-            sm.k[r][tid] = k[r];
-            sm.q[r][tid] = q[r];
+            sm.k[r][tid] = to_float(k[r]);
+            sm.q[r][tid] = to_float(q[r]);
         }
 #pragma unroll
-        for (int y = 0; y < 2; ++y) sm.v[(tid + y * kRecThreads) / kRecCols][tid % kRecCols] = v[y];
+        for (int y = 0; y < 2; ++y) sm.v[(tid + y * kRecThreads) / kRecCols][tid % kRecCols] = to_float(v[y]);
         if (tid < kRecStep) {
-            sm.a[tid] = a;
+            sm.a[tid] = expf(fmaxf(g, kMinGate));
             sm.b[tid] = b;
         }
     }
@@ -126,7 +127,6 @@ gdr_rec_fwd(Args A, float* S0, float* W) {
             for (int m = 0; m < kRecRows; ++m)
                 if (r + 8 * m < A.d) to[static_cast<size_t>(r + 8 * m) * A.e] = S[m];
         }
-#pragma unroll 2
         for (int t = 0; t < m16; ++t) {
             const float a = sm.a[t];
             float p[4] = {};
@@ -197,7 +197,6 @@ gdr_rec_rev(Args A, float* dS1, float* X) {
             for (int m = 0; m < kRecRows; ++m)
                 if (r + 8 * m < A.d) to[static_cast<size_t>(r + 8 * m) * A.e] = D[m];
         }
-#pragma unroll 2
         for (int t = m16 - 1; t >= 0; --t) {
             const float dout = sm.v[t][lc];
             float p[4] = {};
