@@ -83,8 +83,8 @@ bool set_chunk_attrs() {
            set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kBackward>), sizeof(walk::Smem<D>)) &&
            set(reinterpret_cast<const void*>(walk::gdr_join<D>), sizeof(walk::JoinSmem<D>)) &&
            set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kTransfer>), sizeof(walk::Smem<D>)) &&
-           set(reinterpret_cast<const void*>(gdr_grad<D, 64>), sizeof(GradTiles<D, 64>)) &&
-           set(reinterpret_cast<const void*>(grad::gdr_grad_tc<D>), sizeof(grad::Smem<D>));
+           set(reinterpret_cast<const void*>(grad::gdr_grad_tc<D, 64>), sizeof(grad::Smem<D, 64>)) &&
+           set(reinterpret_cast<const void*>(grad::gdr_grad_tc<D, 128>), sizeof(grad::Smem<D, 128>));
 }
 
 bool set_smem_attrs() {
@@ -205,7 +205,7 @@ ChunkLayout chunk_ws(long long BH, int T, int d, int e, bool bwd) {
         w.W = w.dS1 + pages;
         w.X = w.W + rows;
         w.sums = w.X + rows;
-        at = w.sums + (e == 128 ? static_cast<size_t>(kSMs) * (64 << 10) : 0);
+        at = w.sums + static_cast<size_t>(kSMs) * (64 << 10);
     }
     if (!bwd && e == la2::gdr::walk::kE) {
         w.segs = at;
@@ -232,17 +232,17 @@ la2_status walk_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::S
     return LA2_OK;
 }
 
-template <int D>
+template <int D, int E>
 la2_status grad_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::Saved& sv, int chunks, cudaStream_t stream) {
     using namespace la2::gdr;
     CUtensorMap mk, mq, md;
     if (!row_map(&mk, A.k, A.B, A.Hk, A.T, D, A.bthd) || !row_map(&mq, A.q, A.B, A.Hk, A.T, D, A.bthd) ||
-        !row_map(&md, A.dout, A.B, A.H, A.T, grad::kE, A.bthd))
+        !row_map(&md, A.dout, A.B, A.H, A.T, E, A.bthd))
         return LA2_ERR_CUDA;
     int* status = la2::status_word();
     if (!status) return LA2_ERR_CUDA;
     const int units = A.B * A.Hk * chunks;
-    grad::gdr_grad_tc<D><<<units < kSMs ? units : kSMs, grad::kThreads, sizeof(grad::Smem<D>), stream>>>(
+    grad::gdr_grad_tc<D, E><<<units < kSMs ? units : kSMs, grad::kThreads, sizeof(grad::Smem<D, E>), stream>>>(
         A, cw, sv, chunks, units * (A.H / A.Hk), mk, mq, md, status);
     return LA2_OK;
 }
@@ -294,14 +294,14 @@ la2_status chunk_backward(const Args& A, char* ws, cudaStream_t stream) {
         const walk::Segments whole = {1, chunks, nullptr};
         la2_status st = walk_tc<D, walk::kSave>(A, cw, sv, whole, chunks, stream);
         if (st == LA2_OK) st = walk_tc<D, walk::kBackward>(A, cw, sv, whole, chunks, stream);
-        if (st == LA2_OK) st = grad_tc<D>(A, cw, sv, chunks, stream);
+        if (st == LA2_OK) st = grad_tc<D, 128>(A, cw, sv, chunks, stream);
         return st == LA2_OK ? launched() : st;
     } else {
         gdr_chain_rev<D><<<walks, kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, sv, chunks);
     }
     if (chunks > 0) {
-        const unsigned grid = static_cast<unsigned>(A.B) * A.Hk * chunks;
-        gdr_grad<D, 64><<<grid, 32 * kGradWarps, sizeof(GradTiles<D, 64>), stream>>>(A, cw, sv, chunks);
+        const la2_status st = grad_tc<D, 64>(A, cw, sv, chunks, stream);
+        if (st != LA2_OK) return st;
     }
     return launched();
 }

@@ -19,8 +19,9 @@
 //   dS0 = e^{G_C} dS1 + Q^T (e^G dO) - K^T (beta e^G X).
 //
 // gdr_prep makes N and P of all chunks at once; gdr_chain and gdr_chain_rev walk
-// the chunks of a sequence; gdr_grad, again for all chunks at once, makes
-// dq, dk, dg and dbeta (gdr_rec.cuh has its formulas).
+// the chunks of a sequence for e = 64 (gdr_walk_sm100.cuh for e = 128);
+// gdr_grad_tc (gdr_grad_sm100.cuh), again for all chunks at once, makes dq, dk,
+// dv, dg and dbeta.
 //
 // Precision: q, k, v, dO enter the products as they are (bf16, exact); every
 // operand that is formed here (states, N, P, W, X, dP, E) is split into a high
@@ -438,7 +439,7 @@ gdr_prep(Args A, ChunkWs* ws, int chunks) {
 constexpr int kWalkThreads = 128;  // 4 warps of 16 value columns
 constexpr int kWalkCols = 64;
 
-// What the walks leave for gdr_grad, per chunk: the state before it (forward)
+// What the walks leave for gdr_grad_tc, per chunk: the state before it (forward)
 // and the gradient of the state after it (backward), in a high and a low part of
 // d / 8 blocks of [e][8] (one value column's 16 bytes next to the next one's);
 // the rows w and x as fp32 [B*H][T][e].
@@ -723,6 +724,7 @@ gdr_chain(Args A, const ChunkWs* ws, Saved out, int chunks) {
         }
         __syncthreads();
     }
+    if (kSave && nc > 0) save_state<D>(S, out.S0 + (static_cast<size_t>(n) * (chunks + 1) + nc) * 2 * page, A.e, col + g, lane);
     if (!kSave && A.fin) state_out<D>(S, A.fin + n * page, A.e, col, lane);
 }
 
@@ -899,362 +901,11 @@ gdr_chain_rev(Args A, const ChunkWs* ws, Saved out, int chunks) {
                 both(kt, h2, l2);
             }
         }
-        // dv = beta X, through this warp's columns of the dO tile, which it has read
-        store_rows(A, A.dv, A.out_bf16, x, b, h, c * kC, len, col, sm.v[s], wcol, lane);
         __syncthreads();
         if (c > 0) load_mats(c - 1);
         else cp_commit();
     }
     if (A.dinit) state_out<D>(S, A.dinit + n * page, A.e, col, lane);
-}
-
-// ------------------------------------------------------------------ gdr_grad
-
-constexpr int kGradWarps = 8;
-
-template <int D, int E>
-struct GradTiles {
-    unsigned char q[kC * D * 2], k[kC * D * 2], dout[kC * E * 2];
-    unsigned char u[2][kC * E * 2], x[2][kC * E * 2];
-    unsigned char S[2][E * D * 2];
-    unsigned char dp[2][kC * kC * 2], E_[2][kC * kC * 2];
-    float coef[5][kC];  // e^G, e^{G_C - G}, beta, G / ln 2, its low part
-    float db[kC], xr[kC], part[2][kC], dG[kC], red[2 * kGradWarps];
-};
-
-// dq, dk, dg, dbeta of one chunk of key head hk, over the value heads that share
-// it in their order (formulas: gdr_rec.cuh).  Warp (rt, hf) makes rows
-// 16 rt .. 16 rt + 15 and one half of the columns of every product.
-template <int D, int E>
-__global__ void __launch_bounds__(32 * kGradWarps, 1)
-gdr_grad(Args A, const ChunkWs* ws, Saved in, int chunks) {
-    extern __shared__ __align__(128) unsigned char grad_raw[];
-    GradTiles<D, E>& sm = *reinterpret_cast<GradTiles<D, E>*>(grad_raw);
-    constexpr int kThreads = 32 * kGradWarps, kT = D / 16;  // kT: 8-column tiles of a warp's half of d
-    const int c = blockIdx.x % chunks, hk = blockIdx.x / chunks % A.Hk, b = blockIdx.x / chunks / A.Hk;
-    const int len = length_of(A, b), t0 = c * kC;
-    if (t0 >= len) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rt = warp & 3, hf = warp >> 2;
-    const int g = lane >> 2, i = lane & 3, rep = A.H / A.Hk;
-    const uint32_t qt = smem_addr(sm.q), kt = smem_addr(sm.k), dt = smem_addr(sm.dout);
-    const uint32_t uh = smem_addr(sm.u[0]), ul = smem_addr(sm.u[1]), xh = smem_addr(sm.x[0]), xl = smem_addr(sm.x[1]);
-    const uint32_t sh = smem_addr(sm.S[0]), sl = smem_addr(sm.S[1]);
-    load_tile<D, kThreads>(qt, A, A.q, b, hk, A.Hk, D, 0, t0, len);
-    load_tile<D, kThreads>(kt, A, A.k, b, hk, A.Hk, D, 0, t0, len);
-    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(A.v);
-    float accq[kT][4] = {}, acck[kT][4] = {};
-    const auto load_state = [&](const __nv_bfloat16* from) {  // [2][D / 8][E][8]
-        constexpr int kPieces = D / 8;
-        for (int y = tid; y < 2 * E * kPieces; y += kThreads) {
-            const int r = y % E, p = y / E % kPieces, part = y / E / kPieces;
-            cp16((part ? sl : sh) + piece<2 * D>(r, p), from + static_cast<size_t>(y) * 8, true);
-        }
-        cp_commit();
-    };
-    for (int hh = 0; hh < rep; ++hh) {
-        const int h = hk * rep + hh;
-        const size_t seq = static_cast<size_t>(b) * A.H + h, cn = seq * chunks + c;
-        const size_t page = static_cast<size_t>(D) * E;
-        __syncthreads();  // the tiles of the head before are read out
-        load_tile<E, kThreads>(dt, A, A.dout, b, h, A.H, E, 0, t0, len);
-        load_bytes<kThreads>(smem_addr(sm.coef), ws[cn].eg, 3 * kC * 4);
-        load_bytes<kThreads>(smem_addr(sm.coef[3]), ws[cn].g, 2 * kC * 4);
-        load_state(in.S0 + (seq * (chunks + 1) + c) * 2 * page);
-        // rows of w, x, v: u and x as two parts, dbeta and the row sums of x (w - v)
-        for (int t = warp; t < kC; t += kGradWarps) {
-            constexpr int kPer = E / 32;
-            float db = 0.f, xr = 0.f;
-            const float bt = ws[cn].beta[t];
-            float w[kPer], x[kPer];
-#pragma unroll
-            for (int y = 0; y < kPer; ++y) w[y] = x[y] = 0.f;
-            if (t0 + t < len) {
-                const size_t at = (seq * A.T + t0 + t) * E + lane * kPer;
-                const size_t io = row_at(A, b, h, A.H, t0 + t, E) + lane * kPer;
-#pragma unroll
-                for (int y = 0; y < kPer; ++y) {
-                    w[y] = in.W[at + y];
-                    x[y] = in.X[at + y];
-                    db = fmaf(x[y], w[y], db);
-                    xr = fmaf(x[y], w[y] - __bfloat162float(v[io + y]), xr);
-                }
-            }
-#pragma unroll
-            for (int y = 0; y < kPer; y += 2) {
-                const int j = lane * kPer + y;
-                const uint32_t at = piece<2 * E>(t, j >> 3) + 2 * (j & 7);
-                uint32_t hi, lo;
-                split(bt * w[y], bt * w[y + 1], hi, lo);
-                *reinterpret_cast<uint32_t*>(sm.u[0] + at) = hi;
-                *reinterpret_cast<uint32_t*>(sm.u[1] + at) = lo;
-                split(x[y], x[y + 1], hi, lo);
-                *reinterpret_cast<uint32_t*>(sm.x[0] + at) = hi;
-                *reinterpret_cast<uint32_t*>(sm.x[1] + at) = lo;
-            }
-            if constexpr (E == 128) {  // dv = beta x (at e = 64 the walk writes it)
-                if (t0 + t < len) {
-                    const size_t io = row_at(A, b, h, A.H, t0 + t, E) + lane * kPer;
-                    if (A.out_bf16)
-                        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.dv) + io) =
-                            make_uint2(pack(bt * x[0], bt * x[1]), pack(bt * x[2], bt * x[3]));
-                    else
-                        *reinterpret_cast<float4*>(static_cast<float*>(A.dv) + io) =
-                            make_float4(bt * x[0], bt * x[1], bt * x[2], bt * x[3]);
-                }
-            }
-#pragma unroll
-            for (int m = 16; m; m >>= 1) {
-                db += __shfl_xor_sync(0xffffffffu, db, m);
-                xr += __shfl_xor_sync(0xffffffffu, xr, m);
-            }
-            if (lane == 0) {
-                sm.db[t] = db;
-                sm.xr[t] = bt * xr;
-            }
-        }
-        cp_wait<0>();
-        __syncthreads();
-        const float *eg = sm.coef[0], *rest = sm.coef[1], *beta = sm.coef[2], *G = sm.coef[3], *Gl = sm.coef[4];
-        // dP and E: rows of this warp, 32 columns
-        {
-            float p[4][4] = {}, x[4][4] = {};
-            if (2 * hf <= rt) {  // else all above the diagonal
-#pragma unroll
-                for (int kk = 0; kk < E / 16; ++kk) {
-                    uint32_t da[4], xa[4], xb[4], bh[4], bl[4];
-                    ld_a<2 * E>(da, dt, rt, kk, lane);
-                    ld_a<2 * E>(xa, xh, rt, kk, lane);
-                    ld_a<2 * E>(xb, xl, rt, kk, lane);
-#pragma unroll
-                    for (int jp = 0; jp < 2; ++jp) {
-                        if (2 * hf + jp > rt) continue;
-                        ld_b<2 * E>(bh, uh, 2 * hf + jp, kk, lane);
-                        ld_b<2 * E>(bl, ul, 2 * hf + jp, kk, lane);
-                        mma2(p[2 * jp], p[2 * jp + 1], da, bh);
-                        mma2(p[2 * jp], p[2 * jp + 1], da, bl);
-                        mma2(x[2 * jp], x[2 * jp + 1], xa, bh);
-                        mma2(x[2 * jp], x[2 * jp + 1], xb, bh);
-                        mma2(x[2 * jp], x[2 * jp + 1], xa, bl);
-                    }
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int t = 16 * rt + g + 8 * half, s = 32 * hf + 8 * j + 2 * i;
-                    float pp[2], ee[2];
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const float M = s + y <= t ? exp2f((G[t] - G[s + y]) + (Gl[t] - Gl[s + y])) : 0.f;
-                        pp[y] = p[j][2 * half + y] * M;
-                        ee[y] = s + y < t ? -x[j][2 * half + y] * M * beta[t] : 0.f;
-                    }
-                    const uint32_t at = piece<128>(t, 4 * hf + j) + 4 * i;
-                    uint32_t hi, lo;
-                    split(pp[0], pp[1], hi, lo);
-                    *reinterpret_cast<uint32_t*>(sm.dp[0] + at) = hi;
-                    *reinterpret_cast<uint32_t*>(sm.dp[1] + at) = lo;
-                    split(ee[0], ee[1], hi, lo);
-                    *reinterpret_cast<uint32_t*>(sm.E_[0] + at) = hi;
-                    *reinterpret_cast<uint32_t*>(sm.E_[1] + at) = lo;
-                }
-        }
-        float fq[kT][4] = {}, row[kT][4] = {}, col[kT][4] = {};
-        // dO S0^T and X S0^T
-#pragma unroll 2
-        for (int kk = 0; kk < E / 16; ++kk) {
-            uint32_t da[4], xa[4], xb[4], bh[4], bl[4];
-            ld_a<2 * E>(da, dt, rt, kk, lane);
-            ld_a<2 * E>(xa, xh, rt, kk, lane);
-            ld_a<2 * E>(xb, xl, rt, kk, lane);
-#pragma unroll
-            for (int jp = 0; jp < kT / 2; ++jp) {
-                ld_bt<2 * D>(bh, sh, hf * (kT / 2) + jp, kk, lane);
-                ld_bt<2 * D>(bl, sl, hf * (kT / 2) + jp, kk, lane);
-                mma2(fq[2 * jp], fq[2 * jp + 1], da, bh);
-                mma2(fq[2 * jp], fq[2 * jp + 1], da, bl);
-                mma2(row[2 * jp], row[2 * jp + 1], xa, bh);
-                mma2(row[2 * jp], row[2 * jp + 1], xb, bh);
-                mma2(row[2 * jp], row[2 * jp + 1], xa, bl);
-            }
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int t = 16 * rt + g + 8 * half;
-            const float e1 = eg[t], e2 = -beta[t] * eg[t];
-#pragma unroll
-            for (int j = 0; j < kT; ++j)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    fq[j][2 * half + y] *= e1;
-                    row[j][2 * half + y] *= e2;
-                }
-        }
-        __syncthreads();  // dP, E are complete; S0 is read out
-        // <dS1, S0> from memory (S0) and what replaces it
-        load_state(in.dS1 + cn * 2 * page);
-        const uint32_t ph = smem_addr(sm.dp[0]), pl = smem_addr(sm.dp[1]);
-        const uint32_t eh = smem_addr(sm.E_[0]), el = smem_addr(sm.E_[1]);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            uint32_t a0[4], a1[4], a2[4], a3[4], bb[4];
-            if (kk <= rt) {  // rows t, columns s <= t
-                ld_a<128>(a0, ph, rt, kk, lane);
-                ld_a<128>(a1, pl, rt, kk, lane);
-                ld_a<128>(a2, eh, rt, kk, lane);
-                ld_a<128>(a3, el, rt, kk, lane);
-#pragma unroll
-                for (int jp = 0; jp < kT / 2; ++jp) {
-                    ld_bt<2 * D>(bb, kt, hf * (kT / 2) + jp, kk, lane);
-                    mma2(fq[2 * jp], fq[2 * jp + 1], a0, bb);
-                    mma2(fq[2 * jp], fq[2 * jp + 1], a1, bb);
-                    mma2(row[2 * jp], row[2 * jp + 1], a2, bb);
-                    mma2(row[2 * jp], row[2 * jp + 1], a3, bb);
-                }
-            }
-            if (kk >= rt) {  // columns s as rows, t >= s
-                ld_at<128>(a0, ph, rt, kk, lane);
-                ld_at<128>(a1, pl, rt, kk, lane);
-                ld_at<128>(a2, eh, rt, kk, lane);
-                ld_at<128>(a3, el, rt, kk, lane);
-#pragma unroll
-                for (int jp = 0; jp < kT / 2; ++jp) {
-                    ld_bt<2 * D>(bb, qt, hf * (kT / 2) + jp, kk, lane);
-                    mma2(col[2 * jp], col[2 * jp + 1], a0, bb);
-                    mma2(col[2 * jp], col[2 * jp + 1], a1, bb);
-                    ld_bt<2 * D>(bb, kt, hf * (kT / 2) + jp, kk, lane);
-                    mma2(col[2 * jp], col[2 * jp + 1], a2, bb);
-                    mma2(col[2 * jp], col[2 * jp + 1], a3, bb);
-                }
-            }
-        }
-        // q . dq of this half of d, then dq and dk take what is done
-        float qd[2] = {0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < kT; ++j)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int t = 16 * rt + g + 8 * half;
-                const uint32_t qq = *reinterpret_cast<const uint32_t*>(sm.q + piece<2 * D>(t, hf * kT + j) + 4 * i);
-                qd[half] = fmaf(low_of(qq), fq[j][2 * half], fmaf(high_of(qq), fq[j][2 * half + 1], qd[half]));
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    accq[j][2 * half + y] += fq[j][2 * half + y];
-                    acck[j][2 * half + y] += row[j][2 * half + y];
-                }
-            }
-        cp_wait<0>();
-        __syncthreads();
-        float dot = 0.f;
-        {
-            const uint32_t* s0 = reinterpret_cast<const uint32_t*>(in.S0 + (seq * (chunks + 1) + c) * 2 * page);
-            constexpr int kWords = D / 2;
-            for (int y = tid; y < E * kWords; y += kThreads) {  // word y & 3 of piece y / 4 / E of column r
-                const int r = y / 4 % E, x = y / 4 / E * 4 + y % 4;
-                const uint32_t at = piece<2 * D>(r, x >> 2) + 4 * (x & 3);
-                const uint32_t dh = *reinterpret_cast<const uint32_t*>(sm.S[0] + at);
-                const uint32_t dl = *reinterpret_cast<const uint32_t*>(sm.S[1] + at);
-                const uint32_t fh = s0[y], fl = s0[y + E * kWords];
-                dot = fmaf(low_of(dh) + low_of(dl), low_of(fh) + low_of(fl), dot);
-                dot = fmaf(high_of(dh) + high_of(dl), high_of(fh) + high_of(fl), dot);
-            }
-        }
-        // U dS1^T
-        float cs[kT][4] = {};
-#pragma unroll 2
-        for (int kk = 0; kk < E / 16; ++kk) {
-            uint32_t ua[4], ub[4], bh[4], bl[4];
-            ld_a<2 * E>(ua, uh, rt, kk, lane);
-            ld_a<2 * E>(ub, ul, rt, kk, lane);
-#pragma unroll
-            for (int jp = 0; jp < kT / 2; ++jp) {
-                ld_bt<2 * D>(bh, sh, hf * (kT / 2) + jp, kk, lane);
-                ld_bt<2 * D>(bl, sl, hf * (kT / 2) + jp, kk, lane);
-                mma2(cs[2 * jp], cs[2 * jp + 1], ua, bh);
-                mma2(cs[2 * jp], cs[2 * jp + 1], ub, bh);
-                mma2(cs[2 * jp], cs[2 * jp + 1], ua, bl);
-            }
-        }
-        float gc = 0.f;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int t = 16 * rt + g + 8 * half;
-            const float r = rest[t];
-            float kd = 0.f;
-#pragma unroll
-            for (int j = 0; j < kT; ++j) {
-                const uint32_t kw = *reinterpret_cast<const uint32_t*>(sm.k + piece<2 * D>(t, hf * kT + j) + 4 * i);
-                const float k0 = low_of(kw), k1 = high_of(kw);
-                const float c0 = r * cs[j][2 * half], c1 = r * cs[j][2 * half + 1];
-                gc = fmaf(k0, c0, fmaf(k1, c1, gc));
-                const float d0 = c0 + col[j][2 * half], d1 = c1 + col[j][2 * half + 1];
-                kd = fmaf(k0, d0, fmaf(k1, d1, kd));
-                acck[j][2 * half] += d0;
-                acck[j][2 * half + 1] += d1;
-            }
-            float y = qd[half] - kd;
-            y += __shfl_xor_sync(0xffffffffu, y, 1);
-            y += __shfl_xor_sync(0xffffffffu, y, 2);
-            if (i == 0) sm.part[hf][t] = y;
-        }
-#pragma unroll
-        for (int m = 16; m; m >>= 1) {
-            gc += __shfl_xor_sync(0xffffffffu, gc, m);
-            dot += __shfl_xor_sync(0xffffffffu, dot, m);
-        }
-        if (lane == 0) {
-            sm.red[warp] = gc;
-            sm.red[kGradWarps + warp] = dot;
-        }
-        __syncthreads();
-        if (warp == 0) {  // sums of dL/dG from each row to the chunk's end: two rows per lane
-            const int t = 2 * lane;
-            float y0 = sm.part[0][t] + sm.part[1][t] + sm.xr[t];
-            float y1 = sm.part[0][t + 1] + sm.part[1][t + 1] + sm.xr[t + 1];
-            if (lane == 31) {
-                float d1 = 0.f, d2 = 0.f;
-                for (int w = 0; w < kGradWarps; ++w) {
-                    d1 += sm.red[w];
-                    d2 += sm.red[kGradWarps + w];
-                }
-                y1 += fmaf(eg[kC - 1], d2, d1);
-            }
-            float s = y0 + y1;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const float z = __shfl_down_sync(0xffffffffu, s, m);
-                if (lane + m < 32) s += z;
-            }
-            if (A.dg) {
-                if (t0 + t < len) A.dg[row_at(A, b, h, A.H, t0 + t, 1)] = s;
-                if (t0 + t + 1 < len) A.dg[row_at(A, b, h, A.H, t0 + t + 1, 1)] = s - y0;
-            }
-        } else if (warp < 3) {
-            const int t = tid - 32;
-            if (t0 + t < len) A.dbeta[row_at(A, b, h, A.H, t0 + t, 1)] = sm.db[t];
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < kT; ++j)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int t = t0 + 16 * rt + g + 8 * half;
-            if (t < len) {
-                const size_t at = row_at(A, b, hk, A.Hk, t, D) + 8 * (hf * kT + j) + 2 * i;
-                if (A.out_bf16) {
-                    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(A.dq) + at) =
-                        pack(accq[j][2 * half], accq[j][2 * half + 1]);
-                    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(A.dk) + at) =
-                        pack(acck[j][2 * half], acck[j][2 * half + 1]);
-                } else {
-                    *reinterpret_cast<float2*>(static_cast<float*>(A.dq) + at) =
-                        make_float2(accq[j][2 * half], accq[j][2 * half + 1]);
-                    *reinterpret_cast<float2*>(static_cast<float*>(A.dk) + at) =
-                        make_float2(acck[j][2 * half], acck[j][2 * half + 1]);
-                }
-            }
-        }
 }
 
 }  // namespace gdr

@@ -1,6 +1,6 @@
-// gdr_grad_sm100.cuh -- dq, dk, dv, dg and dbeta of the gated delta rule for
-// e = 128 on the tcgen05 tensor cores, all chunks independently, from what the
-// walks left (gdr_walk_sm100.cuh): per chunk the state S0 before it, the gradient
+// gdr_grad_sm100.cuh -- dq, dk, dv, dg and dbeta of the gated delta rule for d, e
+// in {64, 128} on the tcgen05 tensor cores, all chunks independently, from what the
+// walks left (gdr_walk_sm100.cuh, gdr_chunk.cuh): per chunk the state S0 before it, the gradient
 // dS1 of the state after it, and the rows w and x.  With U = beta W:
 //
 //   dP = M o (dO U^T),   E_ts = -beta_t M_ts (x_t . u_s)  (s < t)
@@ -37,7 +37,6 @@ using walk::bulk_load;
 using walk::elect;
 using walk::Waiter;
 
-constexpr int kE = 128;
 constexpr int kThreads = 512;
 constexpr int kEpiWarps = 8, kRowWarps = 4;
 constexpr int kFactors = 9;  // eg .. gl of ChunkWs
@@ -46,14 +45,14 @@ enum Bar { kRows = 0, kRowsFree, kKQ, kKQFree, kXU, kXUFree, kRing, kRingFree = 
            kPEFull, kDone, kFree, kSums, kSumsFree = kSums + 2, kPart = kSumsFree + 2, kDot = kPart + 2,
            kRaw = kDot + 2, kEpi, kEnd, kBars };
 
-template <int D>
+template <int D, int E>
 struct Smem {
     // 64 columns of e: rows of dO, X hi, X lo (the operand [dO; X hi] and, one tile on, [X hi; X lo])
-    unsigned char dx[kE / 64][3][kC * 128];
-    unsigned char u[kE / 64][2][kC * 128];   // U hi, U lo
+    unsigned char dx[E / 64][3][kC * 128];
+    unsigned char u[E / 64][2][kC * 128];   // U hi, U lo
     unsigned char k[D / 64][kC * 128], q[D / 64][kC * 128];
     unsigned char pe[2][2][kC * 128];        // hi, lo: rows of dP, rows of E
-    unsigned char ring[2][D * kE * 2];       // one part of a state: [d / 8][e][8]
+    unsigned char ring[2][D * E * 2];       // one part of a state: [d / 8][e][8]
     float f[2][kFactors][kC];                // factors, by item parity
     float dbeta[2][kC], xv[2][kC];           // row sums, by item parity
     float part[2][4][kC];                    // q . dq - k . col of a quadrant's rows of d, by item parity
@@ -91,13 +90,13 @@ __device__ __forceinline__ void tmem_frag(uint32_t taddr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-template <int D>
+template <int D, int E>
 __global__ void __launch_bounds__(kThreads, 1)
 gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __grid_constant__ CUtensorMap mk,
             const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap md, int* status) {
     extern __shared__ __align__(1024) unsigned char grad_tc_raw[];
-    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(grad_tc_raw);
-    constexpr uint32_t kTile = kC * 128, kPiece = D * kE * 2;
+    Smem<D, E>& sm = *reinterpret_cast<Smem<D, E>*>(grad_tc_raw);
+    constexpr uint32_t kTile = kC * 128, kPiece = D * E * 2;
     constexpr uint32_t cPE = 0, cA = 128, cB = 256, cC = 384;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rep = A.H / A.Hk;
@@ -178,12 +177,11 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             };
             if (y > 0 && !wait(kRowsFree, y - 1)) return false;
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar(kRows), 2 * kTile);
-                tile(sm.dx[0][0], md, x.h, 0, kRows);
-                tile(sm.dx[1][0], md, x.h, 1, kRows);
+                mbar_arrive_expect_tx(bar(kRows), (E / 64) * kTile);
+                for (int z = 0; z < E / 64; ++z) tile(sm.dx[z][0], md, x.h, z, kRows);
             }
             rows = y + 1;
-            const size_t page = static_cast<size_t>(D) * kE;
+            const size_t page = static_cast<size_t>(D) * E;
             const auto piece_in = [&](int z) {
                 const int s = z & 1, p = 4 * y + z;
                 if (p >= 2 && !wait(kRingFree + s, (p >> 1) - 1)) return false;
@@ -241,12 +239,12 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             tc_fence_after();
             if (elect()) {
 #pragma unroll
-                for (int kk = 0; kk < kE / 16; ++kk) {
+                for (int kk = 0; kk < E / 16; ++kk) {
                     const uint32_t a = (kk >> 2) * kDx + (kk & 3) * 32, b = (kk >> 2) * kU + (kk & 3) * 32;
                     mma_bf16_ss(cPE, desc_add(dO, a), desc_add(uh, b), kIdPE, kk > 0);
                 }
 #pragma unroll
-                for (int kk = 0; kk < kE / 16; ++kk) {
+                for (int kk = 0; kk < E / 16; ++kk) {
                     const uint32_t a = (kk >> 2) * kDx + (kk & 3) * 32, b = (kk >> 2) * kU + (kk & 3) * 32;
                     mma_bf16_ss(cB, desc_add(xh, a), desc_add(uh, b), kIdPE2, kk > 0);  // rows 64 ..: X lo U hi
                 }
@@ -258,9 +256,9 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                 if (!wait(kRing + s, p >> 1)) return false;
                 tc_fence_after();
                 if (elect()) {
-                    const uint64_t st = sdesc_blocks(smem_addr(sm.ring[s]), kE * 16);
+                    const uint64_t st = sdesc_blocks(smem_addr(sm.ring[s]), E * 16);
 #pragma unroll
-                    for (int kk = 0; kk < kE / 16; ++kk) {
+                    for (int kk = 0; kk < E / 16; ++kk) {
                         const uint32_t b = (kk >> 2) * kDx + (kk & 3) * 32;
                         const uint64_t a = desc_add(st, kk * 256);
                         mma_bf16_ss(cA, a, desc_add(dO, b), kIdS, z + kk > 0);
@@ -277,9 +275,9 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                 if (!wait(kRing + s, p >> 1)) return false;
                 tc_fence_after();
                 if (elect()) {
-                    const uint64_t st = sdesc_blocks(smem_addr(sm.ring[s]), kE * 16);
+                    const uint64_t st = sdesc_blocks(smem_addr(sm.ring[s]), E * 16);
 #pragma unroll
-                    for (int kk = 0; kk < kE / 16; ++kk)
+                    for (int kk = 0; kk < E / 16; ++kk)
                         mma_bf16_ss(cC, desc_add(st, kk * 256), desc_add(uh, (kk >> 2) * kU + (kk & 3) * 32), kIdSU,
                                     z > 2 || kk > 0);
                     mma_commit(bar(kRingFree + s));
@@ -316,11 +314,11 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
     } else if (warp < 4) {
         each([&](const Item& x, int y) {
             const int t0 = x.c * kC, t = 2 * lane;
-            const size_t seq = static_cast<size_t>(x.b) * A.H + x.h, page = static_cast<size_t>(D) * kE;
+            const size_t seq = static_cast<size_t>(x.b) * A.H + x.h, page = static_cast<size_t>(D) * E;
             // <dS1, S1>, half of the 16-byte pieces: warp 2 and warp 3 take turns of 32
             const uint4* s1 = reinterpret_cast<const uint4*>(in.S0 + (seq * (chunks + 1) + x.c + 1) * 2 * page);
             const uint4* d1 = reinterpret_cast<const uint4*>(in.dS1 + (seq * chunks + x.c) * 2 * page);
-            constexpr int kPieces = D * kE / 8;  // of one part
+            constexpr int kPieces = D * E / 8;  // of one part
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
             for (int z = (warp - 2) * 32 + lane; z < kPieces; z += 4 * 64) {
@@ -594,36 +592,40 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
     } else if (warp >= 12) {
         const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(A.v);
         each([&](const Item& x, int y) {
-            const int t0 = x.c * kC, col = 4 * lane;
+            // E / 4 lanes hold a row, four columns each: a slot is one row (E = 128) or two (E = 64)
+            constexpr int kLanes = E / 4, kPer = 32 / kLanes;
+            const int t0 = x.c * kC, col = 4 * (lane % kLanes);
             const size_t seq = static_cast<size_t>(x.b) * A.H + x.h;
             const ChunkWs& cw = ws[seq * chunks + x.c];
+            const size_t step = A.bthd ? static_cast<size_t>(A.H) * E : E;
 #pragma unroll 1
-            for (int z = 0; z < 2; ++z) {  // 8 rows at a time, all loads first
+            for (int z = 0; z < 2 / kPer; ++z) {  // 8 slots at a time, all loads first
+                const int row0 = 16 * (warp - 12) + 8 * z + lane / kLanes;  // of slot 0; slot r: kPer r further
+                const int left = x.len - t0 - row0;
+                const size_t io = row_at(A, x.b, x.h, A.H, t0 + row0, E) + col;
                 float4 w[8], xx[8];
                 uint2 vv[8];
                 float bt[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                    const int t = 16 * (warp - 12) + 8 * z + r;
                     w[r] = xx[r] = make_float4(0.f, 0.f, 0.f, 0.f);
                     vv[r] = make_uint2(0, 0);
                     bt[r] = 0.f;
-                    if (t0 + t < x.len) {
-                        const size_t at = (seq * A.T + t0 + t) * kE + col;
+                    if (kPer * r < left) {
+                        const size_t at = (seq * A.T + t0 + row0 + kPer * r) * E + col;
                         w[r] = *reinterpret_cast<const float4*>(in.W + at);
                         xx[r] = *reinterpret_cast<const float4*>(in.X + at);
-                        vv[r] = *reinterpret_cast<const uint2*>(v + row_at(A, x.b, x.h, A.H, t0 + t, kE) + col);
-                        bt[r] = cw.beta[t];
+                        vv[r] = *reinterpret_cast<const uint2*>(v + io + kPer * r * step);
+                        bt[r] = cw.beta[row0 + kPer * r];
                     }
                 }
                 // the MMAs have read the operands of the item before, warp 3 the row sums of the one before that
                 if (z == 0 && y > 0 && !wait(kXUFree, y - 1)) return false;
                 if (z == 0 && y > 1 && !wait(kSumsFree + (y & 1), (y >> 1) - 1)) return false;
-                float sum[16];  // of each row: x . w, beta x . (w - v)
-                const int row0 = 16 * (warp - 12) + 8 * z;
+                float sum[16];  // of each slot: x . w, beta x . (w - v)
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                    const uint32_t at = piece<128>(row0 + r, (col & 63) >> 3) + 2 * (col & 7);
+                    const uint32_t at = piece<128>(row0 + kPer * r, (col & 63) >> 3) + 2 * (col & 7);
                     uint32_t h0, h1, l0, l1;
                     split(bt[r] * w[r].x, bt[r] * w[r].y, h0, l0);
                     split(bt[r] * w[r].z, bt[r] * w[r].w, h1, l1);
@@ -637,9 +639,9 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                     sum[2 * r + 1] = bt[r] * fmaf(xx[r].x, w[r].x - low_of(vv[r].x), fmaf(xx[r].y, w[r].y - high_of(vv[r].x),
                                                   fmaf(xx[r].z, w[r].z - low_of(vv[r].y), xx[r].w * (w[r].w - high_of(vv[r].y)))));
                 }
-                // 16 sums over 32 lanes, halving what a lane holds with each exchange: lane l ends with sum l / 2
+                // 16 sums over the lanes of a row, halving what a lane holds with each exchange
 #pragma unroll
-                for (int m = 16, held = 8; m > 1; m >>= 1, held >>= 1)
+                for (int m = kLanes / 2, held = 8; held > 0; m >>= 1, held >>= 1)
 #pragma unroll
                     for (int y2 = 0; y2 < 8; ++y2)
                         if (y2 < held) {
@@ -647,24 +649,22 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                             const float give = up ? sum[y2] : sum[held + y2], keep = up ? sum[held + y2] : sum[y2];
                             sum[y2] = keep + __shfl_xor_sync(0xffffffffu, give, m);
                         }
-                sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
-                if ((lane & 1) == 0) (lane & 2 ? sm.xv : sm.dbeta)[y & 1][row0 + (lane >> 2)] = sum[0];
-                const size_t out0 = row_at(A, x.b, x.h, A.H, t0 + row0, kE) + col;
-                const size_t step = A.bthd ? static_cast<size_t>(A.H) * kE : kE;
-                const int left = x.len - t0 - row0;
+                if (E == 128) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
+                const int mine_ = lane % kLanes / (E == 128 ? 2 : 1);  // which sum this lane ended with
+                if (E == 64 || (lane & 1) == 0) (mine_ & 1 ? sm.xv : sm.dbeta)[y & 1][row0 + kPer * (mine_ >> 1)] = sum[0];
                 if (A.out_bf16) {
-                    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(A.dv) + out0;
+                    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(A.dv) + io;
 #pragma unroll
                     for (int r = 0; r < 8; ++r)
-                        if (r < left)
-                            *reinterpret_cast<uint2*>(p + r * step) = make_uint2(pack(bt[r] * xx[r].x, bt[r] * xx[r].y),
-                                                                                 pack(bt[r] * xx[r].z, bt[r] * xx[r].w));
+                        if (kPer * r < left)
+                            *reinterpret_cast<uint2*>(p + kPer * r * step) = make_uint2(
+                                pack(bt[r] * xx[r].x, bt[r] * xx[r].y), pack(bt[r] * xx[r].z, bt[r] * xx[r].w));
                 } else {
-                    float* p = static_cast<float*>(A.dv) + out0;
+                    float* p = static_cast<float*>(A.dv) + io;
 #pragma unroll
                     for (int r = 0; r < 8; ++r)
-                        if (r < left)
-                            *reinterpret_cast<float4*>(p + r * step) =
+                        if (kPer * r < left)
+                            *reinterpret_cast<float4*>(p + kPer * r * step) =
                                 make_float4(bt[r] * xx[r].x, bt[r] * xx[r].y, bt[r] * xx[r].z, bt[r] * xx[r].w);
                 }
             }
