@@ -607,12 +607,18 @@ def _need(t, name, shape, dtype, device) -> None:
 
 
 class _On:
-    """The tensors' device made current for a call, where it is not already."""
+    """The tensors' device, and the caller's stream if one is given, made current for a call: what
+    the call allocates (and sets to zero) belongs to the stream that its kernels run on."""
 
-    def __init__(self, device):
+    def __init__(self, device, stream=None):
         if device.type != "cuda":
             raise ValueError("the tensors must be CUDA tensors")
-        self._guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+            self._guard = torch.cuda.stream(stream)
+        else:
+            self._guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
     def __enter__(self):
         if self._guard is not None:
@@ -623,14 +629,12 @@ class _On:
             self._guard.__exit__(*exc)
 
 
-def _stream_on(stream, device) -> int:
-    """The caller's stream, or the current stream of the tensors' device."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    return int(stream.cuda_stream)
+def _stream_on(device) -> int:
+    """The current stream of the tensors' device (inside _On: the caller's stream)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _own_workspace(nbytes: int, device, stream, workspace):
+def _own_workspace(nbytes: int, device, workspace):
     """(pointer, size, tensor): the caller's workspace, or one of this call's own.
 
     A call allocates its workspace from torch's caching allocator on the stream
@@ -642,11 +646,7 @@ def _own_workspace(nbytes: int, device, stream, workspace):
         return p, n, workspace
     if nbytes <= 0:
         return 0, 0, None
-    if stream is None:
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    else:
-        with torch.cuda.stream(stream):
-            buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return buf.data_ptr(), nbytes, buf
 
 
@@ -702,16 +702,15 @@ def la2_gdr_fwd(q, k, v, g, beta, layout: str = "bhtd", init_state=None, seq_len
                                         {"init_state": init_state, "final_state": final_state})
     odt, oc = _out_dtype(out_dtype)
     shape = _shape(layout, B, H, T, e)
-    with _On(q.device):
-        sp = _stream_on(stream, q.device)
+    with _On(q.device, stream):
+        sp = _stream_on(q.device)
         if out is None:
             out = (torch.empty if seq_lens is None else torch.zeros)(shape, dtype=odt, device=q.device)
         else:
             _need(out, "out", shape, odt, q.device)
         if final_state is None and want_final:
             final_state = torch.empty((B, H, d, e), dtype=torch.float32, device=q.device)
-        wp, wn, keep = _own_workspace(la2_gdr_workspace_bytes(B, Hk, H, T, d, e, dt, 0), q.device,
-                                      stream, workspace)
+        wp, wn, keep = _own_workspace(la2_gdr_workspace_bytes(B, Hk, H, T, d, e, dt, 0), q.device, workspace)
         st = la2_gdr_fwd_raw(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), beta.data_ptr(),
                              out.data_ptr(), _ptr(init_state), _ptr(final_state), _ptr(seq_lens),
                              B, Hk, H, T, d, e, dt, oc, _LAYOUTS[layout], wp, wn, sp)
@@ -735,8 +734,8 @@ def la2_gdr_bwd(q, k, v, g, beta, dout, layout: str = "bhtd", init_state=None, d
         raise ValueError("dg needs a gate g")
     gate = tuple(beta.shape)
     new = torch.empty if seq_lens is None else torch.zeros
-    with _On(q.device):
-        sp = _stream_on(stream, q.device)
+    with _On(q.device, stream):
+        sp = _stream_on(q.device)
         o = dict(dtype=odt, device=q.device)
         f = dict(dtype=torch.float32, device=q.device)
         dq = new(_shape(layout, B, Hk, T, d), **o) if dq is None else dq
@@ -751,8 +750,7 @@ def la2_gdr_bwd(q, k, v, g, beta, dout, layout: str = "bhtd", init_state=None, d
                                       ("dbeta", dbeta, gate, torch.float32), ("dg", dg, gate, torch.float32)):
             if t is not None:
                 _need(t, name, shape, dtype, q.device)
-        wp, wn, keep = _own_workspace(la2_gdr_workspace_bytes(B, Hk, H, T, d, e, dt, 1), q.device,
-                                      stream, workspace)
+        wp, wn, keep = _own_workspace(la2_gdr_workspace_bytes(B, Hk, H, T, d, e, dt, 1), q.device, workspace)
         st = la2_gdr_bwd_raw(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), beta.data_ptr(),
                              dout.data_ptr(), _ptr(init_state), _ptr(d_final_state), dq.data_ptr(),
                              dk.data_ptr(), dv.data_ptr(), _ptr(dg), dbeta.data_ptr(),
@@ -789,8 +787,8 @@ def la2_gdr_decode(q, k, v, g, beta, states, slots=None, out=None, stream=None) 
         _need(slots, "slots", (B,), torch.int32, dev)
     elif n_slots < B:
         raise ValueError(f"{B} sequences but {n_slots} slots")
-    with _On(dev):
-        sp = _stream_on(stream, dev)
+    with _On(dev, stream):
+        sp = _stream_on(dev)
         if out is None:
             out = torch.empty((B, H, e), dtype=torch.float32, device=dev)
         else:
@@ -813,10 +811,10 @@ def la2_state_copy(states, src, dst, stream=None) -> torch.Tensor:
     _need(states, "states", states.shape, torch.float32, dev)
     _need(src, "src", (n,), torch.int32, dev)
     _need(dst, "dst", (n,), torch.int32, dev)
-    with _On(dev):
+    with _On(dev, stream):
         st = la2_state_copy_raw(states.data_ptr(), src.data_ptr(), dst.data_ptr(), n, n_slots,
                                 states.numel() // n_slots if n_slots else 0,
-                                _stream_on(stream, dev))
+                                _stream_on(dev))
     if st != LA2_OK:
         raise LA2Error(st, "la2_state_copy")
     return states

@@ -415,7 +415,13 @@ la2_status la2_bwd_norm(const void *q, const void *k, const void *v, const float
  * memory of at least la2_gdr_workspace_bytes() bytes, 256-byte aligned, not
  * used by another call that may run at the same time; it grows with T (the
  * backward keeps the state at each chunk's border).  The result does not
- * depend on scheduling (no atomics).  Asynchronous on `stream`.
+ * depend on scheduling (no atomics).  Asynchronous on `stream`; make the first
+ * call on a device before any stream capture (it looks up device addresses).
+ *
+ * bf16 with d and e in {64, 128} runs by 64-row chunks on the tensor cores, every
+ * operand formed on the way held as two bf16 parts (2^-16 of a value is lost;
+ * fp32 results are off by a few 2^-18 of their norm); everything else token by
+ * token in fp32.
  *
  * la2_gdr_bwd gives the gradients of
  * L = sum_t dout_t . out_t + <d_final_state, S_last>.

@@ -334,12 +334,18 @@ def test_ragged_batches_leave_rows_behind_the_end(gpu, dtype, d, e, layout):
     _check_bwd(gpu, x, layout)
     y = _put(x, layout, gpu)
     mark = 7.0
-    like = lambda t, dt=torch.float32: torch.full(t.shape, mark, dtype=dt, device=gpu)  # noqa: E731
-    o = like(y["v"])
-    L.la2_gdr_fwd(y["q"], y["k"], y["v"], y["g"], y["beta"], layout=layout, seq_lens=y["lens"], out=o)
-    outs = dict(dq=like(y["q"]), dk=like(y["k"]), dv=like(y["v"]), dg=like(y["g"]), dbeta=like(y["beta"]))
-    L.la2_gdr_bwd(y["q"], y["k"], y["v"], y["g"], y["beta"], y["do"], layout=layout, seq_lens=y["lens"], **outs)
-    for name, t in dict(outs, o=o).items():
+    for odt in {F32, dtype}:
+        like = lambda t, dt=odt: torch.full(t.shape, mark, dtype=dt, device=gpu)  # noqa: E731,B023
+        o = like(y["v"])
+        L.la2_gdr_fwd(y["q"], y["k"], y["v"], y["g"], y["beta"], layout=layout, seq_lens=y["lens"], out=o, out_dtype=odt)
+        outs = dict(dq=like(y["q"]), dk=like(y["k"]), dv=like(y["v"]), dg=like(y["g"], F32), dbeta=like(y["beta"], F32))
+        L.la2_gdr_bwd(y["q"], y["k"], y["v"], y["g"], y["beta"], y["do"], layout=layout, seq_lens=y["lens"],
+                      out_dtype=odt, **outs)
+        _marked(dict(outs, o=o), layout, lens, T, mark)
+
+
+def _marked(outs, layout, lens, T, mark):
+    for name, t in outs.items():
         t = t.transpose(1, 2) if layout == "bthd" else t
         for b, m in enumerate(lens):
             m = min(max(m, 0), T)
@@ -428,13 +434,15 @@ def test_long_sequences_in_segments(gpu, B, Hk, H, T, d, lens):
 
 
 @pytest.mark.gpu
-def test_empty_sequences_hand_states_on(gpu):
-    s = torch.randn(2, 2, 8, 8, device=gpu)
-    z = torch.zeros(2, 2, 0, 8, device=gpu)
-    o, S = L.la2_gdr_fwd(z, z, z, z[..., 0], z[..., 0], init_state=s, want_final=True)
+@pytest.mark.parametrize("dtype,d,e", [(F32, 8, 8), (BF16, 64, 64), (BF16, 128, 128), (BF16, 64, 128)])
+def test_empty_sequences_hand_states_on(gpu, dtype, d, e):
+    s = torch.randn(2, 2, d, e, device=gpu)
+    z, v = (torch.zeros(2, 2, 0, n, device=gpu, dtype=dtype) for n in (d, e))
+    g = torch.zeros(2, 2, 0, device=gpu)
+    o, S = L.la2_gdr_fwd(z, z, v, g, g, init_state=s, want_final=True)
     assert o.numel() == 0 and torch.equal(S, s)
-    assert torch.equal(L.la2_gdr_bwd(z, z, z, z[..., 0], z[..., 0], z, d_final_state=s, want_d_init=True)[5], s)
-    S = L.la2_gdr_fwd(z, z, z, None, z[..., 0], want_final=True)[1]
+    assert torch.equal(L.la2_gdr_bwd(z, z, v, g, g, v, d_final_state=s, want_d_init=True)[5], s)
+    S = L.la2_gdr_fwd(z, z, v, None, g, want_final=True)[1]
     assert not S.any()
 
 
@@ -605,6 +613,25 @@ def test_prefill_fork_and_decode(gpu, dtype, d):
         _close(got, ro[0, :, n:], TOL[dtype], name="o")
         _close(pool[int(slots[row])].double().cpu(), rS[0], TOL[dtype], name="state")
     assert not pool[3].any() and torch.isnan(pool[2]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 32)])
+def test_calls_on_a_given_stream(gpu, dtype, d):
+    """A stream argument: what the call allocates and clears is ordered on that stream."""
+    x = R.make(3, 1, 2, 90, d, d, dtype, 50, final=True, lens=[90, 3, 0])
+    y = _put(x, "bhtd", gpu)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)  # the current stream is behind: work that lands on it comes too late
+    o, S = L.la2_gdr_fwd(y["q"], y["k"], y["v"], y["g"], y["beta"], seq_lens=y["lens"], want_final=True, stream=side)
+    dq = L.la2_gdr_bwd(y["q"], y["k"], y["v"], y["g"], y["beta"], y["do"], d_final_state=y["dfinal"],
+                       seq_lens=y["lens"], stream=side)[0]
+    side.synchronize()
+    ro, rS = R.forward(x)
+    _close(o.double().cpu(), ro, TOL[dtype], name="o")
+    _close(S.double().cpu(), rS, TOL[dtype], name="state")
+    _close(dq.double().cpu(), R.backward(x)["dq"], TOL[dtype], name="dq")
 
 
 @pytest.mark.gpu
