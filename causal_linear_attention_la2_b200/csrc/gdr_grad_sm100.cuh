@@ -21,9 +21,11 @@
 // 80 KB (d = 128), which is what bounds it; warps:
 //   0      loads: dO and factors, K and Q, the four state parts through a ring
 //   1      MMAs
-//   2, 3   <dS1, S1> (both states out of L2); 3: dg, dbeta; 2: TMEM allocation
-//   4-11   epilogues: dP and E as operands; dq, dk, q . dq
-//   12-15  w, x -> operands U, X; dv, and the sums of rows for dbeta and dg
+//   2      TMEM allocation;  3  dg, dbeta
+//   4-19   epilogues: dP and E as operands; <dS1, S1>; dq, dk, q . dq (16 columns a warp: what a
+//          warp does to an item is one long dependent chain, and 8 warps of 32
+//          columns take nearly twice as long, 650 us against EPITIME on the 15B layer)
+//   20-23  w, x -> operands U, X; dv, and the sums of rows for dbeta and dg
 // Waits are bounded as in gdr_walk_sm100.cuh.
 #pragma once
 #include "gdr_walk_sm100.cuh"
@@ -37,13 +39,12 @@ using walk::bulk_load;
 using walk::elect;
 using walk::Waiter;
 
-constexpr int kThreads = 512;
-constexpr int kEpiWarps = 8, kRowWarps = 4;
+constexpr int kThreads = 768;
+constexpr int kEpiWarps = 16, kRowWarps = 4, kRowWarp0 = 4 + kEpiWarps;
 constexpr int kFactors = 9;  // eg .. gl of ChunkWs
 
 enum Bar { kRows = 0, kRowsFree, kKQ, kKQFree, kXU, kXUFree, kRing, kRingFree = kRing + 2, kPE = kRingFree + 2,
-           kPEFull, kDone, kFree, kSums, kSumsFree = kSums + 2, kPart = kSumsFree + 2, kDot = kPart + 2,
-           kRaw = kDot + 2, kEpi, kEnd, kBars };
+           kPEFull, kDone, kFree, kSums, kSumsFree = kSums + 2, kPart = kSumsFree + 2, kRaw = kPart + 2, kEpi, kEnd, kBars };
 
 template <int D, int E>
 struct Smem {
@@ -56,7 +57,7 @@ struct Smem {
     float f[2][kFactors][kC];                // factors, by item parity
     float dbeta[2][kC], xv[2][kC];           // row sums, by item parity
     float part[2][4][kC];                    // q . dq - k . col of a quadrant's rows of d, by item parity
-    float dot[2];                            // warp 2's half of <dS1, S1>, by item parity
+    float dot[2][kEpiWarps];                 // <dS1, S1> in parts, by item parity
     unsigned long long bar[kBars];
     uint32_t tmem;
     int abort;
@@ -74,20 +75,18 @@ __device__ __forceinline__ uint64_t sdesc_blocks(uint32_t addr, uint32_t mn) {
     return d;
 }
 
-// 16 lanes x 32 columns of TMEM as fragments (the layout of ptx_sm100.cuh's pair of
-// such loads), waited for in the same statement
-__device__ __forceinline__ void tmem_frag(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
+// 16 lanes x 16 columns of TMEM as fragments (v[4 j ..]: columns 8 j .., as in
+// ptx_sm100.cuh's pair of such loads), waited for in the same statement
+__device__ __forceinline__ void tmem_frag(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
         : "r"(taddr)
         : "memory");
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 template <int D, int E>
@@ -115,10 +114,8 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
         mbar_init(bar(kSums + 1), kRowWarps);
         mbar_init(bar(kSumsFree), 1);
         mbar_init(bar(kSumsFree + 1), 1);
-        for (int z = 0; z < 2; ++z) {
-            mbar_init(bar(kPart + z), kEpiWarps);
-            mbar_init(bar(kDot + z), 1);
-        }
+        mbar_init(bar(kPart), kEpiWarps);
+        mbar_init(bar(kPart + 1), kEpiWarps);
         mbar_init(bar(kPEFull), kEpiWarps);
         mbar_init(bar(kFree), kEpiWarps);
         mbar_init(bar(kEpi), kEpiWarps);
@@ -312,50 +309,9 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
         if (elect()) mma_commit(bar(kEnd));
         mbar_wait(bar(kEnd), 0);
     } else if (warp < 4) {
-        each([&](const Item& x, int y) {
+        if (warp == 3) each([&](const Item& x, int y) {
             const int t0 = x.c * kC, t = 2 * lane;
-            const size_t seq = static_cast<size_t>(x.b) * A.H + x.h, page = static_cast<size_t>(D) * E;
-            // <dS1, S1>, half of the 16-byte pieces: warp 2 and warp 3 take turns of 32
-            const uint4* s1 = reinterpret_cast<const uint4*>(in.S0 + (seq * (chunks + 1) + x.c + 1) * 2 * page);
-            const uint4* d1 = reinterpret_cast<const uint4*>(in.dS1 + (seq * chunks + x.c) * 2 * page);
-            constexpr int kPieces = D * E / 8;  // of one part
-            float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-            for (int z = (warp - 2) * 32 + lane; z < kPieces; z += 4 * 64) {
-                uint4 v[4][4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    v[r][0] = s1[z + 64 * r];
-                    v[r][1] = s1[z + 64 * r + kPieces];
-                    v[r][2] = d1[z + 64 * r];
-                    v[r][3] = d1[z + 64 * r + kPieces];
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const auto take = [&](uint32_t sh, uint32_t sl, uint32_t dh, uint32_t dl) {
-                        const float2 s2 = make_float2(low_of(sh) + low_of(sl), high_of(sh) + high_of(sl));
-                        const float2 d2 = make_float2(low_of(dh) + low_of(dl), high_of(dh) + high_of(dl));
-                        sum = fma2(s2, d2, sum);
-                    };
-                    take(v[r][0].x, v[r][1].x, v[r][2].x, v[r][3].x);
-                    take(v[r][0].y, v[r][1].y, v[r][2].y, v[r][3].y);
-                    take(v[r][0].z, v[r][1].z, v[r][2].z, v[r][3].z);
-                    take(v[r][0].w, v[r][1].w, v[r][2].w, v[r][3].w);
-                }
-            }
-            float dot = sum.x + sum.y;
-#pragma unroll
-            for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-            if (warp == 2) {
-                // (warp 3 has left the item before the last one: kSumsFree)
-                if (y >= 2 && !wait(kSumsFree + (y & 1), (y >> 1) - 1)) return false;
-                if (lane == 0) {
-                    sm.dot[y & 1] = dot;
-                    arrive(bar(kDot + (y & 1)));
-                }
-                return true;
-            }
-            if (!(wait(kPart + (y & 1), y >> 1) && wait(kDot + (y & 1), y >> 1) && wait(kSums + (y & 1), y >> 1))) return false;
+            if (!(wait(kPart + (y & 1), y >> 1) && wait(kSums + (y & 1), y >> 1))) return false;
             // sums of dL/dG from each row to the chunk's end: two rows per lane
             const float(*part)[kC] = sm.part[y & 1];
             const float* xv = sm.xv[y & 1];
@@ -364,7 +320,8 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             // (the rows of dO behind the end are whatever lies there)
             if (t0 + t >= x.len) y0 = 0.f;
             if (t0 + t + 1 >= x.len) y1 = 0.f;
-            if (lane == 31) y1 += dot + sm.dot[y & 1];
+            if (lane == 31)
+                for (int w = 0; w < kEpiWarps; ++w) y1 += sm.dot[y & 1][w];
             float s = y0 + y1;
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) {
@@ -385,11 +342,11 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             }
             return true;
         });
-    } else if (warp >= 4 && warp < 12) {
-        const int quad = warp & 3, half = (warp - 4) >> 2, g = lane >> 2, i = lane & 3;
+    } else if (warp < kRowWarp0) {
+        const int quad = warp & 3, part = (warp - 4) >> 2, g = lane >> 2, i = lane & 3;
         const uint32_t row = static_cast<uint32_t>(32 * quad) << 16;
         constexpr int kHalves = D / 64;  // groups of 16 rows of d in this warp's 32 lanes
-        const int r0 = 32 * half;
+        const int r0 = 16 * part;  // this warp's columns
         int met = 0;
         const auto meet = [&] {  // all epilogue warps, with a bounded wait
             __syncwarp();
@@ -397,21 +354,21 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             return wait(kEpi, met++);
         };
         // sums over the value heads of a key head, between two of its items: this thread's dq and dk, a value per 256
-        float* sums = in.sums + static_cast<size_t>(blockIdx.x) * (2 * kHalves * 16 * 32 * kEpiWarps) + (tid - 128);
+        float* sums = in.sums + static_cast<size_t>(blockIdx.x) * (2 * kHalves * 8 * 32 * kEpiWarps) + (tid - 128);
         // factors of the item that begins at or behind (u, hh), into registers and from there into f[y & 1]
-        float fac[3];
+        float fac[2];
         const auto fetch = [&](int u, int hh) {
             while (u < mine && item_at(u, 0).c * kC >= item_at(u, 0).len) ++u;
             if (u >= mine) return;
             const Item x = item_at(u, hh);
             const float* from = ws[(static_cast<size_t>(x.b) * A.H + x.h) * chunks + x.c].eg;
 #pragma unroll
-            for (int z = 0; z < 3; ++z)
+            for (int z = 0; z < 2; ++z)
                 if (tid - 128 + z * 32 * kEpiWarps < kFactors * kC) fac[z] = from[tid - 128 + z * 32 * kEpiWarps];
         };
         const auto store = [&](int y) {
 #pragma unroll
-            for (int z = 0; z < 3; ++z)
+            for (int z = 0; z < 2; ++z)
                 if (tid - 128 + z * 32 * kEpiWarps < kFactors * kC) sm.f[y & 1][0][tid - 128 + z * 32 * kEpiWarps] = fac[z];
         };
         fetch(0, 0);
@@ -427,21 +384,21 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             {  // rows 0 .. 63: dP, 64 .. 127: E; this thread's row, columns r0 ..
                 const int r = 32 * quad + lane, t = r & 63;
                 const bool isE = r >= 64;
-                float v[32], z[32];
-                uint32_t w[32];
-                tmem_ld32(row + cPE + r0, v);
-                tmem_ld32(row + cPE + 64 + r0, z);
+                float v[16], z[16];
+                uint32_t w[16];
+                tmem_ld16(row + cPE + r0, v);
+                tmem_ld16(row + cPE + 64 + r0, z);
 #pragma unroll
-                for (int s = 0; s < 32; ++s) v[s] += z[s];
+                for (int s = 0; s < 16; ++s) v[s] += z[s];
                 if (quad >= 2) {
-                    tmem_ld32(row + cB + r0, z);
+                    tmem_ld16(row + cB + r0, z);
 #pragma unroll
-                    for (int s = 0; s < 32; ++s) v[s] += z[s];
+                    for (int s = 0; s < 16; ++s) v[s] += z[s];
                 }
                 const float gt = G[t], gtl = Gl[t], m = isE ? neg_beta[t] : 1.f;
                 const int last = t0 + t < x.len ? (isE ? t - 1 : t) : -1;  // columns 0 .. last are below the diagonal
 #pragma unroll
-                for (int s = 0; s < 32; s += 4) {
+                for (int s = 0; s < 16; s += 4) {
                     const float4 gs = *reinterpret_cast<const float4*>(G + r0 + s);
                     const float4 gl = *reinterpret_cast<const float4*>(Gl + r0 + s);
                     const float e4[4] = {(gt - gs.x) + (gtl - gl.x), (gt - gs.y) + (gtl - gl.y), (gt - gs.z) + (gtl - gl.z),
@@ -453,34 +410,73 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                         v[s + y4] = r0 + s + y4 <= last ? on : 0.f;
                     }
                 }
-                walk::split32(v, w);
 #pragma unroll
-                for (int p = 0; p < 8; ++p)
-                    st_shared_v4(smem_addr(sm.pe[p >> 2][isE]) + piece<128>(t, 4 * half + (p & 3)), w[4 * p], w[4 * p + 1],
+                for (int y2 = 0; y2 < 8; ++y2) split_pack2v(make_float2(v[2 * y2], v[2 * y2 + 1]), w[y2], w[8 + y2]);
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    st_shared_v4(smem_addr(sm.pe[p >> 1][isE]) + piece<128>(t, 2 * part + (p & 1)), w[4 * p], w[4 * p + 1],
                                  w[4 * p + 2], w[4 * p + 3]);
             }
             tc_fence_before();
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) arrive(bar(kPEFull));
+            // <dS1, S1> out of L2 while the last products run: a share of the 16-byte pieces per thread
+            float dot;
+            {
+                const size_t seq = static_cast<size_t>(x.b) * A.H + x.h, page = static_cast<size_t>(D) * E;
+                const uint4* s1 = reinterpret_cast<const uint4*>(in.S0 + (seq * (chunks + 1) + x.c + 1) * 2 * page);
+                const uint4* d1 = reinterpret_cast<const uint4*>(in.dS1 + (seq * chunks + x.c) * 2 * page);
+                constexpr int kPieces = D * E / 8, kStep = 32 * kEpiWarps;  // of one part
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int z0 = 0; z0 < kPieces; z0 += 2 * kStep) {
+                    uint4 v[2][4];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        if (z0 + r * kStep < kPieces) {
+                            const int z = z0 + r * kStep + tid - 128;
+                            v[r][0] = s1[z];
+                            v[r][1] = s1[z + kPieces];
+                            v[r][2] = d1[z];
+                            v[r][3] = d1[z + kPieces];
+                        }
+                    const auto take = [&](uint32_t sh, uint32_t sl, uint32_t dh, uint32_t dl) {
+                        const float2 s2 = make_float2(low_of(sh) + low_of(sl), high_of(sh) + high_of(sl));
+                        const float2 d2 = make_float2(low_of(dh) + low_of(dl), high_of(dh) + high_of(dl));
+                        sum = fma2(s2, d2, sum);
+                    };
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        if (z0 + r * kStep < kPieces) {
+                            take(v[r][0].x, v[r][1].x, v[r][2].x, v[r][3].x);
+                            take(v[r][0].y, v[r][1].y, v[r][2].y, v[r][3].y);
+                            take(v[r][0].z, v[r][1].z, v[r][2].z, v[r][3].z);
+                            take(v[r][0].w, v[r][1].w, v[r][2].w, v[r][3].w);
+                        }
+                }
+                dot = sum.x + sum.y;
+#pragma unroll
+                for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+            }
             if (!(wait(kDone, y) && wait(kKQ, y) && (y < 2 || wait(kSumsFree + (y & 1), (y >> 1) - 1)))) return false;
             tc_fence_after();
             // dq and dk of this item: rows 16 hb + g (+ 8) of d in this quadrant, columns 8 j + 2 i (+ 1) of this half
             // (D = 64: M = 64 puts 16 rows into each quadrant)
             // of += (factor of the column) accumulator, column block `col`
-            const auto add = [&](uint32_t col, float (&of)[kHalves * 16], const float* f2) {
+            const auto add = [&](uint32_t col, float (&of)[kHalves * 8], const float* f2) {
 #pragma unroll
                 for (int hb = 0; hb < kHalves; ++hb) {
-                    float a[16];
+                    float a[8];
                     tmem_frag(row + col + r0 + (static_cast<uint32_t>(16 * hb) << 16), a);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < 2; ++j) {
                         float2 m = make_float2(1.f, 1.f);
                         if (f2) m = *reinterpret_cast<const float2*>(f2 + r0 + 8 * j + 2 * i);
 #pragma unroll
                         for (int z = 4 * j; z < 4 * j + 4; z += 2) {
-                            of[16 * hb + z] = fmaf(a[z], m.x, of[16 * hb + z]);
-                            of[16 * hb + z + 1] = fmaf(a[z + 1], m.y, of[16 * hb + z + 1]);
+                            of[8 * hb + z] = fmaf(a[z], m.x, of[8 * hb + z]);
+                            of[8 * hb + z + 1] = fmaf(a[z + 1], m.y, of[8 * hb + z + 1]);
                         }
                     }
                 }
@@ -489,36 +485,33 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             const size_t step = A.bthd ? static_cast<size_t>(A.Hk) * D : D;
             const int d_at = (D / 4) * quad, left = x.len - t0;
             const size_t out_at = row_at(A, x.b, x.hk, A.Hk, t0, D) + d_at;
-            float nq[kHalves * 16] = {}, nk[kHalves * 16] = {};  // dq and dk of this item
+            float nq[kHalves * 8] = {}, nk[kHalves * 8] = {};  // dq and dk of this item
             // dq (o = 0) or dk (o = 1) added to the heads before, and kept or written out
-            const auto finish = [&](float (&now)[kHalves * 16], int o, void* out) {
-                float* sum = sums + o * (kHalves * 16 * 32 * kEpiWarps);
+            const auto finish = [&](float (&now)[kHalves * 8], int o, void* out) {
+                float* sum = sums + o * (kHalves * 8 * 32 * kEpiWarps);
                 if (!first)
 #pragma unroll
-                    for (int z = 0; z < kHalves * 16; ++z) now[z] += sum[z * 32 * kEpiWarps];
+                    for (int z = 0; z < kHalves * 8; ++z) now[z] += sum[z * 32 * kEpiWarps];
                 if (!last_head) {
 #pragma unroll
-                    for (int z = 0; z < kHalves * 16; ++z) sum[z * 32 * kEpiWarps] = now[z];
+                    for (int z = 0; z < kHalves * 8; ++z) sum[z * 32 * kEpiWarps] = now[z];
                 } else if (A.out_bf16) {
-                    // through this warp's part of the dP, E operand, which the MMAs have read: [32 rows][16 or 32 columns]
+                    // through this warp's part of the dP, E operand, which the MMAs have read: [16 rows][16 or 32 columns]
                     constexpr int kRow = 2 * (D / 4), kPc = kRow / 16;  // bytes and pieces of a row
                     unsigned char* to = sm.pe[0][0] + (2 * (warp - 4) + o) * (2 * kC * 128 / kEpiWarps);
 #pragma unroll
-                    for (int hb = 0; hb < kHalves; ++hb)
-#pragma unroll
-                        for (int jp = 0; jp < 2; ++jp) {
-                            const int m = lane >> 3, t = 8 * (2 * jp + (m >> 1)) + (lane & 7), p = 2 * hb + (m & 1);
-                            const int z = 16 * hb + 8 * jp;
-                            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(
-                                             smem_addr(to) + t * kRow + ((p ^ ((t >> 1) & (kPc - 1))) << 4)),
-                                         "r"(pack(now[z], now[z + 1])), "r"(pack(now[z + 2], now[z + 3])),
-                                         "r"(pack(now[z + 4], now[z + 5])), "r"(pack(now[z + 6], now[z + 7]))
-                                         : "memory");
-                        }
+                    for (int hb = 0; hb < kHalves; ++hb) {
+                        const int m = lane >> 3, t = 8 * (m >> 1) + (lane & 7), p = 2 * hb + (m & 1), z = 8 * hb;
+                        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(
+                                         smem_addr(to) + t * kRow + ((p ^ ((t >> 1) & (kPc - 1))) << 4)),
+                                     "r"(pack(now[z], now[z + 1])), "r"(pack(now[z + 2], now[z + 3])),
+                                     "r"(pack(now[z + 4], now[z + 5])), "r"(pack(now[z + 6], now[z + 7]))
+                                     : "memory");
+                    }
                     __syncwarp();
                     __nv_bfloat16* p = static_cast<__nv_bfloat16*>(out) + out_at;
 #pragma unroll
-                    for (int z = lane; z < 32 * kPc; z += 32) {
+                    for (int z = lane; z < 16 * kPc; z += 32) {
                         const int t = z / kPc, c = z % kPc;
                         if (r0 + t < left)
                             *reinterpret_cast<uint4*>(p + (r0 + t) * step + 8 * c) =
@@ -527,34 +520,32 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                 } else {
                     float* p = static_cast<float*>(out) + out_at;
 #pragma unroll
-                    for (int z = 0; z < kHalves * 16; ++z) {
-                        const int t = r0 + 8 * (z / 4 % 4) + 2 * i + (z & 1);
-                        if (t < left) p[t * step + g + 16 * (z >> 4) + 8 * (z >> 1 & 1)] = now[z];
+                    for (int z = 0; z < kHalves * 8; ++z) {
+                        const int t = r0 + 8 * (z / 4 % 2) + 2 * i + (z & 1);
+                        if (t < left) p[t * step + g + 16 * (z >> 3) + 8 * (z >> 1 & 1)] = now[z];
                     }
                 }
             };
             add(cC, nk, rest);
             add(cC + 64, nk, rest);
             add(cPE, nk, nullptr);
-            float s[8] = {};  // of columns 8 (j / 2) + 2 i + j % 2: this warp's rows of d of q . dq - k . col
-            const auto along = [&](const unsigned char (*rows)[kC * 128], const float (&of)[kHalves * 16], float sign) {
+            float s[4] = {};  // of columns 8 (j / 2) + 2 i + j % 2: this warp's rows of d of q . dq - k . col
+            const auto along = [&](const unsigned char (*rows)[kC * 128], const float (&of)[kHalves * 8], float sign) {
 #pragma unroll
-                for (int hb = 0; hb < kHalves; ++hb)
+                for (int hb = 0; hb < kHalves; ++hb) {
+                    // fragments of the transposed tile: rows of d, columns t, of the two tiles of this warp's columns
+                    const int d0 = d_at + 16 * hb, m = lane >> 3;
+                    uint32_t qq[4];
+                    ldsm_t(qq, smem_addr(rows[d0 >> 6]) +
+                                   piece<128>(r0 + 8 * (m >> 1) + (lane & 7), ((d0 & 63) >> 3) + (m & 1)));
 #pragma unroll
-                    for (int jp = 0; jp < 2; ++jp) {
-                        // fragments of the transposed tile: rows of d, columns t, of tiles 2 jp and 2 jp + 1
-                        const int d0 = d_at + 16 * hb, m = lane >> 3;
-                        uint32_t qq[4];
-                        ldsm_t(qq, smem_addr(rows[d0 >> 6]) +
-                                       piece<128>(r0 + 8 * (2 * jp + (m >> 1)) + (lane & 7), ((d0 & 63) >> 3) + (m & 1)));
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            const int at = 16 * hb + 4 * (2 * jp + z), j = 2 * (2 * jp + z);
-                            s[j] = fmaf(sign * low_of(qq[2 * z]), of[at], fmaf(sign * low_of(qq[2 * z + 1]), of[at + 2], s[j]));
-                            s[j + 1] = fmaf(sign * high_of(qq[2 * z]), of[at + 1],
-                                            fmaf(sign * high_of(qq[2 * z + 1]), of[at + 3], s[j + 1]));
-                        }
+                    for (int z = 0; z < 2; ++z) {
+                        const int at = 8 * hb + 4 * z, j = 2 * z;
+                        s[j] = fmaf(sign * low_of(qq[2 * z]), of[at], fmaf(sign * low_of(qq[2 * z + 1]), of[at + 2], s[j]));
+                        s[j + 1] = fmaf(sign * high_of(qq[2 * z]), of[at + 1],
+                                        fmaf(sign * high_of(qq[2 * z + 1]), of[at + 3], s[j + 1]));
                     }
+                }
             };
             along(sm.k, nk, -1.f);
             add(cA + 64, nk, neg_beta_eg);
@@ -566,18 +557,20 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             if (lane == 0) arrive(bar(kFree));  // the accumulators are read out: the next item's products may begin
             {
                 along(sm.q, nq, 1.f);
-                // 8 sums over the 8 lanes of equal i, halving what a lane holds: lane g ends with sum g
+                // 4 sums over the 8 lanes of equal i, halving what a lane holds: lanes of g / 2 = j end with sum j
 #pragma unroll
-                for (int m = 16, held = 4; m >= 4; m >>= 1, held >>= 1)
+                for (int m = 16, held = 2; m >= 8; m >>= 1, held >>= 1)
 #pragma unroll
-                    for (int z = 0; z < 4; ++z)
+                    for (int z = 0; z < 2; ++z)
                         if (z < held) {
                             const bool up = lane & m;
                             const float give = up ? s[z] : s[held + z], keep = up ? s[held + z] : s[z];
                             s[z] = keep + __shfl_xor_sync(0xffffffffu, give, m);
                         }
-                sm.part[y & 1][quad][r0 + 8 * (g >> 1) + 2 * i + (g & 1)] = s[0];
+                s[0] += __shfl_xor_sync(0xffffffffu, s[0], 4);
+                if (!(g & 1)) sm.part[y & 1][quad][r0 + 8 * (g >> 2) + 2 * i + (g >> 1 & 1)] = s[0];
             }
+            if (lane == 0) sm.dot[y & 1][warp - 4] = dot;
             __syncwarp();
             if (lane == 0) {
                 arrive(bar(kPart + (y & 1)));
@@ -589,7 +582,7 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             // what was staged in the place of dP and E is read out, and the next item's factors are there
             return meet();
         });
-    } else if (warp >= 12) {
+    } else {
         const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(A.v);
         each([&](const Item& x, int y) {
             // E / 4 lanes hold a row, four columns each: a slot is one row (E = 128) or two (E = 64)
@@ -599,15 +592,15 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             const ChunkWs& cw = ws[seq * chunks + x.c];
             const size_t step = A.bthd ? static_cast<size_t>(A.H) * E : E;
 #pragma unroll 1
-            for (int z = 0; z < 2 / kPer; ++z) {  // 8 slots at a time, all loads first
-                const int row0 = 16 * (warp - 12) + 8 * z + lane / kLanes;  // of slot 0; slot r: kPer r further
+            for (int z = 0; z < 4 / kPer; ++z) {  // 4 slots at a time, all loads first
+                const int row0 = 16 * (warp - kRowWarp0) + 4 * kPer * z + lane / kLanes;  // of slot 0; slot r: kPer r further
                 const int left = x.len - t0 - row0;
                 const size_t io = row_at(A, x.b, x.h, A.H, t0 + row0, E) + col;
-                float4 w[8], xx[8];
-                uint2 vv[8];
-                float bt[8];
+                float4 w[4], xx[4];
+                uint2 vv[4];
+                float bt[4];
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
+                for (int r = 0; r < 4; ++r) {
                     w[r] = xx[r] = make_float4(0.f, 0.f, 0.f, 0.f);
                     vv[r] = make_uint2(0, 0);
                     bt[r] = 0.f;
@@ -622,9 +615,9 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                 // the MMAs have read the operands of the item before, warp 3 the row sums of the one before that
                 if (z == 0 && y > 0 && !wait(kXUFree, y - 1)) return false;
                 if (z == 0 && y > 1 && !wait(kSumsFree + (y & 1), (y >> 1) - 1)) return false;
-                float sum[16];  // of each slot: x . w, beta x . (w - v)
+                float sum[8];  // of each slot: x . w, beta x . (w - v)
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
+                for (int r = 0; r < 4; ++r) {
                     const uint32_t at = piece<128>(row0 + kPer * r, (col & 63) >> 3) + 2 * (col & 7);
                     uint32_t h0, h1, l0, l1;
                     split(bt[r] * w[r].x, bt[r] * w[r].y, h0, l0);
@@ -639,30 +632,31 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                     sum[2 * r + 1] = bt[r] * fmaf(xx[r].x, w[r].x - low_of(vv[r].x), fmaf(xx[r].y, w[r].y - high_of(vv[r].x),
                                                   fmaf(xx[r].z, w[r].z - low_of(vv[r].y), xx[r].w * (w[r].w - high_of(vv[r].y)))));
                 }
-                // 16 sums over the lanes of a row, halving what a lane holds with each exchange
+                // 8 sums over the lanes of a row, halving what a lane holds with each exchange
 #pragma unroll
-                for (int m = kLanes / 2, held = 8; held > 0; m >>= 1, held >>= 1)
+                for (int m = kLanes / 2, held = 4; held > 0; m >>= 1, held >>= 1)
 #pragma unroll
-                    for (int y2 = 0; y2 < 8; ++y2)
+                    for (int y2 = 0; y2 < 4; ++y2)
                         if (y2 < held) {
                             const bool up = lane & m;
                             const float give = up ? sum[y2] : sum[held + y2], keep = up ? sum[held + y2] : sum[y2];
                             sum[y2] = keep + __shfl_xor_sync(0xffffffffu, give, m);
                         }
-                if (E == 128) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
-                const int mine_ = lane % kLanes / (E == 128 ? 2 : 1);  // which sum this lane ended with
-                if (E == 64 || (lane & 1) == 0) (mine_ & 1 ? sm.xv : sm.dbeta)[y & 1][row0 + kPer * (mine_ >> 1)] = sum[0];
+#pragma unroll
+                for (int m = kLanes / 16; m; m >>= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], m);
+                const int mine_ = lane % kLanes / (kLanes / 8);  // which sum this lane ended with
+                if (lane % (kLanes / 8) == 0) (mine_ & 1 ? sm.xv : sm.dbeta)[y & 1][row0 + kPer * (mine_ >> 1)] = sum[0];
                 if (A.out_bf16) {
                     __nv_bfloat16* p = static_cast<__nv_bfloat16*>(A.dv) + io;
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
+                    for (int r = 0; r < 4; ++r)
                         if (kPer * r < left)
                             *reinterpret_cast<uint2*>(p + kPer * r * step) = make_uint2(
                                 pack(bt[r] * xx[r].x, bt[r] * xx[r].y), pack(bt[r] * xx[r].z, bt[r] * xx[r].w));
                 } else {
                     float* p = static_cast<float*>(A.dv) + io;
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
+                    for (int r = 0; r < 4; ++r)
                         if (kPer * r < left)
                             *reinterpret_cast<float4*>(p + kPer * r * step) =
                                 make_float4(bt[r] * xx[r].x, bt[r] * xx[r].y, bt[r] * xx[r].z, bt[r] * xx[r].w);
