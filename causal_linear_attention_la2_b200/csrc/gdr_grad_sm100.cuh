@@ -9,6 +9,10 @@
 //   dv = beta x,   dbeta_t = x_t . w_t
 //   dL/dG_t = q_t . dq_t + beta_t x_t . (w_t - v_t) - k_t . col_t, col the last three terms of dk,
 //   and <dS1, S1> more in the chunk's last row; dg: sums of dL/dG from a row to the chunk's end.
+//   With c_t = k_t . dS1 u_t e^{G_C - G_t}, the last term of k_t . col_t, that is
+//   <dS1, S1> = e^{G_C} <dS1, S0> + sum of c_t: the sum is made of the c_t that the rows subtract,
+//   so that they go out exactly.  (From the saved S1, whose parts are off by 2^-18 each, dg was off
+//   by up to 1e-4 of its norm where the gates close and what a chunk writes is all of S1.)
 // (k_t . col_t is x_t . u_t, so dL/dG_t = q_t . dq_t - v_t . dv_t; but computed from that, what
 // x_t is off by is not taken out again, and dg is off by 1.5e-5 instead of 6e-6 of its norm.)
 //
@@ -22,7 +26,7 @@
 //   0      loads: dO and factors, K and Q, the four state parts through a ring
 //   1      MMAs
 //   2      TMEM allocation;  3  dg, dbeta
-//   4-19   epilogues: dP and E as operands; <dS1, S1>; dq, dk, q . dq (16 columns a warp: what a
+//   4-19   epilogues: dP and E as operands; <dS1, S0>; dq, dk, q . dq (16 columns a warp: what a
 //          warp does to an item is one long dependent chain, and 8 warps of 32
 //          columns take nearly twice as long, 650 us against EPITIME on the 15B layer)
 //   20-23  w, x -> operands U, X; dv, and the sums of rows for dbeta and dg
@@ -421,11 +425,11 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) arrive(bar(kPEFull));
-            // <dS1, S1> out of L2 while the last products run: a share of the 16-byte pieces per thread
+            // <dS1, S0> out of L2 while the last products run: a share of the 16-byte pieces per thread
             float dot;
             {
                 const size_t seq = static_cast<size_t>(x.b) * A.H + x.h, page = static_cast<size_t>(D) * E;
-                const uint4* s1 = reinterpret_cast<const uint4*>(in.S0 + (seq * (chunks + 1) + x.c + 1) * 2 * page);
+                const uint4* s0 = reinterpret_cast<const uint4*>(in.S0 + (seq * (chunks + 1) + x.c) * 2 * page);
                 const uint4* d1 = reinterpret_cast<const uint4*>(in.dS1 + (seq * chunks + x.c) * 2 * page);
                 constexpr int kPieces = D * E / 8, kStep = 32 * kEpiWarps;  // of one part
                 float2 sum = make_float2(0.f, 0.f);
@@ -436,8 +440,8 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                     for (int r = 0; r < 2; ++r)
                         if (z0 + r * kStep < kPieces) {
                             const int z = z0 + r * kStep + tid - 128;
-                            v[r][0] = s1[z];
-                            v[r][1] = s1[z + kPieces];
+                            v[r][0] = s0[z];
+                            v[r][1] = s0[z + kPieces];
                             v[r][2] = d1[z];
                             v[r][3] = d1[z + kPieces];
                         }
@@ -455,9 +459,7 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                             take(v[r][0].w, v[r][1].w, v[r][2].w, v[r][3].w);
                         }
                 }
-                dot = sum.x + sum.y;
-#pragma unroll
-                for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+                dot = eg[kC - 1] * (sum.x + sum.y);
             }
             if (!(wait(kDone, y) && wait(kKQ, y) && (y < 2 || wait(kSumsFree + (y & 1), (y >> 1) - 1)))) return false;
             tc_fence_after();
@@ -528,7 +530,6 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             };
             add(cC, nk, rest);
             add(cC + 64, nk, rest);
-            add(cPE, nk, nullptr);
             float s[4] = {};  // of columns 8 (j / 2) + 2 i + j % 2: this warp's rows of d of q . dq - k . col
             const auto along = [&](const unsigned char (*rows)[kC * 128], const float (&of)[kHalves * 8], float sign) {
 #pragma unroll
@@ -547,6 +548,13 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                     }
                 }
             };
+            along(sm.k, nk, 1.f);
+            dot += (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+            for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] = 0.f;
+            add(cPE, nk, nullptr);
             along(sm.k, nk, -1.f);
             add(cA + 64, nk, neg_beta_eg);
             add(cB + 64, nk, nullptr);

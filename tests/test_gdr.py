@@ -381,6 +381,26 @@ def test_extreme_gates_and_strengths(gpu, dtype, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,e", [(BF16, 64, 64), (BF16, 128, 64), (BF16, 64, 128), (BF16, 128, 128), (F32, 48, 48)])
+def test_gate_gradient_where_the_gate_closes(gpu, dtype, d, e):
+    """One row that forgets the state before it, whose product with the gradient is all that the row wrote: dg is
+    c - c = 0 with c = k . dS1 u.
+
+    Both c are sums of the same d products of k_i and (dS1 u)_i, one of them over up to 64 partial sums in another order:
+    64 roundings of at most 2^-24 (2^-24 / sqrt(3) on average) of a partial sum no larger than c as a rule add up to
+    sqrt(64) 2^-24 = 4.8e-7 of c on average over many heads.  A c from operands of two bf16 parts would be off by
+    2e-6."""
+    x = R.make(4, 1, 64, 1, d, e, dtype, 21, init=True, final=True)
+    x["g"][:] = -60.0
+    x["do"][:] = 0.0
+    y = _put(x, "bhtd", gpu)
+    got = L.la2_gdr_bwd(y["q"], y["k"], y["v"], y["g"], y["beta"], y["do"], init_state=y["init"], d_final_state=y["dfinal"])
+    u = x["beta"].double()[..., None] * x["v"].double()  # [B, H, 1, e]
+    c = torch.einsum("bhi,bhij,bhj->bh", x["k"].double().expand(4, 64, 1, d)[:, :, 0], x["dfinal"].double(), u[:, :, 0])
+    assert _rms(got[3].double().cpu()) <= 4.8e-7 * _rms(c)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_correlated_keys(gpu, dtype):
     """Keys close to one another with beta near 1: every position corrects nearly all of the ones before it.
