@@ -75,12 +75,10 @@ template <int D>
 bool set_chunk_attrs() {
     using namespace la2::gdr;
     return set(reinterpret_cast<const void*>(gdr_prep<D>), sizeof(PrepSmem<D>)) &&
-           set(reinterpret_cast<const void*>(gdr_chain<D, false>), sizeof(WalkSmem<D>)) &&
-           set(reinterpret_cast<const void*>(gdr_chain<D, true>), sizeof(WalkSmem<D>)) &&
-           set(reinterpret_cast<const void*>(gdr_chain_rev<D>), sizeof(WalkSmem<D>)) &&
+           set(reinterpret_cast<const void*>(gdr_chain<D>), sizeof(WalkSmem<D>)) &&
+           set(reinterpret_cast<const void*>(gdr_chains<D>), sizeof(WalkSmem<D>)) &&
            set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kForward>), sizeof(walk::Smem<D>)) &&
-           set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kSave>), sizeof(walk::Smem<D>)) &&
-           set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kBackward>), sizeof(walk::Smem<D>)) &&
+           set(reinterpret_cast<const void*>(walk::gdr_walks<D>), sizeof(walk::Smem<D>)) &&
            set(reinterpret_cast<const void*>(walk::gdr_join<D>), sizeof(walk::JoinSmem<D>)) &&
            set(reinterpret_cast<const void*>(walk::gdr_walk<D, walk::kTransfer>), sizeof(walk::Smem<D>)) &&
            set(reinterpret_cast<const void*>(grad::gdr_grad_tc<D, 64>), sizeof(grad::Smem<D, 64>)) &&
@@ -133,8 +131,8 @@ RecWs rec_ws(long long BH, int T, int d, int e) {
 template <typename Tin>
 la2_status rec_forward(const Args& A, cudaStream_t stream) {
     const dim3 grid(A.B * A.H, cdiv(A.e, la2::gdr::kRecCols));
-    if (A.d <= 64) la2::gdr::gdr_rec_fwd<Tin, false, 8><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, nullptr, nullptr);
-    else la2::gdr::gdr_rec_fwd<Tin, false, 16><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, nullptr, nullptr);
+    if (A.d <= 64) la2::gdr::gdr_rec_fwd<Tin, 8><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A);
+    else la2::gdr::gdr_rec_fwd<Tin, 16><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A);
     return launched();
 }
 
@@ -145,15 +143,9 @@ la2_status rec_backward(const Args& A, char* ws, cudaStream_t stream) {
     float* dS1 = reinterpret_cast<float*>(ws + w.dS1);
     float* W = reinterpret_cast<float*>(ws + w.W);
     float* X = reinterpret_cast<float*>(ws + w.X);
-    const dim3 grid(A.B * A.H, cdiv(A.e, la2::gdr::kRecCols));
-    const auto walks = [&](auto rows) {
-        constexpr int kRows = decltype(rows)::value;
-        if (A.T > 0)
-            la2::gdr::gdr_rec_fwd<Tin, true, kRows><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, S0, W);
-        la2::gdr::gdr_rec_rev<Tin, kRows><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, dS1, X);
-    };
-    if (A.d <= 64) walks(std::integral_constant<int, 8>());
-    else walks(std::integral_constant<int, 16>());
+    const dim3 grid(A.B * A.H, 2 * cdiv(A.e, la2::gdr::kRecCols));
+    if (A.d <= 64) la2::gdr::gdr_rec_walks<Tin, 8><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, S0, dS1, W, X);
+    else la2::gdr::gdr_rec_walks<Tin, 16><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, S0, dS1, W, X);
     if (A.T > 0)
         la2::gdr::gdr_grad_rec<Tin><<<static_cast<unsigned>(A.B) * A.Hk * cdiv(A.T, la2::gdr::kRecChunk),
                                       la2::gdr::kGradThreads, sizeof(la2::gdr::GradSmem), stream>>>(A, S0, dS1, W, X);
@@ -201,7 +193,7 @@ ChunkLayout chunk_ws(long long BH, int T, int d, int e, bool bwd) {
         const size_t pages = align256(seqs * chunks * 2 * d * e * 2);  // two bf16 parts
         const size_t rows = align256(seqs * T * e * sizeof(float));
         w.S0 = at;
-        w.dS1 = w.S0 + pages + align256(seqs * 2 * d * e * 2);
+        w.dS1 = w.S0 + pages;
         w.W = w.dS1 + pages;
         w.X = w.W + rows;
         w.sums = w.X + rows;
@@ -217,18 +209,33 @@ ChunkLayout chunk_ws(long long BH, int T, int d, int e, bool bwd) {
 
 // One walk along every sequence: e = 128 on tcgen05 (T = 0 has no rows to map).
 template <int D, int kMode>
-la2_status walk_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::Saved& sv,
-                   const la2::gdr::walk::Segments& sg, int chunks, cudaStream_t stream) {
+la2_status walk_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::walk::Segments& sg, int chunks,
+                   cudaStream_t stream) {
     using namespace la2::gdr;
     CUtensorMap mk, mq, mv;
     if (!row_map(&mk, A.k, A.B, A.Hk, A.T, D, A.bthd) || !row_map(&mq, A.q, A.B, A.Hk, A.T, D, A.bthd) ||
-        !row_map(&mv, kMode == walk::kBackward ? A.dout : A.v, A.B, A.H, A.T, walk::kE, A.bthd))
+        !row_map(&mv, A.v, A.B, A.H, A.T, walk::kE, A.bthd))
         return LA2_ERR_CUDA;
     int* status = la2::status_word();
     if (!status) return LA2_ERR_CUDA;
-    const int parts = kMode == walk::kTransfer ? 2 * (sg.segs - 1) - 1 : kMode == walk::kForward ? sg.segs : 1;
+    const int parts = kMode == walk::kTransfer ? 2 * (sg.segs - 1) - 1 : sg.segs;
     walk::gdr_walk<D, kMode><<<A.B * A.H * parts, walk::kThreads, sizeof(walk::Smem<D>), stream>>>(
-        A, cw, sv, sg, chunks, mk, mq, mv, status);
+        A, cw, sg, chunks, mk, mq, mv, status);
+    return LA2_OK;
+}
+
+// Both walks of a backward
+template <int D>
+la2_status walks_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::Saved& sv, int chunks, cudaStream_t stream) {
+    using namespace la2::gdr;
+    CUtensorMap mk, mq, mv, md;
+    if (!row_map(&mk, A.k, A.B, A.Hk, A.T, D, A.bthd) || !row_map(&mq, A.q, A.B, A.Hk, A.T, D, A.bthd) ||
+        !row_map(&mv, A.v, A.B, A.H, A.T, walk::kE, A.bthd) || !row_map(&md, A.dout, A.B, A.H, A.T, walk::kE, A.bthd))
+        return LA2_ERR_CUDA;
+    int* status = la2::status_word();
+    if (!status) return LA2_ERR_CUDA;
+    walk::gdr_walks<D><<<2 * A.B * A.H, walk::kThreads, sizeof(walk::Smem<D>), stream>>>(A, cw, sv, chunks, mk, mq, mv, md,
+                                                                                       status);
     return LA2_OK;
 }
 
@@ -262,14 +269,14 @@ la2_status chunk_forward(const Args& A, char* ws, cudaStream_t stream) {
         const walk::Segments sg = {pl.segs, pl.per, reinterpret_cast<float*>(ws + chunk_ws(seqs, A.T, A.d, A.e, false).segs)};
         la2_status st = LA2_OK;
         if (pl.segs > 1) {
-            st = walk_tc<D, walk::kTransfer>(A, cw, Saved{}, sg, chunks, stream);
+            st = walk_tc<D, walk::kTransfer>(A, cw, sg, chunks, stream);
             if (st != LA2_OK) return st;
             walk::gdr_join<D><<<dim3(A.B * A.H, walk::kE / 32), walk::kJoinThreads, sizeof(walk::JoinSmem<D>), stream>>>(A, sg);
         }
-        st = walk_tc<D, walk::kForward>(A, cw, Saved{}, sg, chunks, stream);
+        st = walk_tc<D, walk::kForward>(A, cw, sg, chunks, stream);
         return st == LA2_OK ? launched() : st;
     }
-    gdr_chain<D, false><<<A.B * A.H * (A.e / kWalkCols), kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, Saved{}, chunks);
+    gdr_chain<D><<<A.B * A.H * (A.e / kWalkCols), kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, chunks);
     return launched();
 }
 
@@ -285,25 +292,17 @@ la2_status chunk_backward(const Args& A, char* ws, cudaStream_t stream) {
     sv.W = reinterpret_cast<float*>(ws + w.W);
     sv.X = reinterpret_cast<float*>(ws + w.X);
     sv.sums = reinterpret_cast<float*>(ws + w.sums);
-    const int walks = A.B * A.H * (A.e / kWalkCols);
-    if (chunks > 0) {
+    if (chunks > 0)
         gdr_prep<D><<<static_cast<unsigned>(A.B) * A.H * chunks, kPrepThreads, sizeof(PrepSmem<D>), stream>>>(A, cw, chunks);
-        if (!on_tc(A)) gdr_chain<D, true><<<walks, kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, sv, chunks);
-    }
+    la2_status st = LA2_OK;
     if (on_tc(A)) {
-        const walk::Segments whole = {1, chunks, nullptr};
-        la2_status st = walk_tc<D, walk::kSave>(A, cw, sv, whole, chunks, stream);
-        if (st == LA2_OK) st = walk_tc<D, walk::kBackward>(A, cw, sv, whole, chunks, stream);
+        st = walks_tc<D>(A, cw, sv, chunks, stream);
         if (st == LA2_OK) st = grad_tc<D, 128>(A, cw, sv, chunks, stream);
-        return st == LA2_OK ? launched() : st;
     } else {
-        gdr_chain_rev<D><<<walks, kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, sv, chunks);
+        gdr_chains<D><<<2 * A.B * A.H * (A.e / kWalkCols), kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, sv, chunks);
+        if (chunks > 0) st = grad_tc<D, 64>(A, cw, sv, chunks, stream);
     }
-    if (chunks > 0) {
-        const la2_status st = grad_tc<D, 64>(A, cw, sv, chunks, stream);
-        if (st != LA2_OK) return st;
-    }
-    return launched();
+    return st == LA2_OK ? launched() : st;
 }
 
 // Sizes and enums of a sequence call; *empty: nothing to do (no batch entry or
@@ -317,8 +316,8 @@ la2_status size_checks(int B, int Hk, int H, int T, int d, int e, la2_dtype dtyp
     if (H > 0 && (Hk == 0 || H % Hk != 0)) return LA2_ERR_INVALID_ARG;
     if (d > la2::gdr::kMaxDim || e > la2::gdr::kMaxDim) return LA2_ERR_UNSUPPORTED;
     if (dtype == LA2_DTYPE_F32 && out_dtype == LA2_DTYPE_BF16) return LA2_ERR_UNSUPPORTED;
-    // one CTA per (sequence, chunk) at most, in one grid dimension
-    if (B > 0 && H > 0 && static_cast<long long>(B) * H > (INT_MAX - 1) / (static_cast<long long>(T) / 32 + 1))
+    // one CTA per (sequence, chunk), or four per sequence, at most, in one grid dimension
+    if (B > 0 && H > 0 && static_cast<long long>(B) * H > (INT_MAX - 1) / (static_cast<long long>(T) / 32 + 4))
         return LA2_ERR_UNSUPPORTED;
     *empty = B == 0 || H == 0;
     return LA2_OK;

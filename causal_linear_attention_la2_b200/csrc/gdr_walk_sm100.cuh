@@ -150,10 +150,11 @@ __device__ __forceinline__ uint32_t tile_bits(uint32_t tile, int r, int c) {
 }
 __device__ __forceinline__ float tile_at(uint32_t tile, int r, int c) { return __uint_as_float(tile_bits(tile, r, c) << 16); }
 
+// The walk of CTA `block` of seqs x parts
 template <int D, int kMode>
-__global__ void __launch_bounds__(kThreads, 1)
-gdr_walk(Args A, const ChunkWs* ws, Saved out, Segments sg, int chunks, const __grid_constant__ CUtensorMap mk,
-         const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mv, int* status) {
+__device__ __forceinline__ void walk_along(const Args& A, const ChunkWs* ws, const Saved& out, const Segments& sg, int chunks,
+                                           const CUtensorMap& mk, const CUtensorMap& mq, const CUtensorMap& mv, int* status,
+                                           int block) {
     extern __shared__ __align__(1024) unsigned char walk_tc_raw[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(walk_tc_raw);
     constexpr bool kRev = kMode == kBackward;
@@ -161,7 +162,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, Segments sg, int chunks, const __
     // TMEM columns
     constexpr uint32_t cS = 0, cB = D, cA = 2 * D, cD2 = cA + 64, cW = cD2 + 64, cD4 = cW + 64;
     // kForward: segment by segment; kTransfer: B of the first one, B and M of the others
-    const int seqs = A.B * A.H, n = blockIdx.x % seqs, part = blockIdx.x / seqs;
+    const int seqs = A.B * A.H, n = block % seqs, part = block / seqs;
     const int seg = kMode == kTransfer ? (part + 1) >> 1 : kMode == kForward ? part : 0;
     const bool unit = kMode == kTransfer && part > 0 && !(part & 1);  // from the identity, with v = 0
     const int b = n / A.H, h = n % A.H, hk = h / (A.H / A.Hk);
@@ -444,7 +445,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, Segments sg, int chunks, const __
         // neighbouring lanes'.  `at`: forward, the chunk that the state enters; backward, the one whose dS1 it is.
         const auto keep = [&](const uint32_t (&w)[32], int q, int at) {
             __nv_bfloat16* to = (kRev ? out.dS1 + (static_cast<size_t>(n) * chunks + at) * 2 * page
-                                      : out.S0 + (static_cast<size_t>(n) * (chunks + 1) + at) * 2 * page) + e * 8;
+                                      : out.S0 + (static_cast<size_t>(n) * chunks + at) * 2 * page) + e * 8;
 #pragma unroll
             for (int x = 0; x < 32; x += 4)
                 *reinterpret_cast<uint4*>(to + (x >> 4) * page + (4 * q + (x & 15) / 4) * (kE * 8)) =
@@ -552,7 +553,7 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, Segments sg, int chunks, const __
             if (lane == 0) arrive(bar(kEmpty + s));  // this stage's rows and factors are read out
             if (!(ok = wait(kS, it))) break;
             tc_fence_after();
-            if (it + 1 < nc || kMode == kSave) {
+            if (it + 1 < nc) {
 #pragma unroll 1
                 for (int y = 0; y < kGroups; ++y) {
                     const int q = half * kGroups + y;
@@ -560,10 +561,8 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, Segments sg, int chunks, const __
                     uint32_t w[32];
                     tmem_ld32(row + cS + 32 * q, S);
                     split32(S, w);
-                    if (it + 1 < nc) {
-                        tmem_st32u(row + cB + 32 * q, w);
-                        done(kState + y);
-                    }
+                    tmem_st32u(row + cB + 32 * q, w);
+                    done(kState + y);
                     if (kMode == kSave || kRev) keep(w, q, kRev ? c - 1 : c + 1);
                 }
             } else if (last) {
@@ -699,6 +698,28 @@ gdr_walk(Args A, const ChunkWs* ws, Saved out, Segments sg, int chunks, const __
     __syncthreads();
     tc_fence_after();
     if (warp == 2) tmem_dealloc(tm, 512);
+}
+
+template <int D, int kMode>
+__global__ void __launch_bounds__(kThreads, 1)
+gdr_walk(Args A, const ChunkWs* ws, Segments sg, int chunks, const __grid_constant__ CUtensorMap mk,
+         const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mv, int* status) {
+    walk_along<D, kMode>(A, ws, Saved{}, sg, chunks, mk, mq, mv, status, blockIdx.x);
+}
+
+// Both walks of a backward: the gradient of the state needs nothing of the forward
+// walk, so they run side by side where the SMs suffice, the longer one's CTAs first.
+// 80 sequences of 96 chunks, d = 128: 647 us (12 CTAs find no SM at first), one after
+// the other 319 + 338 us.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+gdr_walks(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant__ CUtensorMap mk,
+          const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mv,
+          const __grid_constant__ CUtensorMap md, int* status) {
+    const int seqs = gridDim.x / 2, block = blockIdx.x;
+    const Segments whole = {1, chunks, nullptr};
+    if (block < seqs) walk_along<D, kBackward>(A, ws, out, whole, chunks, mk, mq, md, status, block);
+    else walk_along<D, kSave>(A, ws, out, whole, chunks, mk, mq, mv, status, block - seqs);
 }
 
 // The states that enter segments 1, 2, ..: S_{s+1} = M_s S_s + B_s in fp32, 32
