@@ -85,12 +85,18 @@ bool set_chunk_attrs() {
            set(reinterpret_cast<const void*>(grad::gdr_grad_tc<D, 128>), sizeof(grad::Smem<D, 128>));
 }
 
+template <int kTeam>
+bool set_bulk_attrs() {
+    using namespace la2::gdr;
+    return set(reinterpret_cast<const void*>(gdr_step_bulk<float, kTeam>), bulk_smem_bytes<kTeam>()) &&
+           set(reinterpret_cast<const void*>(gdr_step_bulk<__nv_bfloat16, kTeam>), bulk_smem_bytes<kTeam>());
+}
+
 bool set_smem_attrs() {
     return set_chunk_attrs<64>() && set_chunk_attrs<128>() &&
            set(reinterpret_cast<const void*>(la2::gdr::gdr_grad_rec<float>), sizeof(la2::gdr::GradSmem)) &&
            set(reinterpret_cast<const void*>(la2::gdr::gdr_grad_rec<__nv_bfloat16>), sizeof(la2::gdr::GradSmem)) &&
-           set(reinterpret_cast<const void*>(la2::gdr::gdr_step_bulk<float>), la2::gdr::bulk_smem_bytes(128, 128)) &&
-           set(reinterpret_cast<const void*>(la2::gdr::gdr_step_bulk<__nv_bfloat16>), la2::gdr::bulk_smem_bytes(128, 128)) &&
+           set_bulk_attrs<128>() && set_bulk_attrs<256>() && set_bulk_attrs<512>() &&
            set(reinterpret_cast<const void*>(la2::gdr::pool_copy<float4>), 200 << 10) &&
            set(reinterpret_cast<const void*>(la2::gdr::pool_copy<float>), 200 << 10);
 }
@@ -419,16 +425,22 @@ la2_status la2_gdr_decode(const void* q, const void* k, const void* v, const flo
     const long long blocks = static_cast<long long>(B) * H * cdiv(e, la2::gdr::kStepUnits * (vec ? 4 : 1));
     if (blocks > INT_MAX) return LA2_ERR_UNSUPPORTED;
     const unsigned grid = static_cast<unsigned>(blocks);
-    // From four states per SM on the pipelined kernel (KERNELTIMES)
-    const bool bulk = vec && n_slots > 0 && static_cast<long long>(B) * H >= 4 * kSMs && d * e >= 4096;
+    // From two states per SM on the pipelined kernel (KERNELTIMES)
+    const bool bulk = vec && n_slots > 0 && static_cast<long long>(B) * H >= 2 * kSMs;
     int* status = nullptr;
     if (bulk && (!device_setup() || !(status = la2::status_word()))) return LA2_ERR_CUDA;
     const auto go = [&](auto tag) {
         using Tin = decltype(tag);
         const Tin *qq = static_cast<const Tin*>(q), *kk = static_cast<const Tin*>(k), *vv = static_cast<const Tin*>(v);
-        if (bulk)
-            la2::gdr::gdr_step_bulk<Tin><<<kSMs, la2::gdr::kBulkThreads, la2::gdr::bulk_smem_bytes(d, e), s>>>(
-                qq, kk, vv, g, beta, states, slots, n_slots, out, B * H, Hk, H, d, e, status);
+        const auto pipelined = [&](auto team) {
+            constexpr int kTeam = decltype(team)::value;
+            la2::gdr::gdr_step_bulk<Tin, kTeam><<<kSMs, la2::gdr::kBulkThreads, la2::gdr::bulk_smem_bytes<kTeam>(), s>>>(
+                qq, kk, vv, g, beta, states, slots, n_slots, out, B * H, Hk, H, d, e, la2::gdr::bulk_stages(d, e), status);
+        };
+        const int team = bulk ? la2::gdr::bulk_team(d, e) : 0;  // (e >= 4)
+        if (team == 128) pipelined(std::integral_constant<int, 128>());
+        else if (team == 256) pipelined(std::integral_constant<int, 256>());
+        else if (team == 512) pipelined(std::integral_constant<int, 512>());
         else if (vec)
             la2::gdr::gdr_step<Tin, 4><<<grid, la2::gdr::kStepThreads, 0, s>>>(qq, kk, vv, g, beta, states, slots,
                                                                              n_slots, out, Hk, H, d, e);

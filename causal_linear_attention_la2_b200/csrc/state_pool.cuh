@@ -135,83 +135,145 @@ gdr_step(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __rest
     }
 }
 
-// The same step for many states: a CTA per SM walks over its (row, head)s with
-// three whole states in shared memory, one being loaded (bulk copy), one worked
-// on, one being stored, so that the memory system always has 64 KB to bring and
-// 64 KB to take per SM whatever the arithmetic in between waits for.  States are
-// 16-byte aligned, e a multiple of 4.  Each thread keeps its part of the state in
-// registers between the two products and the update.
+// The same step for many states: a CTA per SM whose threads form teams, as many
+// as leave each thread at most 8 16-byte pieces of a state (one of 512 threads at
+// 128 x 128, four at 64 x 64).  A team walks over its (row, head)s with three or
+// more whole states in shared memory, one being worked on, one being stored, the
+// others being loaded (bulk copies), so that the memory system always has 64 KB to
+// bring and 64 KB to take per SM whatever the arithmetic in between waits for.  What
+// a step reads besides (the slot and the rows before it that name it too, gates, k,
+// q, v) is on its way a step ahead: read in the step itself, its latency is the
+// step's.  States are 16-byte aligned, e a multiple of 4.  Each thread keeps its part
+// of the state in registers between the two products and the update.
+// 2560 states of 128 x 128: 63 us (84% of the copy rate), with what a step reads
+// besides read in the step 79 us; of 64 x 64: 25 us, with one team of 512 49 us.
 constexpr int kBulkThreads = 512;
 constexpr int kBulkRows = 8;
-constexpr int kBulkStages = 3;
+constexpr int kBulkStages = 8;  // at most; at least three
+constexpr int kBulkStates = 3 * 128 * 128;  // floats of all states of a CTA
 
-struct BulkSmem {
-    float part[2][kBulkThreads * 4];
+template <int kTeam>
+struct alignas(16) BulkSmem {  // one per team, one behind the other
+    float part[2][kTeam * 4];
     float ks[2][128], qs[2][128];
     float u[128], kq;
     unsigned long long full[kBulkStages];
 };
 
-inline size_t bulk_smem_bytes(int d, int e) {
-    return sizeof(BulkSmem) + 128 + static_cast<size_t>(kBulkStages) * d * e * sizeof(float);
+inline int bulk_team(int d, int e) {
+    for (int team = 128; team < kBulkThreads; team *= 2)
+        if (d <= kBulkRows * (team / (e / 4)) && d <= team && e <= team) return team;
+    return kBulkThreads;
 }
 
-template <typename Tin>
+inline int bulk_stages(int d, int e) {
+    const int fit = kBulkStates / (kBulkThreads / bulk_team(d, e) * d * e);
+    return fit < kBulkStages ? fit : kBulkStages;
+}
+
+template <int kTeam>
+constexpr size_t bulk_smem_bytes() {
+    return (sizeof(BulkSmem<kTeam>) * (kBulkThreads / kTeam) + 127) / 128 * 128 + kBulkStates * sizeof(float);
+}
+
+// Barriers of one team
+template <int kTeam>
+struct Team {
+    int id;  // hardware barrier
+    __device__ __forceinline__ void sync() const {
+        asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "n"(kTeam) : "memory");
+    }
+    __device__ __forceinline__ bool any(bool x) const {
+        int r;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\t"
+            "selp.s32 %0, 1, 0, q;\n\t}"
+            : "=r"(r) : "r"(static_cast<int>(x)), "r"(id), "n"(kTeam) : "memory");
+        return r != 0;
+    }
+};
+
+template <typename Tin, int kTeam>
 __global__ void __launch_bounds__(kBulkThreads, 1)
 gdr_step_bulk(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v,
               const float* __restrict__ g, const float* __restrict__ beta, float* state,
               const int* __restrict__ slots, int n_slots, float* __restrict__ out, int total, int Hk, int H, int d,
-              int e, int* status) {
+              int e, int stages, int* status) {
     extern __shared__ __align__(128) unsigned char bulk_raw[];
-    BulkSmem& sm = *reinterpret_cast<BulkSmem*>(bulk_raw);
-    float* stage = reinterpret_cast<float*>(bulk_raw + (sizeof(BulkSmem) + 127) / 128 * 128);
-    const int tid = threadIdx.x, page = d * e;
+    constexpr int kTeams = kBulkThreads / kTeam;
+    const int team = threadIdx.x / kTeam, tid = threadIdx.x % kTeam, page = d * e;
+    BulkSmem<kTeam>& sm = reinterpret_cast<BulkSmem<kTeam>*>(bulk_raw)[team];
+    float* stage = reinterpret_cast<float*>(bulk_raw + (sizeof(BulkSmem<kTeam>) * kTeams + 127) / 128 * 128) +
+                   static_cast<size_t>(team) * stages * page;
+    const Team<kTeam> all{1 + team};
     const uint32_t bytes = static_cast<uint32_t>(page) * 4, full = smem_u32(sm.full);
-    const int cu = e / 4, groups = kBulkThreads / cu, rg = tid / cu, ju = tid % cu;
+    const int cu = e / 4, groups = kTeam / cu, rg = tid / cu, ju = tid % cu;
     const bool on = rg < groups;
-    const int mine = (total - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-    const auto index = [&](int y) { return static_cast<int>(blockIdx.x) + y * static_cast<int>(gridDim.x); };
+    const int first = team * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    const int every = kTeams * static_cast<int>(gridDim.x);
+    const int mine = first < total ? (total - 1 - first) / every + 1 : 0;
+    const auto index = [&](int y) { return first + y * every; };
     const auto slot_of = [&](int y) {
         const int b = index(y) / H;
         return slots ? slots[b] : b;
     };
     const auto load = [&](int y, int slot) {  // one thread
         if (slot < 0 || slot >= n_slots) slot = 0;  // read and dropped: a pool without slots is not launched
-        const uint32_t bar = full + 8 * (y % kBulkStages);
+        const uint32_t bar = full + 8 * (y % stages);
         mbar_arrive_expect_tx(bar, bytes);
         asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                         smem_u32(stage + static_cast<size_t>(y % kBulkStages) * page)),
+                         smem_u32(stage + static_cast<size_t>(y % stages) * page)),
                      "l"(state + (static_cast<size_t>(slot) * H + index(y) % H) * page), "r"(bytes), "r"(bar)
                      : "memory");
     };
-    const auto row = [&](int y) {  // this thread's element of k or q of one state
-        if (tid >= 2 * d || y >= mine) return 0.f;
-        const int n = index(y), i = tid < d ? tid : tid - d;
-        const size_t at = (static_cast<size_t>(n / H) * Hk + n % H / (H / Hk)) * d + i;
-        return to_float(tid < d ? k[at] : q[at]);
-    };
-    const auto keep = [&](int y, float x) {
-        if (tid < d) sm.ks[y & 1][tid] = x;
-        else if (tid < 2 * d) sm.qs[y & 1][tid - d] = x;
+    const auto keep = [&](int y, Tin kk, Tin qq) {
+        if (tid < d) {
+            sm.ks[y & 1][tid] = to_float(kk);
+            sm.qs[y & 1][tid] = to_float(qq);
+        }
     };
     if (tid == 0) {
-        for (int s = 0; s < kBulkStages; ++s) mbar_init(full + 8 * s, 1);
+        for (int s = 0; s < stages; ++s) mbar_init(full + 8 * s, 1);
         fence_mbar_init();
-        for (int y = 0; y < 2 && y < mine; ++y) load(y, slot_of(y));
+        for (int y = 0; y + 1 < stages && y < mine; ++y) load(y, slot_of(y));
     }
-    keep(0, row(0));
-    __syncthreads();
-    for (int y = 0; y < mine; ++y) {
-        const int n = index(y), b = n / H, s = y % kBulkStages;
-        const float next = row(y + 1);
-        const int slot = slot_of(y), ahead = y + 2 < mine && tid == 0 ? slot_of(y + 2) : 0;
-        const float a = g ? expf(g[n]) : 1.f, bt = beta[n];
-        int twice = 0;
+    struct Step {  // what one step reads besides the state
+        int slot, other;  // other: this thread's share of the rows before (their first kTeam)
+        float g, bt;
+        Tin k, q, v;  // converted when they are used: a conversion waits for the load
+    };
+    const auto fetch = [&](int y) {
+        Step x = {-1, -1, 0.f, 0.f, Tin(0.f), Tin(0.f), Tin(0.f)};
+        if (y < mine) {
+            const int n = index(y), b = n / H;
+            x.slot = slots ? slots[b] : b;
+            if (slots && tid < b) x.other = slots[tid];
+            if (tid < d) {
+                const size_t at = (static_cast<size_t>(b) * Hk + (n - b * H) / (H / Hk)) * d + tid;
+                x.k = k[at];
+                x.q = q[at];
+            }
+            if (g) x.g = g[n];
+            x.bt = beta[n];
+            if (tid < e) x.v = v[static_cast<size_t>(n) * e + tid];
+        }
+        return x;
+    };
+    Step now = fetch(0);
+    keep(0, now.k, now.q);
+    all.sync();
+    for (int y = 0, s = 0, turn = 0; y < mine; ++y) {
+        const int n = index(y), b = n / H;
+        const Step next = fetch(y + 1);
+        const int ahead = y + stages - 1 < mine && tid == 0 ? slot_of(y + stages - 1) : 0;
+        const int slot = now.slot;
+        const float a = g ? expf(now.g) : 1.f, bt = now.bt;
+        int twice = slots && tid < b && now.other == slot;
         if (slots)
-            for (int x = tid; x < b; x += kBulkThreads) twice |= slots[x] == slot;
-        const float vv = tid < e ? to_float(v[static_cast<size_t>(n) * e + tid]) : 0.f;
-        const bool ok = mbar_wait(full + 8 * s, (y / kBulkStages) & 1);
-        if (!__syncthreads_and(ok)) {
+            for (int x = tid + kTeam; x < b; x += kTeam) twice |= slots[x] == slot;
+        const float vv = to_float(now.v);
+        const bool ok = mbar_wait(full + 8 * s, turn);
+        if (all.any(!ok)) {
             if (tid == 0) atomicCAS(status, 0, 5 | (230 << 8));
             break;
         }
@@ -239,14 +301,14 @@ gdr_step_bulk(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* _
             reinterpret_cast<float4*>(sm.part[0])[tid] = pk;
             reinterpret_cast<float4*>(sm.part[1])[tid] = pq;
         }
-        if (tid >= kBulkThreads - 32) {  // k . q
+        if (tid >= kTeam - 32) {  // k . q
             float kq = 0.f;
             for (int i = tid & 31; i < d; i += 32) kq = fmaf(ks[i], qs[i], kq);
 #pragma unroll
             for (int m = 16; m; m >>= 1) kq += __shfl_xor_sync(0xffffffffu, kq, m);
-            if (tid == kBulkThreads - 1) sm.kq = kq;
+            if (tid == kTeam - 1) sm.kq = kq;
         }
-        const bool live = !__syncthreads_or(twice) && slot >= 0 && slot < n_slots;
+        const bool live = !all.any(twice) && slot >= 0 && slot < n_slots;
         if (tid < e) {
             float sk = 0.f, sq = 0.f;
             const float kq = sm.kq;
@@ -259,8 +321,8 @@ gdr_step_bulk(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* _
             sm.u[tid] = u;
             out[static_cast<size_t>(n) * e + tid] = live ? fmaf(a, sq, kq * u) : 0.f;
         }
-        keep(y + 1, next);
-        __syncthreads();
+        keep(y + 1, next.k, next.q);
+        all.sync();
         if (live && on) {
             const float4 u = reinterpret_cast<const float4*>(sm.u)[ju];
 #pragma unroll
@@ -274,7 +336,7 @@ gdr_step_bulk(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* _
             }
         }
         fence_proxy_async_smem();
-        __syncthreads();
+        all.sync();
         if (tid == 0) {
             if (live)
                 asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
@@ -282,11 +344,16 @@ gdr_step_bulk(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* _
                              "r"(smem_u32(S)), "r"(bytes)
                              : "memory");
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            if (y + 2 < mine) {
+            if (y + stages - 1 < mine) {
                 // its stage is the one that was stored a step ago
                 asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                load(y + 2, ahead);
+                load(y + stages - 1, ahead);
             }
+        }
+        now = next;
+        if (++s == stages) {
+            s = 0;
+            turn ^= 1;
         }
     }
     if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
