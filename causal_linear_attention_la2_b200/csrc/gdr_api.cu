@@ -166,8 +166,9 @@ bool by_chunks(la2_dtype dtype, int d, int e) {
 // Segments of the forward walk (gdr_walk_sm100.cuh) for `seqs` sequences of
 // `chunks` chunks, by the chunks that the busiest SM walks: a segment's own and,
 // with segments, those of the two walks that make its entering state; a join takes
-// about a chunk's time.  16 sequences of 1024 chunks (T = 65,536): 9 segments,
-// JOINTIMES.
+// about a chunk's time.  The whole forward, d = e = 128, cut and not: 16 sequences of 1024
+// chunks (T = 65,536) 1289 and 3388 us, of 256 chunks 372 and 859 us; 40 of 128 chunks
+// 382 and 503 us; 60 of 128 and 80 of 96 are not cut (554 and 460 us).
 struct SegPlan {
     int segs, per;
 };
@@ -425,7 +426,9 @@ la2_status la2_gdr_decode(const void* q, const void* k, const void* v, const flo
     const long long blocks = static_cast<long long>(B) * H * cdiv(e, la2::gdr::kStepUnits * (vec ? 4 : 1));
     if (blocks > INT_MAX) return LA2_ERR_UNSUPPORTED;
     const unsigned grid = static_cast<unsigned>(blocks);
-    // From two states per SM on the pipelined kernel (KERNELTIMES)
+    // From two states per SM on the pipelined kernel; it and the other one, in us: states of 64 x 64: 148 of them
+    // 8.2 and 8.2, 296 10.2 and 10.2, 592 12.3 and 14.3, 2560 25 and 41; of 128 x 128: 148 12.3 and 11, 296 16.4 and
+    // 16.4, 592 22.5 and 26.6, 2560 63 and 90; of 16 x 16: 296 8.2 and 8.2, 5120 29 and 33.
     const bool bulk = vec && n_slots > 0 && static_cast<long long>(B) * H >= 2 * kSMs;
     int* status = nullptr;
     if (bulk && (!device_setup() || !(status = la2::status_word()))) return LA2_ERR_CUDA;

@@ -248,8 +248,10 @@ __device__ __forceinline__ void take(float (&acc)[4], const float (*M)[kPitchM],
 // four blocks of 16 by forward substitution in fp32 (a thread per column,
 // N_ts = Ah_ts - sum_{s < r < t} Ah_tr beta_r N_rs), then 16 -> 32 -> 64 on the
 // tensor cores.  A substitution over all 64 rows is a chain four
-// times as long with most threads idle (7680 chunks of d = 128: 355 us against
-// 257 us with the joins on the SIMT cores, bound by shared memory).
+// times as long with most threads idle (7680 chunks of d = 128: 355 us, 257 us
+// with the joins on the SIMT cores, 165 us as it is).  What is left is a row of short
+// phases with a barrier between them, four CTAs per SM in different ones: 12 us a
+// chunk, against 77 us for the bytes.
 template <int D>
 __global__ void __launch_bounds__(kPrepThreads, 4)
 gdr_prep(Args A, ChunkWs* ws, int chunks) {

@@ -16,9 +16,12 @@
 //             X = dU - N^T (beta dU);
 //             dS = e^{G_C} dS + Q^T (e^G dO) - K^T (beta e^G X).
 // e^{G_C} is multiplied in one chunk ahead, when the two parts of the state are
-// already handed to the next product.  An MMA of 64 columns takes as long as one
-// of 128 (measured: 62 cycles either way at M = 128, K = 16), so S K^T and S Q^T
-// are one product of 128 columns.
+// already handed to the next product.  S K^T and S Q^T are one product of 128 columns:
+// half as many instructions to issue, which is done inside elect.sync (about 20
+// cycles each; 78 under a test of the lane).  Each round from one product's
+// commit to the next one's issue costs some 1800 cycles, of which the MMAs are a
+// fraction: three of them bound the walk, 2.9 us a chunk (80 sequences of 96 chunks
+// of d = 128: 281 us; 28 warps instead of 16 took 338 us).
 //
 // Warps (16): 0 loads (TMA tiles, bulk copies of what gdr_prep left), 1 issues
 // the MMAs, 2 owns the TMEM allocation; 4-7 and 8-11 are the chain's epilogue,
