@@ -39,6 +39,7 @@
 #include <type_traits>
 
 #include "gdr_common.cuh"
+#include "ptx_sm100.cuh"
 
 namespace la2 {
 namespace gdr {
@@ -239,6 +240,12 @@ __device__ __forceinline__ void take(float (&acc)[4], const float (*M)[kPitchM],
     }
 }
 
+// Shared memory to global memory past the registers; what was written has been fenced
+__device__ __forceinline__ void store_bulk(void* to, const void* from, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(smem_addr(from)), "r"(bytes)
+                 : "memory");
+}
+
 // N and P of one chunk: warps 0-3 make 16 rows of K K^T each, warps 4-7 of Q K^T.
 //
 // N = (I + Ah diag(beta))^{-1} Ah by halves: with the blocks of the first and
@@ -250,7 +257,7 @@ __device__ __forceinline__ void take(float (&acc)[4], const float (*M)[kPitchM],
 // tensor cores.  A substitution over all 64 rows is a chain four
 // times as long with most threads idle (7680 chunks of d = 128: 355 us, 257 us
 // with the joins on the SIMT cores, 165 us as it is).  What is left is a row of short
-// phases with a barrier between them, four CTAs per SM in different ones: 12 us a
+// phases with a barrier between them, four CTAs per SM in different ones: 11 us a
 // chunk, against 77 us for the bytes.
 template <int D>
 __global__ void __launch_bounds__(kPrepThreads, 4)
@@ -306,6 +313,7 @@ gdr_prep(Args A, ChunkWs* ws, int chunks) {
             sm.out.rest_beta[y] = sm.out.rest[y] * bt;
             sm.out.neg_beta_eg[y] = -bt * sm.out.eg[y];
         }
+        fence_proxy_async_smem();
     }
     cp_wait<0>();
     __syncthreads();
@@ -354,7 +362,14 @@ gdr_prep(Args A, ChunkWs* ws, int chunks) {
             }
         }
     }
+    if (isq) fence_proxy_async_smem();
     __syncthreads();
+    ChunkWs& to = ws[static_cast<size_t>(n) * chunks + c];
+    const bool storer = tid == kPrepThreads - 1;
+    if (storer) {
+        store_bulk(to.img[2], sm.pimg, sizeof(sm.pimg));
+        store_bulk(to.eg, &sm.out, sizeof(sm.out));
+    }
     if (tid < kC) {  // blocks of 16: column tid
         const int r0 = tid & ~15, sl = tid & 15;
         float bN[16];
@@ -426,14 +441,12 @@ gdr_prep(Args A, ChunkWs* ws, int chunks) {
             *reinterpret_cast<uint4*>(sm.nimg[1] + piece<128>(t, p)) = make_uint4(w[4], w[5], w[6], w[7]);
         }
     }
+    fence_proxy_async_smem();
     __syncthreads();
-    ChunkWs& to = ws[static_cast<size_t>(n) * chunks + c];
-    const auto copy = [&](void* dst, const void* src, int bytes) {
-        for (int x = tid; x < bytes / 16; x += kPrepThreads) static_cast<uint4*>(dst)[x] = static_cast<const uint4*>(src)[x];
-    };
-    copy(to.img[0], sm.nimg, sizeof(sm.nimg));
-    copy(to.img[2], sm.pimg, sizeof(sm.pimg));
-    copy(to.eg, &sm.out, sizeof(sm.out));
+    if (storer) {
+        store_bulk(to.img[0], sm.nimg, sizeof(sm.nimg));
+        asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
 }
 
 // ----------------------------------------------------------------- gdr_chain
