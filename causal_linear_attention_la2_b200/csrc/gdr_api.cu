@@ -85,6 +85,13 @@ bool set_chunk_attrs() {
            set(reinterpret_cast<const void*>(grad::gdr_grad_tc<D, 128>), sizeof(grad::Smem<D, 128>));
 }
 
+template <int kCols>
+bool set_rec_attrs() {
+    using namespace la2::gdr;
+    return set(reinterpret_cast<const void*>(gdr_grad_rec<float, kCols>), sizeof(GradSmem)) &&
+           set(reinterpret_cast<const void*>(gdr_grad_rec<__nv_bfloat16, kCols>), sizeof(GradSmem));
+}
+
 template <int kTeam>
 bool set_bulk_attrs() {
     using namespace la2::gdr;
@@ -94,8 +101,7 @@ bool set_bulk_attrs() {
 
 bool set_smem_attrs() {
     return set_chunk_attrs<64>() && set_chunk_attrs<128>() &&
-           set(reinterpret_cast<const void*>(la2::gdr::gdr_grad_rec<float>), sizeof(la2::gdr::GradSmem)) &&
-           set(reinterpret_cast<const void*>(la2::gdr::gdr_grad_rec<__nv_bfloat16>), sizeof(la2::gdr::GradSmem)) &&
+           set_rec_attrs<64>() && set_rec_attrs<128>() &&
            set_bulk_attrs<128>() && set_bulk_attrs<256>() && set_bulk_attrs<512>() &&
            set(reinterpret_cast<const void*>(la2::gdr::pool_copy<float4>), 200 << 10) &&
            set(reinterpret_cast<const void*>(la2::gdr::pool_copy<float>), 200 << 10);
@@ -150,11 +156,16 @@ la2_status rec_backward(const Args& A, char* ws, cudaStream_t stream) {
     float* W = reinterpret_cast<float*>(ws + w.W);
     float* X = reinterpret_cast<float*>(ws + w.X);
     const dim3 grid(A.B * A.H, 2 * cdiv(A.e, la2::gdr::kRecCols));
-    if (A.d <= 64) la2::gdr::gdr_rec_walks<Tin, 8><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, S0, dS1, W, X);
-    else la2::gdr::gdr_rec_walks<Tin, 16><<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, S0, dS1, W, X);
-    if (A.T > 0)
-        la2::gdr::gdr_grad_rec<Tin><<<static_cast<unsigned>(A.B) * A.Hk * cdiv(A.T, la2::gdr::kRecChunk),
-                                      la2::gdr::kGradThreads, sizeof(la2::gdr::GradSmem), stream>>>(A, S0, dS1, W, X);
+    const unsigned chunks = static_cast<unsigned>(A.B) * A.Hk * cdiv(A.T, la2::gdr::kRecChunk);
+    const auto go = [&](auto rows, auto cols) {
+        la2::gdr::gdr_rec_walks<Tin, decltype(rows)::value>
+            <<<grid, la2::gdr::kRecThreads, 0, stream>>>(A, S0, dS1, W, X);
+        if (A.T > 0)
+            la2::gdr::gdr_grad_rec<Tin, decltype(cols)::value>
+                <<<chunks, la2::gdr::kGradThreads, sizeof(la2::gdr::GradSmem), stream>>>(A, S0, dS1, W, X);
+    };
+    if (A.d <= 64) go(std::integral_constant<int, 8>(), std::integral_constant<int, 64>());
+    else go(std::integral_constant<int, 16>(), std::integral_constant<int, 128>());
     return launched();
 }
 

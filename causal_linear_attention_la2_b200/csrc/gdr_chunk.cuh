@@ -256,7 +256,7 @@ __device__ __forceinline__ void store_bulk(void* to, const void* from, uint32_t 
 // N_ts = Ah_ts - sum_{s < r < t} Ah_tr beta_r N_rs), then 16 -> 32 -> 64 on the
 // tensor cores.  A substitution over all 64 rows is a chain four
 // times as long with most threads idle (7680 chunks of d = 128: 355 us, 257 us
-// with the joins on the SIMT cores, 165 us as it is).  What is left is a row of short
+// with the joins on the SIMT cores, 158 us as it is).  What is left is a row of short
 // phases with a barrier between them, four CTAs per SM in different ones: 11 us a
 // chunk, against 77 us for the bytes.
 template <int D>

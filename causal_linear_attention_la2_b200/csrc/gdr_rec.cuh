@@ -46,13 +46,16 @@ struct RecRows {
         const int tid = threadIdx.x, hk = h / (A.H / A.Hk);
         const Tin* kp = static_cast<const Tin*>(A.k);
         const Tin* qp = static_cast<const Tin*>(A.q);
+        const size_t at = row_at(A, b0, hk, A.Hk, t0, A.d) + tid, step = A.bthd ? static_cast<size_t>(A.Hk) * A.d : A.d;
+        kp += at;
+        qp += at;
+        const int rows = tid < A.d ? n : 0;
 #pragma unroll
         for (int r = 0; r < kRecStep; ++r) {
             k[r] = q[r] = Tin(0.f);
-            if (r < n && tid < A.d) {
-                const size_t at = row_at(A, b0, hk, A.Hk, t0 + r, A.d) + tid;
-                k[r] = kp[at];
-                q[r] = qp[at];
+            if (r < rows) {
+                k[r] = kp[r * step];
+                q[r] = qp[r * step];
             }
         }
 #pragma unroll
@@ -90,6 +93,21 @@ __device__ __forceinline__ float sum8(float x) {
     return x;
 }
 
+// Lane r of the eight has rows 32 (m / 4) + 4 r + m % 4, m = 0 .. kRows - 1: 16 bytes next to its neighbours'
+__device__ __forceinline__ int rec_row(int r, int m) { return 32 * (m >> 2) + 4 * r + (m & 3); }
+
+template <int kRows>
+__device__ __forceinline__ void rec_load(const float* p, int r, float (&x)[kRows]) {
+#pragma unroll
+    for (int m = 0; m < kRows; m += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(p + rec_row(r, m));
+        x[m] = y.x;
+        x[m + 1] = y.y;
+        x[m + 2] = y.z;
+        x[m + 3] = y.w;
+    }
+}
+
 // Forward.  kRecRows: rows of the state per lane, 8 (d <= 64) or 16.  kSave: no output; the state entering each chunk goes to S0
 // [B*H][chunks][d][e] and the rows w to W [B*H][T][e], for the backward.
 template <typename Tin, bool kSave, int kRecRows>
@@ -105,7 +123,7 @@ __device__ __forceinline__ void rec_fwd(const Args& A, float* S0, float* W, RecS
     float S[kRecRows];
 #pragma unroll
     for (int m = 0; m < kRecRows; ++m) {
-        const int i = r + 8 * m;
+        const int i = rec_row(r, m);
         S[m] = A.init && on && i < A.d ? A.init[n * page + static_cast<size_t>(i) * A.e + j] : 0.f;
     }
     const size_t step = A.bthd ? static_cast<size_t>(A.H) * A.e : A.e;  // from one row of v, out, dv to the next
@@ -123,23 +141,40 @@ __device__ __forceinline__ void rec_fwd(const Args& A, float* S0, float* W, RecS
             float* to = S0 + (static_cast<size_t>(n) * chunks + t0 / kRecChunk) * page + j;
 #pragma unroll
             for (int m = 0; m < kRecRows; ++m)
-                if (r + 8 * m < A.d) to[static_cast<size_t>(r + 8 * m) * A.e] = S[m];
+                if (rec_row(r, m) < A.d) to[static_cast<size_t>(rec_row(r, m)) * A.e] = S[m];
         }
+        float kn[kRecRows], qn[kRecRows];  // of the token to come
+        rec_load(sm.k[0], r, kn);
+        if (!kSave) rec_load(sm.q[0], r, qn);
+        float an = sm.a[0], bn = sm.b[0], vn = sm.v[0][lc];
+#pragma unroll 2
         for (int t = 0; t < m16; ++t) {
-            const float a = sm.a[t];
+            float kk[kRecRows], qq[kRecRows];
+#pragma unroll
+            for (int m = 0; m < kRecRows; ++m) {
+                kk[m] = kn[m];
+                qq[m] = qn[m];
+            }
+            const float a = an, bt = bn, vt = vn;
+            const int t1 = min(t + 1, kRecStep - 1);
+            rec_load(sm.k[t1], r, kn);
+            if (!kSave) rec_load(sm.q[t1], r, qn);
+            an = sm.a[t1];
+            bn = sm.b[t1];
+            vn = sm.v[t1][lc];
             float p[4] = {};
 #pragma unroll
             for (int m = 0; m < kRecRows; ++m) {
                 S[m] *= a;
-                p[m & 3] = fmaf(S[m], sm.k[t][r + 8 * m], p[m & 3]);
+                p[m & 3] = fmaf(S[m], kk[m], p[m & 3]);
             }
-            const float w = sm.v[t][lc] - sum8((p[0] + p[1]) + (p[2] + p[3]));
-            const float u = sm.b[t] * w;
+            const float w = vt - sum8((p[0] + p[1]) + (p[2] + p[3]));
+            const float u = bt * w;
             float o4[4] = {};
 #pragma unroll
             for (int m = 0; m < kRecRows; ++m) {
-                S[m] = fmaf(sm.k[t][r + 8 * m], u, S[m]);
-                if (!kSave) o4[m & 3] = fmaf(S[m], sm.q[t][r + 8 * m], o4[m & 3]);
+                S[m] = fmaf(kk[m], u, S[m]);
+                if (!kSave) o4[m & 3] = fmaf(S[m], qq[m], o4[m & 3]);
             }
             float o = (o4[0] + o4[1]) + (o4[2] + o4[3]);
             if (kSave) {
@@ -153,7 +188,7 @@ __device__ __forceinline__ void rec_fwd(const Args& A, float* S0, float* W, RecS
     if (!kSave && A.fin && on) {
 #pragma unroll
         for (int m = 0; m < kRecRows; ++m)
-            if (r + 8 * m < A.d) A.fin[n * page + static_cast<size_t>(r + 8 * m) * A.e + j] = S[m];
+            if (rec_row(r, m) < A.d) A.fin[n * page + static_cast<size_t>(rec_row(r, m)) * A.e + j] = S[m];
     }
 }
 
@@ -172,7 +207,7 @@ __device__ __forceinline__ void rec_rev(const Args& A, float* dS1, float* X, Rec
     float D[kRecRows];
 #pragma unroll
     for (int m = 0; m < kRecRows; ++m) {
-        const int i = r + 8 * m;
+        const int i = rec_row(r, m);
         D[m] = A.dfinal && on && i < A.d ? A.dfinal[n * page + static_cast<size_t>(i) * A.e + j] : 0.f;
     }
     const size_t step = A.bthd ? static_cast<size_t>(A.H) * A.e : A.e;
@@ -191,19 +226,36 @@ __device__ __forceinline__ void rec_rev(const Args& A, float* dS1, float* X, Rec
             float* to = dS1 + (static_cast<size_t>(n) * chunks + t0 / kRecChunk) * page + j;
 #pragma unroll
             for (int m = 0; m < kRecRows; ++m)
-                if (r + 8 * m < A.d) to[static_cast<size_t>(r + 8 * m) * A.e] = D[m];
+                if (rec_row(r, m) < A.d) to[static_cast<size_t>(rec_row(r, m)) * A.e] = D[m];
         }
+        float kn[kRecRows], qn[kRecRows];  // of the token to come
+        rec_load(sm.k[m16 - 1], r, kn);
+        rec_load(sm.q[m16 - 1], r, qn);
+        float an = sm.a[m16 - 1], bn = sm.b[m16 - 1], vn = sm.v[m16 - 1][lc];
+#pragma unroll 2
         for (int t = m16 - 1; t >= 0; --t) {
-            const float dout = sm.v[t][lc];
+            float kk[kRecRows], qq[kRecRows];
+#pragma unroll
+            for (int m = 0; m < kRecRows; ++m) {
+                kk[m] = kn[m];
+                qq[m] = qn[m];
+            }
+            const float a = an, bt = bn, dout = vn;
+            const int t1 = max(t - 1, 0);
+            rec_load(sm.k[t1], r, kn);
+            rec_load(sm.q[t1], r, qn);
+            an = sm.a[t1];
+            bn = sm.b[t1];
+            vn = sm.v[t1][lc];
             float p[4] = {};
 #pragma unroll
             for (int m = 0; m < kRecRows; ++m) {
-                D[m] = fmaf(sm.q[t][r + 8 * m], dout, D[m]);
-                p[m & 3] = fmaf(D[m], sm.k[t][r + 8 * m], p[m & 3]);
+                D[m] = fmaf(qq[m], dout, D[m]);
+                p[m & 3] = fmaf(D[m], kk[m], p[m & 3]);
             }
-            const float x = sum8((p[0] + p[1]) + (p[2] + p[3])), dw = sm.b[t] * x, a = sm.a[t];
+            const float x = sum8((p[0] + p[1]) + (p[2] + p[3])), dw = bt * x;
 #pragma unroll
-            for (int m = 0; m < kRecRows; ++m) D[m] = a * fmaf(-sm.k[t][r + 8 * m], dw, D[m]);
+            for (int m = 0; m < kRecRows; ++m) D[m] = a * fmaf(-kk[m], dw, D[m]);
             if (on && r == 0) {
                 X[(static_cast<size_t>(n) * A.T + t0 + t) * A.e + j] = x;
                 put(A.dv, row0 + (t0 + t) * step, dw, A.out_bf16);
@@ -213,7 +265,7 @@ __device__ __forceinline__ void rec_rev(const Args& A, float* dS1, float* X, Rec
     if (A.dinit && on) {
 #pragma unroll
         for (int m = 0; m < kRecRows; ++m)
-            if (r + 8 * m < A.d) A.dinit[n * page + static_cast<size_t>(r + 8 * m) * A.e + j] = D[m];
+            if (rec_row(r, m) < A.d) A.dinit[n * page + static_cast<size_t>(rec_row(r, m)) * A.e + j] = D[m];
     }
 }
 
@@ -228,7 +280,7 @@ gdr_rec_fwd(Args A) {
 // walk, so they run side by side, the longer one's CTAs first.  4 sequences of up to
 // 517 rows, d = e = 64, fp32: 149 us, one after the other 124 + 149 us.
 template <typename Tin, int kRecRows>
-__global__ void __launch_bounds__(kRecThreads)
+__global__ void __launch_bounds__(kRecThreads, 4)
 gdr_rec_walks(Args A, float* S0, float* dS1, float* W, float* X) {
     __shared__ RecSmem sm;
     const int half = gridDim.y / 2, cols = blockIdx.y;
@@ -249,11 +301,17 @@ gdr_rec_walks(Args A, float* S0, float* dS1, float* W, float* X) {
 //   dL/dG_t = q_t . dq_t + k_t . row_t - k_t . col_t, and <dS1, S1> more at the chunk's end,
 //   with k_t . row_t = beta_t x_t . (w_t - v_t) (the rows' definition, so no product is needed);
 //   dg = sums of dL/dG from a row to the chunk's end.
+//
+// A thread makes column i of 16 rows (8 where d <= 64).  In each product one factor is the same for
+// all lanes and is read four numbers at a time, and one differs (a row of S per
+// lane); read one by one, the loads took five times as long as the multiply-adds
+// (2048 chunks of d = e = 128: 1245 us, 670 us now, the loads of a chunk among them).
 struct GradSmem {
-    static constexpr int C = kRecChunk, P = kMaxDim + 1;
-    float q[C][P], k[C][P], dout[C][P], u[C][P], x[C][P];
-    float S[kMaxDim][P];
-    float dp[C][C + 1], E[C][C + 1];
+    static constexpr int C = kRecChunk, P = kMaxDim + 1, P4 = kMaxDim + 4, CP = C + 4;
+    float dout[C][P4], u[C][P4], x[C][P4];  // zero behind e
+    float dp[C][CP], E[C][CP];
+    float q[C][P], k[C][P];
+    float S[kMaxDim][P];                    // zero behind e
     float G[C], Gl[C], b[C], db[C], xr[C], dG[C];
     float part[8][C];
     float red[8];
@@ -261,11 +319,12 @@ struct GradSmem {
 
 constexpr int kGradThreads = 256;
 
-template <typename Tin>
-__global__ void __launch_bounds__(kGradThreads)
+// kCols: columns i of dq and dk that are worked on side by side, 64 (d <= 64) or 128
+template <typename Tin, int kCols>
+__global__ void __launch_bounds__(kGradThreads, 1)
 gdr_grad_rec(Args A, const float* S0, const float* dS1, const float* W, const float* X) {
     constexpr int C = kRecChunk;
-    extern __shared__ float gsm_raw[];
+    extern __shared__ __align__(16) float gsm_raw[];
     GradSmem& sm = *reinterpret_cast<GradSmem*>(gsm_raw);
     const int chunks = (A.T + C - 1) / C;
     const int c = blockIdx.x % chunks, hk = blockIdx.x / chunks % A.Hk;
@@ -274,12 +333,14 @@ gdr_grad_rec(Args A, const float* S0, const float* dS1, const float* W, const fl
     if (t0 >= len) return;
     const int n = min(C, len - t0), rep = A.H / A.Hk, tid = threadIdx.x;
     const int lane = tid & 31, warp = tid >> 5;
-    const int i = tid & 127, half = tid >> 7;  // column i of dq and dk, rows half, half + 2, ...
+    constexpr int kRows = C * kCols / kGradThreads, kWarps = kCols / 32;
+    const int i = tid % kCols, r0 = tid / kCols * kRows;  // column i of dq and dk, rows r0 ..
     const size_t page = static_cast<size_t>(A.d) * A.e;
     const Tin* q = static_cast<const Tin*>(A.q);
     const Tin* k = static_cast<const Tin*>(A.k);
     const Tin* v = static_cast<const Tin*>(A.v);
     const Tin* dout = static_cast<const Tin*>(A.dout);
+#pragma unroll 8
     for (int y = tid; y < C * kMaxDim; y += kGradThreads) {
         const int t = y / kMaxDim, m = y % kMaxDim;
         const bool ok = t < n && m < A.d;
@@ -287,9 +348,9 @@ gdr_grad_rec(Args A, const float* S0, const float* dS1, const float* W, const fl
         sm.q[t][m] = ok ? to_float(q[at]) : 0.f;
         sm.k[t][m] = ok ? to_float(k[at]) : 0.f;
     }
-    float accq[C / 2], acck[C / 2];
+    float accq[kRows], acck[kRows];
 #pragma unroll
-    for (int m = 0; m < C / 2; ++m) accq[m] = acck[m] = 0.f;
+    for (int m = 0; m < kRows; ++m) accq[m] = acck[m] = 0.f;
     for (int hh = 0; hh < rep; ++hh) {
         const int h = hk * rep + hh;
         const size_t seq = static_cast<size_t>(b) * A.H + h;
@@ -297,17 +358,22 @@ gdr_grad_rec(Args A, const float* S0, const float* dS1, const float* W, const fl
         const float* dS1c = dS1 + (seq * chunks + c) * page;
         __syncthreads();
         if (tid < C) {  // cumulative gates, as two floats: a difference of two large ones keeps its digits
-            double s = 0.0;
-            for (int t = 0; t <= tid; ++t)
-                s += t < n ? static_cast<double>(gate_at(A, row_at(A, b, h, A.H, t0 + t, 1))) : 0.0;
+            double s = tid < n ? static_cast<double>(gate_at(A, row_at(A, b, h, A.H, t0 + tid, 1))) : 0.0;
+#pragma unroll
+            for (int m = 1; m < C; m <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, s, m);
+                if (lane >= m) s += y;
+            }
             sm.G[tid] = static_cast<float>(s);
             sm.Gl[tid] = static_cast<float>(s - sm.G[tid]);
             sm.b[tid] = tid < n ? A.beta[row_at(A, b, h, A.H, t0 + tid, 1)] : 0.f;
         }
         __syncthreads();
         // a warp takes rows warp, warp + 8, ..: u, x, dout and the row sums
+#pragma unroll
         for (int t = warp; t < C; t += 8) {
             float db = 0.f, xr = 0.f;
+#pragma unroll
             for (int j = lane; j < kMaxDim; j += 32) {
                 float w = 0.f, x = 0.f, dd = 0.f, vv = 0.f;
                 if (t < n && j < A.e) {
@@ -333,15 +399,23 @@ gdr_grad_rec(Args A, const float* S0, const float* dS1, const float* W, const fl
                 sm.xr[t] = sm.b[t] * xr;
             }
         }
-        for (int y = tid; y < A.d * A.e; y += kGradThreads) sm.S[y / A.e][y % A.e] = S0c[y];
+#pragma unroll 4
+        for (int r = warp; r < A.d; r += 8)
+#pragma unroll
+            for (int j = lane; j < kMaxDim; j += 32) sm.S[r][j] = j < A.e ? S0c[static_cast<size_t>(r) * A.e + j] : 0.f;
         __syncthreads();
+        const auto dot4 = [](const float4& a, const float4& x, float y) {
+            return fmaf(a.x, x.x, fmaf(a.y, x.y, fmaf(a.z, x.z, fmaf(a.w, x.w, y))));
+        };
+        const auto at4 = [](const float* p) { return *reinterpret_cast<const float4*>(p); };
         for (int y = tid; y < C * C; y += kGradThreads) {
             const int t = y / C, s = y % C;
             float p = 0.f, x = 0.f;
             if (s <= t) {
-                for (int j = 0; j < A.e; ++j) {
-                    p = fmaf(sm.dout[t][j], sm.u[s][j], p);
-                    x = fmaf(sm.x[t][j], sm.u[s][j], x);
+                for (int j = 0; j < A.e; j += 4) {
+                    const float4 us = at4(&sm.u[s][j]);
+                    p = dot4(at4(&sm.dout[t][j]), us, p);
+                    x = dot4(at4(&sm.x[t][j]), us, x);
                 }
                 const float M = expf((sm.G[t] - sm.G[s]) + (sm.Gl[t] - sm.Gl[s]));
                 p *= M;
@@ -351,59 +425,76 @@ gdr_grad_rec(Args A, const float* S0, const float* dS1, const float* W, const fl
             sm.E[t][s] = x;
         }
         __syncthreads();
-        float fq[C / 2], row[C / 2], col[C / 2], colS[C / 2];
+        float fq[kRows], row[kRows], col[kRows], colS[kRows];
 #pragma unroll
-        for (int m = 0; m < C / 2; ++m) fq[m] = row[m] = col[m] = colS[m] = 0.f;
+        for (int m = 0; m < kRows; ++m) fq[m] = row[m] = col[m] = colS[m] = 0.f;
         if (i < A.d) {
-            for (int j = 0; j < A.e; ++j) {
-                const float s = sm.S[i][j];
+            for (int j = 0; j < A.e; j += 4) {
+                const float4 s = make_float4(sm.S[i][j], sm.S[i][j + 1], sm.S[i][j + 2], sm.S[i][j + 3]);
 #pragma unroll
-                for (int m = 0; m < C / 2; ++m) {
-                    fq[m] = fmaf(sm.dout[half + 2 * m][j], s, fq[m]);
-                    row[m] = fmaf(sm.x[half + 2 * m][j], s, row[m]);
+                for (int m = 0; m < kRows; ++m) {
+                    fq[m] = dot4(at4(&sm.dout[r0 + m][j]), s, fq[m]);
+                    row[m] = dot4(at4(&sm.x[r0 + m][j]), s, row[m]);
                 }
             }
 #pragma unroll
-            for (int m = 0; m < C / 2; ++m) {
-                const int t = half + 2 * m;
+            for (int m = 0; m < kRows; ++m) {
+                const int t = r0 + m;
                 const float eg = expf(sm.G[t]) * (1.f + sm.Gl[t]);
                 fq[m] *= eg;
                 row[m] *= -sm.b[t] * eg;
             }
-            for (int s = 0; s < C; ++s) {
-                const float ks = sm.k[s][i], qs = sm.q[s][i];
+#pragma unroll 1
+            for (int s = 0; s < C; s += 4) {
+                const float4 ks = make_float4(sm.k[s][i], sm.k[s + 1][i], sm.k[s + 2][i], sm.k[s + 3][i]);
+                const float4 qs = make_float4(sm.q[s][i], sm.q[s + 1][i], sm.q[s + 2][i], sm.q[s + 3][i]);
 #pragma unroll
-                for (int m = 0; m < C / 2; ++m) {
-                    const int t = half + 2 * m;
-                    fq[m] = fmaf(sm.dp[t][s], ks, fq[m]);
-                    row[m] = fmaf(sm.E[t][s], ks, row[m]);
-                    col[m] = fmaf(sm.E[s][t], ks, fmaf(sm.dp[s][t], qs, col[m]));
+                for (int m = 0; m < kRows; ++m) {
+                    fq[m] = dot4(at4(&sm.dp[r0 + m][s]), ks, fq[m]);
+                    row[m] = dot4(at4(&sm.E[r0 + m][s]), ks, row[m]);
                 }
+                const auto across = [&](int y, float kk, float qq) {  // row s + y of E and dP, columns r0 ..
+#pragma unroll
+                    for (int m = 0; m < kRows; m += 4) {
+                        const float4 ee = at4(&sm.E[s + y][r0 + m]), pp = at4(&sm.dp[s + y][r0 + m]);
+                        col[m] = fmaf(ee.x, kk, fmaf(pp.x, qq, col[m]));
+                        col[m + 1] = fmaf(ee.y, kk, fmaf(pp.y, qq, col[m + 1]));
+                        col[m + 2] = fmaf(ee.z, kk, fmaf(pp.z, qq, col[m + 2]));
+                        col[m + 3] = fmaf(ee.w, kk, fmaf(pp.w, qq, col[m + 3]));
+                    }
+                };
+                across(0, ks.x, qs.x);
+                across(1, ks.y, qs.y);
+                across(2, ks.z, qs.z);
+                across(3, ks.w, qs.w);
             }
         }
         __syncthreads();
         // <dS1, S0> while the states change places
         float dot = 0.f;
-        for (int y = tid; y < A.d * A.e; y += kGradThreads) {
-            const float ds = dS1c[y];
-            dot = fmaf(ds, sm.S[y / A.e][y % A.e], dot);
-            sm.S[y / A.e][y % A.e] = ds;
-        }
+#pragma unroll 4
+        for (int r = warp; r < A.d; r += 8)
+#pragma unroll
+            for (int j = lane; j < kMaxDim; j += 32) {
+                const float ds = j < A.e ? dS1c[static_cast<size_t>(r) * A.e + j] : 0.f;
+                dot = fmaf(ds, sm.S[r][j], dot);
+                sm.S[r][j] = ds;
+            }
         for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
         if (lane == 0) sm.red[warp] = dot;
         __syncthreads();
         if (i < A.d) {
-            for (int j = 0; j < A.e; ++j) {
-                const float s = sm.S[i][j];
+            for (int j = 0; j < A.e; j += 4) {
+                const float4 s = make_float4(sm.S[i][j], sm.S[i][j + 1], sm.S[i][j + 2], sm.S[i][j + 3]);
 #pragma unroll
-                for (int m = 0; m < C / 2; ++m) colS[m] = fmaf(sm.u[half + 2 * m][j], s, colS[m]);
+                for (int m = 0; m < kRows; ++m) colS[m] = dot4(at4(&sm.u[r0 + m][j]), s, colS[m]);
             }
         }
-        // row sums over i (128 threads of this half: 4 warps), then <dS1, S1>
+        // row sums over i (kWarps warps have the same rows), then <dS1, S1>
         float gc = 0.f;
 #pragma unroll
-        for (int m = 0; m < C / 2; ++m) {
-            const int t = half + 2 * m;
+        for (int m = 0; m < kRows; ++m) {
+            const int t = r0 + m;
             const float ki = i < A.d ? sm.k[t][i] : 0.f, qi = i < A.d ? sm.q[t][i] : 0.f;
             colS[m] *= expf((sm.G[C - 1] - sm.G[t]) + (sm.Gl[C - 1] - sm.Gl[t]));
             col[m] += colS[m];
@@ -419,9 +510,9 @@ gdr_grad_rec(Args A, const float* S0, const float* dS1, const float* W, const fl
         if (lane == 0) sm.red[warp] = fmaf(expf(sm.G[C - 1]) * (1.f + sm.Gl[C - 1]), sm.red[warp], gc);
         __syncthreads();
         if (tid < C) {
-            const int w0 = (tid & 1) * 4;
-            float s = sm.part[w0][tid] + sm.part[w0 + 1][tid] + sm.part[w0 + 2][tid] + sm.part[w0 + 3][tid];
-            s += sm.xr[tid];
+            float s = sm.xr[tid];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) s += sm.part[tid / kRows * kWarps + w][tid];
             if (tid == C - 1)
                 for (int w = 0; w < 8; ++w) s += sm.red[w];
             sm.dG[tid] = s;
@@ -432,15 +523,16 @@ gdr_grad_rec(Args A, const float* S0, const float* dS1, const float* W, const fl
             A.dbeta[at] = sm.db[tid];
             if (A.dg) {
                 float s = 0.f;
-                for (int t = C - 1; t >= tid; --t) s += sm.dG[t];
+#pragma unroll
+                for (int t = C - 1; t >= 0; --t) s += t >= tid ? sm.dG[t] : 0.f;
                 A.dg[at] = s;
             }
         }
     }
     if (i < A.d) {
 #pragma unroll
-        for (int m = 0; m < C / 2; ++m) {
-            const int t = half + 2 * m;
+        for (int m = 0; m < kRows; ++m) {
+            const int t = r0 + m;
             if (t < n) {
                 const size_t at = row_at(A, b, hk, A.Hk, t0 + t, A.d) + i;
                 put(A.dq, at, accq[m], A.out_bf16);
