@@ -506,7 +506,9 @@ def test_decode_step(gpu, dtype, d, e, Hk, H, gate):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("B,Hk,H,d,e,dtype", [(40, 20, 20, 128, 128, BF16), (75, 4, 8, 64, 64, F32), (43, 7, 14, 100, 44, BF16),
-                                              (150, 4, 4, 128, 36, F32)])
+                                              (150, 4, 4, 128, 36, F32), (300, 1, 2, 34, 120, BF16), (150, 2, 2, 64, 128, F32),
+                                              (700, 1, 1, 128, 32, BF16), (1400, 1, 1, 16, 4, F32), (101, 3, 3, 1, 128, F32),
+                                              (99, 3, 3, 128, 12, F32), (74, 4, 4, 33, 124, F32)])
 def test_decode_of_many_states(gpu, B, Hk, H, d, e, dtype):
     """More states than the GPU holds at a time, padded and repeated slots among them."""
     N = B + 3
@@ -514,8 +516,8 @@ def test_decode_of_many_states(gpu, B, Hk, H, d, e, dtype):
     one = {n: x[n][:, :, 0].contiguous() for n in ("q", "k", "v", "g", "beta")}
     pool = torch.randn(N, H, d, e, generator=torch.Generator().manual_seed(1))
     slots = torch.randperm(N, generator=torch.Generator().manual_seed(2))[:B].to(torch.int32)
-    slots[3], slots[B // 2], slots[B - 1] = -1, slots[1], N
-    dead = [3, B // 2, B - 1]
+    slots[3], slots[B // 2], slots[B - 1], slots[B - 2] = -1, slots[1], N, slots[B - 4]
+    dead = [3, B // 2, B - 1, B - 2]
     live = [i for i in range(B) if i not in dead]
     dp, dev = pool.to(gpu), {n: t.to(gpu) for n, t in one.items()}
     o = L.la2_gdr_decode(dev["q"], dev["k"], dev["v"], dev["g"], dev["beta"], dp, slots=slots.to(gpu))
