@@ -7,14 +7,14 @@
 //   dq^T = S0 dO^T diag(e^G) + K^T dP^T
 //   dk^T = -S0 X^T diag(beta e^G) + K^T E^T + K^T E + Q^T dP + dS1 U^T diag(e^{G_C - G})
 //   dv = beta x,   dbeta_t = x_t . w_t
-//   dL/dG_t = q_t . dq_t + beta_t x_t . (w_t - v_t) - k_t . col_t, col the last three terms of dk,
-//   and <dS1, S1> more in the chunk's last row; dg: sums of dL/dG from a row to the chunk's end.
-//   With c_t = k_t . dS1 u_t e^{G_C - G_t}, the last term of k_t . col_t, that is
-//   <dS1, S1> = e^{G_C} <dS1, S0> + sum of c_t: the sum is made of the c_t that the rows subtract,
-//   so that they go out exactly.  (From the saved S1, whose parts are off by 2^-18 each, dg was off
-//   by up to 1e-4 of its norm where the gates close and what a chunk writes is all of S1.)
-// (k_t . col_t is x_t . u_t, so dL/dG_t = q_t . dq_t - v_t . dv_t; but computed from that, what
-// x_t is off by is not taken out again, and dg is off by 1.5e-5 instead of 6e-6 of its norm.)
+//   dL/dG_t = q_t . dq_t + k_t . row_t - k_t . col_t, row the first two terms of dk, col the
+//   others, and <dS1, S1> more in the chunk's last row; dg: sums of dL/dG from a row to the chunk's end.
+//   Most of it cancels (a pair of rows that are both summed does), so both sides are made of the
+//   same operands: row from E, like col (from x and w, k_t . row_t = beta_t x_t . (w_t - v_t), what the
+//   parts of E are off by stays), and with c_t = k_t . dS1 u_t e^{G_C - G_t}, the last term of
+//   k_t . col_t, <dS1, S1> = e^{G_C} <dS1, S0> + sum of c_t.  (From the saved S1, whose parts are
+//   off by 2^-18 each, dg was off by up to 1e-4 of its norm where the gates close and what a chunk
+//   writes is all of S1.)
 //
 // The products run with d on the TMEM lanes (M = d; 128 rows for dP and E, which
 // are made together as [dO; X] U^T).  The scales of single rows are applied when
@@ -29,7 +29,7 @@
 //   4-19   epilogues: dP and E as operands; <dS1, S0>; dq, dk, q . dq (16 columns a warp: what a
 //          warp does to an item is one long dependent chain, and 8 warps of 32
 //          columns take nearly twice as long, 650 us against 592 us on 80 sequences of 96 chunks)
-//   20-23  w, x -> operands U, X; dv, and the sums of rows for dbeta and dg
+//   20-23  w, x -> operands U, X; dv, and dbeta
 // Waits are bounded as in gdr_walk_sm100.cuh.
 #pragma once
 #include "gdr_walk_sm100.cuh"
@@ -59,8 +59,8 @@ struct Smem {
     unsigned char pe[2][2][kC * 128];        // hi, lo: rows of dP, rows of E
     unsigned char ring[2][D * E * 2];       // one part of a state: [d / 8][e][8]
     float f[2][kFactors][kC];                // factors, by item parity
-    float dbeta[2][kC], xv[2][kC];           // row sums, by item parity
-    float part[2][4][kC];                    // q . dq - k . col of a quadrant's rows of d, by item parity
+    float dbeta[2][kC];                      // row sums, by item parity
+    float part[2][4][kC];                    // q . dq + k . (row - col) of a quadrant's rows of d, by item parity
     float dot[2][kEpiWarps];                 // <dS1, S1> in parts, by item parity
     unsigned long long bar[kBars];
     uint32_t tmem;
@@ -318,9 +318,8 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             if (!(wait(kPart + (y & 1), y >> 1) && wait(kSums + (y & 1), y >> 1))) return false;
             // sums of dL/dG from each row to the chunk's end: two rows per lane
             const float(*part)[kC] = sm.part[y & 1];
-            const float* xv = sm.xv[y & 1];
-            float y0 = part[0][t] + part[1][t] + part[2][t] + part[3][t] + xv[t];
-            float y1 = part[0][t + 1] + part[1][t + 1] + part[2][t + 1] + part[3][t + 1] + xv[t + 1];
+            float y0 = part[0][t] + part[1][t] + part[2][t] + part[3][t];
+            float y1 = part[0][t + 1] + part[1][t + 1] + part[2][t + 1] + part[3][t + 1];
             // (the rows of dO behind the end are whatever lies there)
             if (t0 + t >= x.len) y0 = 0.f;
             if (t0 + t + 1 >= x.len) y1 = 0.f;
@@ -530,7 +529,7 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             };
             add(cC, nk, rest);
             add(cC + 64, nk, rest);
-            float s[4] = {};  // of columns 8 (j / 2) + 2 i + j % 2: this warp's rows of d of q . dq - k . col
+            float s[4] = {};  // of columns 8 (j / 2) + 2 i + j % 2: this warp's rows of d of q . dq + k . (row - col)
             const auto along = [&](const unsigned char (*rows)[kC * 128], const float (&of)[kHalves * 8], float sign) {
 #pragma unroll
                 for (int hb = 0; hb < kHalves; ++hb) {
@@ -555,9 +554,10 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[j] = 0.f;
             add(cPE, nk, nullptr);
-            along(sm.k, nk, -1.f);
+            along(sm.k, nk, -2.f);
             add(cA + 64, nk, neg_beta_eg);
             add(cB + 64, nk, nullptr);
+            along(sm.k, nk, 1.f);  // row + col - 2 col
             add(cA, nq, eg);
             add(cB, nq, nullptr);
             tc_fence_before();
@@ -591,7 +591,6 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
             return meet();
         });
     } else {
-        const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(A.v);
         each([&](const Item& x, int y) {
             // E / 4 lanes hold a row, four columns each: a slot is one row (E = 128) or two (E = 64)
             constexpr int kLanes = E / 4, kPer = 32 / kLanes;
@@ -605,25 +604,22 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                 const int left = x.len - t0 - row0;
                 const size_t io = row_at(A, x.b, x.h, A.H, t0 + row0, E) + col;
                 float4 w[4], xx[4];
-                uint2 vv[4];
                 float bt[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     w[r] = xx[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    vv[r] = make_uint2(0, 0);
                     bt[r] = 0.f;
                     if (kPer * r < left) {
                         const size_t at = (seq * A.T + t0 + row0 + kPer * r) * E + col;
                         w[r] = *reinterpret_cast<const float4*>(in.W + at);
                         xx[r] = *reinterpret_cast<const float4*>(in.X + at);
-                        vv[r] = *reinterpret_cast<const uint2*>(v + io + kPer * r * step);
                         bt[r] = cw.beta[row0 + kPer * r];
                     }
                 }
                 // the MMAs have read the operands of the item before, warp 3 the row sums of the one before that
                 if (z == 0 && y > 0 && !wait(kXUFree, y - 1)) return false;
                 if (z == 0 && y > 1 && !wait(kSumsFree + (y & 1), (y >> 1) - 1)) return false;
-                float sum[8];  // of each slot: x . w, beta x . (w - v)
+                float sum[4];  // of each slot: x . w
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const uint32_t at = piece<128>(row0 + kPer * r, (col & 63) >> 3) + 2 * (col & 7);
@@ -636,24 +632,22 @@ gdr_grad_tc(Args A, const ChunkWs* ws, Saved in, int chunks, int items, const __
                     split(xx[r].z, xx[r].w, h1, l1);
                     *reinterpret_cast<uint2*>(sm.dx[col >> 6][1] + at) = make_uint2(h0, h1);
                     *reinterpret_cast<uint2*>(sm.dx[col >> 6][2] + at) = make_uint2(l0, l1);
-                    sum[2 * r] = fmaf(xx[r].x, w[r].x, fmaf(xx[r].y, w[r].y, fmaf(xx[r].z, w[r].z, xx[r].w * w[r].w)));
-                    sum[2 * r + 1] = bt[r] * fmaf(xx[r].x, w[r].x - low_of(vv[r].x), fmaf(xx[r].y, w[r].y - high_of(vv[r].x),
-                                                  fmaf(xx[r].z, w[r].z - low_of(vv[r].y), xx[r].w * (w[r].w - high_of(vv[r].y)))));
+                    sum[r] = fmaf(xx[r].x, w[r].x, fmaf(xx[r].y, w[r].y, fmaf(xx[r].z, w[r].z, xx[r].w * w[r].w)));
                 }
-                // 8 sums over the lanes of a row, halving what a lane holds with each exchange
+                // 4 sums over the lanes of a row, halving what a lane holds with each exchange
 #pragma unroll
-                for (int m = kLanes / 2, held = 4; held > 0; m >>= 1, held >>= 1)
+                for (int m = kLanes / 2, held = 2; held > 0; m >>= 1, held >>= 1)
 #pragma unroll
-                    for (int y2 = 0; y2 < 4; ++y2)
+                    for (int y2 = 0; y2 < 2; ++y2)
                         if (y2 < held) {
                             const bool up = lane & m;
                             const float give = up ? sum[y2] : sum[held + y2], keep = up ? sum[held + y2] : sum[y2];
                             sum[y2] = keep + __shfl_xor_sync(0xffffffffu, give, m);
                         }
 #pragma unroll
-                for (int m = kLanes / 16; m; m >>= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], m);
-                const int mine_ = lane % kLanes / (kLanes / 8);  // which sum this lane ended with
-                if (lane % (kLanes / 8) == 0) (mine_ & 1 ? sm.xv : sm.dbeta)[y & 1][row0 + kPer * (mine_ >> 1)] = sum[0];
+                for (int m = kLanes / 8; m; m >>= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], m);
+                const int mine_ = lane % kLanes / (kLanes / 4);  // which sum this lane ended with
+                if (lane % (kLanes / 4) == 0) sm.dbeta[y & 1][row0 + kPer * mine_] = sum[0];
                 if (A.out_bf16) {
                     __nv_bfloat16* p = static_cast<__nv_bfloat16*>(A.dv) + io;
 #pragma unroll
