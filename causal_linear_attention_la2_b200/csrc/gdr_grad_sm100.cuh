@@ -21,14 +21,16 @@
 // the accumulators are read.  Every formed operand is a high and a low bf16 part.
 //
 // One persistent CTA per SM walks over (chunk, key head, value head) items.  Per
-// item it reads 2 x 64 KB of states, 64 KB of w and x and 64 KB of rows and writes
-// 80 KB (d = 128), which is what bounds it; warps:
+// item it reads 2 x 64 KB of states (dS1 and S0 once more, out of L2), 64 KB of w and x
+// and 48 KB of rows and writes 80 KB (d = 128); the conversions of w and x and the ring of
+// the state parts, one after the other, bound it.  80 sequences of 96 chunks, d = e = 128:
+// 533 us; 128 of 32 chunks, d = e = 64: 165 us.  Warps:
 //   0      loads: dO and factors, K and Q, the four state parts through a ring
 //   1      MMAs
 //   2      TMEM allocation;  3  dg, dbeta
 //   4-19   epilogues: dP and E as operands; <dS1, S0>; dq, dk, q . dq (16 columns a warp: what a
 //          warp does to an item is one long dependent chain, and 8 warps of 32
-//          columns take nearly twice as long, 650 us against 592 us on 80 sequences of 96 chunks)
+//          columns took 650 us where these took 592 us, on 80 sequences of 96 chunks)
 //   20-23  w, x -> operands U, X; dv, and dbeta
 // Waits are bounded as in gdr_walk_sm100.cuh.
 #pragma once

@@ -420,8 +420,7 @@ la2_status la2_bwd_norm(const void *q, const void *k, const void *v, const float
  *
  * bf16 with d and e in {64, 128} runs by 64-row chunks on the tensor cores, every
  * operand formed on the way held as two bf16 parts (2^-16 of a value is lost;
- * fp32 results are off by a few 2^-18 of their norm, dg, a difference of larger
- * terms, by up to some 2^-16 in batches of a few rows); everything else token by
+ * fp32 results are off by a few 2^-18 of their norm); everything else token by
  * token in fp32.
  *
  * la2_gdr_bwd gives the gradients of
