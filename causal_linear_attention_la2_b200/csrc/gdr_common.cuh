@@ -45,12 +45,13 @@ __device__ __forceinline__ int length_of(const Args& a, int b) {
 
 // exp(g) underflows fp32 below -104; a gate of -inf (or far below) is brought
 // to where its exponential is 0 all the same, so that differences of
-// cumulative gates stay finite.
+// cumulative gates stay finite.  A comparison, not fmaxf, which would bring a
+// NaN to the bound as well: a NaN gate has to be seen in the results.
 constexpr float kMinGate = -128.f;
 
-__device__ __forceinline__ float gate_at(const Args& a, size_t i) {
-    return a.g ? fmaxf(a.g[i], kMinGate) : 0.f;
-}
+__device__ __forceinline__ float bounded_gate(float g) { return g < kMinGate ? kMinGate : g; }
+
+__device__ __forceinline__ float gate_at(const Args& a, size_t i) { return a.g ? bounded_gate(a.g[i]) : 0.f; }
 
 // 2^x, off by at most 2 units in the last place (results below 2^-126 are zero);
 // without a branch, so that it can be computed where it is not used.

@@ -80,7 +80,7 @@ struct RecRows {
 #pragma unroll
         for (int y = 0; y < 2; ++y) sm.v[(tid + y * kRecThreads) / kRecCols][tid % kRecCols] = to_float(v[y]);
         if (tid < kRecStep) {
-            sm.a[tid] = expf(fmaxf(g, kMinGate));
+            sm.a[tid] = expf(bounded_gate(g));
             sm.b[tid] = b;
         }
     }

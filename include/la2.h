@@ -397,7 +397,9 @@ la2_status la2_bwd_norm(const void *q, const void *k, const void *v, const float
  * NULL: no gate, a_t = 1) and beta: fp32 [B, H, T] (or [B, T, H]).  H is a
  * multiple of Hk; value head h reads key head h / (H / Hk), and dq and dk are
  * sums over the value heads that share a key head, in a fixed order.  A gate of
- * -inf (or any g below -104, where exp(g) is 0 in fp32) forgets everything.
+ * -inf (or any g below -104, where exp(g) is 0 in fp32) forgets everything; a
+ * NaN gate makes every later row of its sequence and head NaN, and the gradients
+ * that depend on it (bf16 by chunks: other rows of its 64-row chunk too).
  *
  * seq_lens: device int32 [B], or NULL (every sequence has T rows): sequence b
  * has seq_lens[b] rows, brought into 0 .. T; rows behind them are not read, and

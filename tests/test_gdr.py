@@ -381,6 +381,58 @@ def test_extreme_gates_and_strengths(gpu, dtype, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["bhtd", "bthd"])
+@pytest.mark.parametrize("dtype,d,e,T,at", [(BF16, 64, 64, 150, 70), (BF16, 128, 128, 150, 70), (BF16, 128, 64, 150, 149),
+                                            (BF16, 64, 128, 150, 0), (BF16, 72, 100, 150, 70), (F32, 64, 64, 150, 70),
+                                            (F32, 128, 20, 40, 39), (BF16, 128, 128, 2200, 1000)])
+def test_a_nan_gate_is_seen(gpu, dtype, d, e, T, at, layout):
+    """One gate that is NaN: every row from it on, the final state and the gradients that depend on it are NaN; what does
+    not depend on it is, bit by bit, what it is without (by chunks of 64 rows, the other rows of its chunk aside)."""
+    x = R.make(3, 1, 2, T, d, e, dtype, 60, init=True, final=True)
+    runs = []
+    for bad in (False, True):
+        z = dict(x)
+        if bad:
+            z["g"] = x["g"].clone()
+            z["g"][1, 0, at] = float("nan")
+        y = _put(z, layout, gpu)
+        a = (y["q"], y["k"], y["v"], y["g"], y["beta"])
+        o, S = L.la2_gdr_fwd(*a, layout=layout, init_state=y["init"], want_final=True)
+        gr = L.la2_gdr_bwd(*a, y["do"], layout=layout, init_state=y["init"], d_final_state=y["dfinal"], want_d_init=True)
+        runs.append([_back(o, layout), S.double().cpu(), *(_back(t, layout) for t in gr[:5]), gr[5].double().cpu()])
+    first = at // 64 * 64  # first row of the chunk
+    for name, c, n in zip(("o", "S", "dq", "dk", "dv", "dg", "dbeta", "dinit"), *runs):
+        assert torch.isfinite(c).all(), name
+        others = [0, 2]
+        assert torch.equal(n[others], c[others]), name
+        if name in ("dq", "dk"):  # sums over the two value heads
+            continue
+        assert torch.equal(n[1, 1], c[1, 1]), name
+    o, S, dq, dk, dv, dg, db, dinit = runs[1]
+    assert torch.isnan(o[1, 0, at:]).all() and torch.equal(o[1, 0, :first], runs[0][0][1, 0, :first])
+    assert torch.isnan(S[1, 0]).all() and torch.isnan(dinit[1, 0]).all()
+    assert torch.isnan(dq[1, 0, at:]).all()
+    for t in (dk[1, 0], dv[1, 0], db[1, 0], dg[1, 0]):
+        assert torch.isnan(t[:at]).all()
+    assert torch.isnan(dg[1, 0, at]) and torch.isnan(db[1, 0, at])
+    assert torch.equal(dv[1, 0, first + 64:], runs[0][4][1, 0, first + 64:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [3, 200])
+def test_a_nan_gate_is_seen_by_a_step(gpu, B):
+    x = R.make(B, 1, 2, 1, 64, 64, F32, 61)
+    one = {n: x[n][:, :, 0].contiguous().to(gpu) for n in ("q", "k", "v", "g", "beta")}
+    one["g"][1, 0] = float("nan")
+    pool = torch.randn(B, 2, 64, 64, device=gpu)
+    o = L.la2_gdr_decode(one["q"], one["k"], one["v"], one["g"], one["beta"], pool)
+    for t in (o, pool):
+        assert torch.isnan(t[1, 0]).all()
+        t[1, 0] = 0.0
+        assert torch.isfinite(t).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype,d,e", [(BF16, 64, 64), (BF16, 128, 64), (BF16, 64, 128), (BF16, 128, 128), (F32, 48, 48)])
 def test_gate_gradient_where_the_gate_closes(gpu, dtype, d, e):
     """One row that forgets the state before it, whose product with the gradient is all that the row wrote: dg is
