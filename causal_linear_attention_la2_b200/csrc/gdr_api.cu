@@ -334,6 +334,8 @@ la2_status size_checks(int B, int Hk, int H, int T, int d, int e, la2_dtype dtyp
     if (H > 0 && (Hk == 0 || H % Hk != 0)) return LA2_ERR_INVALID_ARG;
     if (d > la2::gdr::kMaxDim || e > la2::gdr::kMaxDim) return LA2_ERR_UNSUPPORTED;
     if (dtype == LA2_DTYPE_F32 && out_dtype == LA2_DTYPE_BF16) return LA2_ERR_UNSUPPORTED;
+    // the kernels step a chunk past a sequence's last row, in 32 bits
+    if (T > INT_MAX - (la2::gdr::kC - 1)) return LA2_ERR_UNSUPPORTED;
     // one CTA per (sequence, chunk), or four per sequence, at most, in one grid dimension
     if (B > 0 && H > 0 && static_cast<long long>(B) * H > (INT_MAX - 1) / (static_cast<long long>(T) / 32 + 4))
         return LA2_ERR_UNSUPPORTED;

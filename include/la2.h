@@ -412,7 +412,7 @@ la2_status la2_bwd_norm(const void *q, const void *k, const void *v, const float
  * BF16 inputs); dg (may be NULL, and must be without g), dbeta and the states
  * are fp32.  No output may alias an input or another output.
  *
- * 1 <= d, e <= 128 for both dtypes (more: LA2_ERR_UNSUPPORTED).  q, k, v, out,
+ * 1 <= d, e <= 128 for both dtypes, T <= 2^31 - 64 (more: LA2_ERR_UNSUPPORTED).  q, k, v, out,
  * dout, dq, dk, dv 16-byte aligned, the others 4-byte.  workspace: device
  * memory of at least la2_gdr_workspace_bytes() bytes, 256-byte aligned, not
  * used by another call that may run at the same time; it grows with T (the

@@ -138,6 +138,17 @@ def test_more_rows_than_a_grid_holds_are_unsupported(lib):
     assert L.la2_gdr_workspace_bytes(1 << 14, 1, 1 << 13, 1 << 20, 64, 64, 1, 1) == (1 << 64) - 1
 
 
+@pytest.mark.parametrize("T", [2 ** 31 - 1, 2 ** 31 - 63])
+@pytest.mark.parametrize("d,dtype", [(1, 1), (1, 0), (64, 1)])
+def test_rows_whose_numbers_pass_32_bits_are_unsupported(lib, T, d, dtype):
+    """The kernels step 16, 32 or 64 rows past a sequence's last one, in 32 bits."""
+    kw = dict(B=1, Hk=1, H=1, T=T, d=d, e=d, dtype=dtype, out_dtype=0)
+    assert _raw_fwd(**kw) == L.LA2_ERR_UNSUPPORTED
+    assert _raw_bwd(**kw) == L.LA2_ERR_UNSUPPORTED
+    assert L.la2_gdr_workspace_bytes(1, 1, 1, T, d, d, dtype, 1) == (1 << 64) - 1
+    assert L.la2_gdr_workspace_bytes(1, 1, 1, 2 ** 31 - 64, d, d, dtype, 1) < 1 << 62
+
+
 @pytest.mark.parametrize("name", ["q", "k", "v", "beta", "out"])
 def test_forward_refuses_null_and_misaligned(lib, name):
     assert _raw_fwd(**{name: 0}) == L.LA2_ERR_INVALID_ARG
