@@ -99,10 +99,16 @@ bool set_bulk_attrs() {
            set(reinterpret_cast<const void*>(gdr_step_bulk<__nv_bfloat16, kTeam>), bulk_smem_bytes<kTeam>());
 }
 
+// The kernels of la2_gdr_selftest_timeout
+bool set_held_attrs() {
+    using namespace la2::gdr;
+    return set(reinterpret_cast<const void*>(gdr_step_bulk<__nv_bfloat16, 512, true>), bulk_smem_bytes<512>());
+}
+
 bool set_smem_attrs() {
     return set_chunk_attrs<64>() && set_chunk_attrs<128>() &&
            set_rec_attrs<64>() && set_rec_attrs<128>() &&
-           set_bulk_attrs<128>() && set_bulk_attrs<256>() && set_bulk_attrs<512>() &&
+           set_held_attrs() && set_bulk_attrs<128>() && set_bulk_attrs<256>() && set_bulk_attrs<512>() &&
            set(reinterpret_cast<const void*>(la2::gdr::pool_copy<float4>), 200 << 10) &&
            set(reinterpret_cast<const void*>(la2::gdr::pool_copy<float>), 200 << 10);
 }
@@ -466,6 +472,35 @@ la2_status la2_gdr_decode(const void* q, const void* k, const void* v, const flo
     };
     if (dtype == LA2_DTYPE_BF16) go(__nv_bfloat16());
     else go(float());
+    return launched();
+}
+
+la2_status la2_gdr_selftest_timeout(la2_gdr_kernel kernel, void* workspace, size_t workspace_bytes, la2_stream_t stream) {
+    if (kernel != LA2_GDR_KERNEL_DECODE) return LA2_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < LA2_GDR_SELFTEST_BYTES) return LA2_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return LA2_ERR_INVALID_ARG;
+    int* status = nullptr;
+    if (!device_setup() || !(status = la2::status_word())) return LA2_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (cudaMemsetAsync(workspace, 0, LA2_GDR_SELFTEST_BYTES, s) != cudaSuccess) return LA2_ERR_CUDA;
+    char* at = static_cast<char*>(workspace);
+    const auto take = [&](size_t bytes) {
+        char* p = at;
+        at += align256(bytes);
+        return p;
+    };
+    using la2::gdr::kMaxDim;
+    constexpr int d = kMaxDim, e = kMaxDim;
+    {  // one CTA, six rows one after the other
+        constexpr int B = 6;
+        const auto *q = reinterpret_cast<__nv_bfloat16*>(take(B * d * 2)), *k = reinterpret_cast<__nv_bfloat16*>(take(B * d * 2));
+        const auto* v = reinterpret_cast<__nv_bfloat16*>(take(B * e * 2));
+        const float* beta = reinterpret_cast<float*>(take(B * sizeof(float)));
+        float *states = reinterpret_cast<float*>(take(B * d * e * sizeof(float)));
+        float* out = reinterpret_cast<float*>(take(B * e * sizeof(float)));
+        la2::gdr::gdr_step_bulk<__nv_bfloat16, 512, true><<<1, la2::gdr::kBulkThreads, la2::gdr::bulk_smem_bytes<512>(), s>>>(
+            q, k, v, nullptr, beta, states, nullptr, B, out, B, 1, 1, d, e, la2::gdr::bulk_stages(d, e), status);
+    }
     return launched();
 }
 

@@ -193,7 +193,10 @@ struct Team {
     }
 };
 
-template <typename Tin, int kTeam>
+// Every wait is bounded; a team that gives up waits for its copies in flight before
+// its shared memory can go to another CTA.  kHold (la2_gdr_selftest_timeout): the
+// third state is announced and not loaded, and the bound is 20 ms.
+template <typename Tin, int kTeam, bool kHold = false>
 __global__ void __launch_bounds__(kBulkThreads, 1)
 gdr_step_bulk(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* __restrict__ v,
               const float* __restrict__ g, const float* __restrict__ beta, float* state,
@@ -210,6 +213,7 @@ gdr_step_bulk(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* _
     const int cu = e / 4, groups = kTeam / cu, rg = tid / cu, ju = tid % cu;
     const bool on = rg < groups;
     const int first = team * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    constexpr uint64_t kLimit = kHold ? 20000000ull : 2000000000ull;  // ns
     const int every = kTeams * static_cast<int>(gridDim.x);
     const int mine = first < total ? (total - 1 - first) / every + 1 : 0;
     const auto index = [&](int y) { return first + y * every; };
@@ -221,6 +225,7 @@ gdr_step_bulk(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* _
         if (slot < 0 || slot >= n_slots) slot = 0;  // read and dropped: a pool without slots is not launched
         const uint32_t bar = full + 8 * (y % stages);
         mbar_arrive_expect_tx(bar, bytes);
+        if (kHold && y == 2) return;
         asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                          smem_u32(stage + static_cast<size_t>(y % stages) * page)),
                      "l"(state + (static_cast<size_t>(slot) * H + index(y) % H) * page), "r"(bytes), "r"(bar)
@@ -272,9 +277,13 @@ gdr_step_bulk(const Tin* __restrict__ q, const Tin* __restrict__ k, const Tin* _
         if (slots)
             for (int x = tid + kTeam; x < b; x += kTeam) twice |= slots[x] == slot;
         const float vv = to_float(now.v);
-        const bool ok = mbar_wait(full + 8 * s, turn);
+        const bool ok = mbar_wait(full + 8 * s, turn, kLimit);
         if (all.any(!ok)) {
-            if (tid == 0) atomicCAS(status, 0, 5 | (230 << 8));
+            if (tid == 0) {
+                atomicCAS(status, 0, 5 | (230 << 8));
+                for (int x = y; x < mine && x < y + stages - 1; ++x)  // loads in flight
+                    mbar_wait(full + 8 * (x % stages), x / stages & 1, kLimit);
+            }
             break;
         }
         float4* S = reinterpret_cast<float4*>(stage + static_cast<size_t>(s) * page);

@@ -32,7 +32,7 @@ EXPORTS = ("la2_workspace_bytes", "la2_fwd", "la2_fwd_state", "la2_fwd_ex", "la2
            "la2_bwd_state", "la2_dlambda", "la2_dlambda_workspace_bytes",
            "la2_norm_workspace_bytes", "la2_fwd_norm", "la2_bwd_norm",
            "la2_gdr_workspace_bytes", "la2_gdr_fwd", "la2_gdr_bwd", "la2_gdr_decode",
-           "la2_state_copy")
+           "la2_gdr_selftest_timeout", "la2_state_copy")
 
 LA2_LAYOUT_BHTD = 0
 LA2_LAYOUT_BTHD = 1
@@ -114,6 +114,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.la2_gdr_bwd.restype = i
     lib.la2_gdr_decode.argtypes = [vp] * 7 + [i, vp] + [i] * 6 + [vp]
     lib.la2_gdr_decode.restype = i
+    lib.la2_gdr_selftest_timeout.argtypes = [i, vp, sz, vp]
+    lib.la2_gdr_selftest_timeout.restype = i
     lib.la2_state_copy.argtypes = [vp, vp, vp, i, i, ctypes.c_longlong, vp]
     lib.la2_state_copy.restype = i
     _lib = lib
@@ -585,6 +587,17 @@ def la2_gdr_decode_raw(q, k, v, g, beta, states, slots, n_slots, out, B, Hk, H, 
     """The C call with integer pointers (0 = NULL); returns the status."""
     return int(load().la2_gdr_decode(q, k, v, g, beta, states, slots, n_slots, out, B, Hk, H, d, e,
                                      dtype, stream))
+
+
+LA2_GDR_SELFTEST_BYTES = 16 << 20
+LA2_GDR_KERNEL_DECODE = 0
+
+
+def la2_gdr_selftest_timeout_raw(kernel, workspace, ws_bytes, stream=0) -> int:
+    """Failure-path self-test: one of the gated delta rule's kernels waits, bounded by 20 ms, for a
+    copy that is never issued and records LA2_ERR_TIMEOUT; returns the launch status (read the
+    recorded code with la2_device_status)."""
+    return int(load().la2_gdr_selftest_timeout(kernel, workspace, ws_bytes, stream))
 
 
 def la2_state_copy_raw(states, src, dst, n, n_slots, slot_elems, stream=0) -> int:

@@ -477,6 +477,24 @@ la2_status la2_gdr_decode(const void *q, const void *k, const void *v, const flo
 la2_status la2_state_copy(float *states, const int *src, const int *dst, int n, int n_slots,
                           long long slot_elems, la2_stream_t stream);
 
+/*
+ * la2_selftest_timeout's counterpart for the kernels above that wait inside a
+ * CTA: one of them on a small problem of zeros, with one copy that it announces
+ * and never issues, and its waits bounded by 20 ms instead of two seconds.  The
+ * wait for that copy runs out, LA2_ERR_TIMEOUT | site << 8 is recorded (sites
+ * 198 .. 230), the copies and products in flight are waited for and the kernel
+ * ends.  `workspace`: LA2_GDR_SELFTEST_BYTES bytes of device memory, 256-byte
+ * aligned, overwritten.  Returns LA2_OK once the launches are queued; read the
+ * recorded code with la2_device_status.  Nothing traps, faults or hangs.
+ */
+#define LA2_GDR_SELFTEST_BYTES (16u << 20)
+typedef enum la2_gdr_kernel {
+    LA2_GDR_KERNEL_DECODE = 0 /* la2_gdr_decode, many states */
+} la2_gdr_kernel;
+
+la2_status la2_gdr_selftest_timeout(la2_gdr_kernel kernel, void *workspace, size_t workspace_bytes,
+                                    la2_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 const char *la2_status_str(la2_status status);
 
