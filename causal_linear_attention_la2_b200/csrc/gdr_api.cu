@@ -102,7 +102,8 @@ bool set_bulk_attrs() {
 // The kernels of la2_gdr_selftest_timeout
 bool set_held_attrs() {
     using namespace la2::gdr;
-    return set(reinterpret_cast<const void*>(gdr_step_bulk<__nv_bfloat16, 512, true>), bulk_smem_bytes<512>());
+    return set(reinterpret_cast<const void*>(grad::gdr_grad_tc<128, 128, true>), sizeof(grad::Smem<128, 128>)) &&
+           set(reinterpret_cast<const void*>(gdr_step_bulk<__nv_bfloat16, 512, true>), bulk_smem_bytes<512>());
 }
 
 bool set_smem_attrs() {
@@ -263,7 +264,7 @@ la2_status walks_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::
     return LA2_OK;
 }
 
-template <int D, int E>
+template <int D, int E, bool kHold = false>
 la2_status grad_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::Saved& sv, int chunks, cudaStream_t stream) {
     using namespace la2::gdr;
     CUtensorMap mk, mq, md;
@@ -273,7 +274,7 @@ la2_status grad_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::S
     int* status = la2::status_word();
     if (!status) return LA2_ERR_CUDA;
     const int units = A.B * A.Hk * chunks;
-    grad::gdr_grad_tc<D, E><<<units < kSMs ? units : kSMs, grad::kThreads, sizeof(grad::Smem<D, E>), stream>>>(
+    grad::gdr_grad_tc<D, E, kHold><<<units < kSMs ? units : kSMs, grad::kThreads, sizeof(grad::Smem<D, E>), stream>>>(
         A, cw, sv, chunks, units * (A.H / A.Hk), mk, mq, md, status);
     return LA2_OK;
 }
@@ -304,7 +305,7 @@ la2_status chunk_forward(const Args& A, char* ws, cudaStream_t stream) {
     return launched();
 }
 
-template <int D>
+template <int D, bool kHoldGrad = false>
 la2_status chunk_backward(const Args& A, char* ws, cudaStream_t stream) {
     using namespace la2::gdr;
     const int chunks = cdiv(A.T, kC);
@@ -321,7 +322,7 @@ la2_status chunk_backward(const Args& A, char* ws, cudaStream_t stream) {
     la2_status st = LA2_OK;
     if (on_tc(A)) {
         st = walks_tc<D>(A, cw, sv, chunks, stream);
-        if (st == LA2_OK) st = grad_tc<D, 128>(A, cw, sv, chunks, stream);
+        if (st == LA2_OK) st = grad_tc<D, 128, kHoldGrad>(A, cw, sv, chunks, stream);
     } else {
         gdr_chains<D><<<2 * A.B * A.H * (A.e / kWalkCols), kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, sv, chunks);
         if (chunks > 0) st = grad_tc<D, 64>(A, cw, sv, chunks, stream);
@@ -476,7 +477,7 @@ la2_status la2_gdr_decode(const void* q, const void* k, const void* v, const flo
 }
 
 la2_status la2_gdr_selftest_timeout(la2_gdr_kernel kernel, void* workspace, size_t workspace_bytes, la2_stream_t stream) {
-    if (kernel != LA2_GDR_KERNEL_DECODE) return LA2_ERR_INVALID_ARG;
+    if (kernel != LA2_GDR_KERNEL_DECODE && kernel != LA2_GDR_KERNEL_GRAD) return LA2_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < LA2_GDR_SELFTEST_BYTES) return LA2_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return LA2_ERR_INVALID_ARG;
     int* status = nullptr;
@@ -491,17 +492,36 @@ la2_status la2_gdr_selftest_timeout(la2_gdr_kernel kernel, void* workspace, size
     };
     using la2::gdr::kMaxDim;
     constexpr int d = kMaxDim, e = kMaxDim;
-    {  // one CTA, six rows one after the other
+    if (kernel == LA2_GDR_KERNEL_DECODE) {  // one CTA, six rows one after the other
         constexpr int B = 6;
-        const auto *q = reinterpret_cast<__nv_bfloat16*>(take(B * d * 2)), *k = reinterpret_cast<__nv_bfloat16*>(take(B * d * 2));
-        const auto* v = reinterpret_cast<__nv_bfloat16*>(take(B * e * 2));
+        const auto *q = reinterpret_cast<__nv_bfloat16*>(take(B * d * 2)), *k = reinterpret_cast<__nv_bfloat16*>(take(B * d * 2)),
+                   *v = reinterpret_cast<__nv_bfloat16*>(take(B * e * 2));
         const float* beta = reinterpret_cast<float*>(take(B * sizeof(float)));
-        float *states = reinterpret_cast<float*>(take(B * d * e * sizeof(float)));
+        float* states = reinterpret_cast<float*>(take(B * d * e * sizeof(float)));
         float* out = reinterpret_cast<float*>(take(B * e * sizeof(float)));
         la2::gdr::gdr_step_bulk<__nv_bfloat16, 512, true><<<1, la2::gdr::kBulkThreads, la2::gdr::bulk_smem_bytes<512>(), s>>>(
             q, k, v, nullptr, beta, states, nullptr, B, out, B, 1, 1, d, e, la2::gdr::bulk_stages(d, e), status);
+        return launched();
     }
-    return launched();
+    // Two sequences of two value heads and up to four chunks; one ends inside its second chunk, whose padding
+    // takes the copies' other way (kRaw).
+    static const int lens[2] = {100, 200};
+    Args A = {};
+    A.B = 2; A.Hk = 1; A.H = 2; A.T = 200; A.d = d; A.e = e;
+    const size_t keys = static_cast<size_t>(A.B) * A.Hk * A.T * d * 2, values = static_cast<size_t>(A.B) * A.H * A.T * e * 2,
+                 gates = static_cast<size_t>(A.B) * A.H * A.T * sizeof(float);
+    A.out_bf16 = 1;
+    A.q = take(keys); A.k = take(keys); A.v = take(values); A.dout = take(values);
+    A.beta = reinterpret_cast<float*>(take(gates));
+    A.o = take(values); A.dq = take(keys); A.dk = take(keys); A.dv = take(values);
+    A.dbeta = reinterpret_cast<float*>(take(gates));
+    int* n = reinterpret_cast<int*>(take(sizeof(lens)));
+    if (cudaMemcpyAsync(n, lens, sizeof(lens), cudaMemcpyHostToDevice, s) != cudaSuccess) return LA2_ERR_CUDA;
+    A.lens = n;
+    const size_t need = chunk_ws(static_cast<long long>(A.B) * A.H, A.T, d, e, true).bytes;
+    char* ws = take(need);
+    if (at > static_cast<char*>(workspace) + LA2_GDR_SELFTEST_BYTES) return LA2_ERR_WORKSPACE;
+    return chunk_backward<d, true>(A, ws, s);
 }
 
 la2_status la2_state_copy(float* states, const int* src, const int* dst, int n, int n_slots,
