@@ -102,7 +102,9 @@ bool set_bulk_attrs() {
 // The kernels of la2_gdr_selftest_timeout
 bool set_held_attrs() {
     using namespace la2::gdr;
-    return set(reinterpret_cast<const void*>(grad::gdr_grad_tc<128, 128, true>), sizeof(grad::Smem<128, 128>)) &&
+    return set(reinterpret_cast<const void*>(walk::gdr_walk<128, walk::kForward, true>), sizeof(walk::Smem<128>)) &&
+           set(reinterpret_cast<const void*>(walk::gdr_walks<128, true>), sizeof(walk::Smem<128>)) &&
+           set(reinterpret_cast<const void*>(grad::gdr_grad_tc<128, 128, true>), sizeof(grad::Smem<128, 128>)) &&
            set(reinterpret_cast<const void*>(gdr_step_bulk<__nv_bfloat16, 512, true>), bulk_smem_bytes<512>());
 }
 
@@ -233,7 +235,7 @@ ChunkLayout chunk_ws(long long BH, int T, int d, int e, bool bwd) {
 }
 
 // One walk along every sequence: e = 128 on tcgen05 (T = 0 has no rows to map).
-template <int D, int kMode>
+template <int D, int kMode, bool kHold = false>
 la2_status walk_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::walk::Segments& sg, int chunks,
                    cudaStream_t stream) {
     using namespace la2::gdr;
@@ -244,13 +246,13 @@ la2_status walk_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::w
     int* status = la2::status_word();
     if (!status) return LA2_ERR_CUDA;
     const int parts = kMode == walk::kTransfer ? 2 * (sg.segs - 1) - 1 : sg.segs;
-    walk::gdr_walk<D, kMode><<<A.B * A.H * parts, walk::kThreads, sizeof(walk::Smem<D>), stream>>>(
+    walk::gdr_walk<D, kMode, kHold><<<A.B * A.H * parts, walk::kThreads, sizeof(walk::Smem<D>), stream>>>(
         A, cw, sg, chunks, mk, mq, mv, status);
     return LA2_OK;
 }
 
 // Both walks of a backward
-template <int D>
+template <int D, bool kHold = false>
 la2_status walks_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::Saved& sv, int chunks, cudaStream_t stream) {
     using namespace la2::gdr;
     CUtensorMap mk, mq, mv, md;
@@ -259,8 +261,8 @@ la2_status walks_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::
         return LA2_ERR_CUDA;
     int* status = la2::status_word();
     if (!status) return LA2_ERR_CUDA;
-    walk::gdr_walks<D><<<2 * A.B * A.H, walk::kThreads, sizeof(walk::Smem<D>), stream>>>(A, cw, sv, chunks, mk, mq, mv, md,
-                                                                                       status);
+    walk::gdr_walks<D, kHold><<<2 * A.B * A.H, walk::kThreads, sizeof(walk::Smem<D>), stream>>>(A, cw, sv, chunks, mk, mq, mv,
+                                                                                              md, status);
     return LA2_OK;
 }
 
@@ -281,7 +283,7 @@ la2_status grad_tc(const Args& A, const la2::gdr::ChunkWs* cw, const la2::gdr::S
 
 bool on_tc(const Args& A) { return A.e == la2::gdr::walk::kE && A.T > 0; }
 
-template <int D>
+template <int D, bool kHold = false>
 la2_status chunk_forward(const Args& A, char* ws, cudaStream_t stream) {
     using namespace la2::gdr;
     const int chunks = cdiv(A.T, kC);
@@ -298,14 +300,14 @@ la2_status chunk_forward(const Args& A, char* ws, cudaStream_t stream) {
             if (st != LA2_OK) return st;
             walk::gdr_join<D><<<dim3(A.B * A.H, walk::kE / 32), walk::kJoinThreads, sizeof(walk::JoinSmem<D>), stream>>>(A, sg);
         }
-        st = walk_tc<D, walk::kForward>(A, cw, sg, chunks, stream);
+        st = walk_tc<D, walk::kForward, kHold>(A, cw, sg, chunks, stream);
         return st == LA2_OK ? launched() : st;
     }
     gdr_chain<D><<<A.B * A.H * (A.e / kWalkCols), kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, chunks);
     return launched();
 }
 
-template <int D, bool kHoldGrad = false>
+template <int D, bool kHoldWalks = false, bool kHoldGrad = false>
 la2_status chunk_backward(const Args& A, char* ws, cudaStream_t stream) {
     using namespace la2::gdr;
     const int chunks = cdiv(A.T, kC);
@@ -321,7 +323,8 @@ la2_status chunk_backward(const Args& A, char* ws, cudaStream_t stream) {
         gdr_prep<D><<<static_cast<unsigned>(A.B) * A.H * chunks, kPrepThreads, sizeof(PrepSmem<D>), stream>>>(A, cw, chunks);
     la2_status st = LA2_OK;
     if (on_tc(A)) {
-        st = walks_tc<D>(A, cw, sv, chunks, stream);
+        st = walks_tc<D, kHoldWalks>(A, cw, sv, chunks, stream);
+        if (kHoldWalks) return st == LA2_OK ? launched() : st;
         if (st == LA2_OK) st = grad_tc<D, 128, kHoldGrad>(A, cw, sv, chunks, stream);
     } else {
         gdr_chains<D><<<2 * A.B * A.H * (A.e / kWalkCols), kWalkThreads, sizeof(WalkSmem<D>), stream>>>(A, cw, sv, chunks);
@@ -477,7 +480,7 @@ la2_status la2_gdr_decode(const void* q, const void* k, const void* v, const flo
 }
 
 la2_status la2_gdr_selftest_timeout(la2_gdr_kernel kernel, void* workspace, size_t workspace_bytes, la2_stream_t stream) {
-    if (kernel != LA2_GDR_KERNEL_DECODE && kernel != LA2_GDR_KERNEL_GRAD) return LA2_ERR_INVALID_ARG;
+    if (kernel < LA2_GDR_KERNEL_DECODE || kernel > LA2_GDR_KERNEL_WALKS) return LA2_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < LA2_GDR_SELFTEST_BYTES) return LA2_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return LA2_ERR_INVALID_ARG;
     int* status = nullptr;
@@ -521,7 +524,8 @@ la2_status la2_gdr_selftest_timeout(la2_gdr_kernel kernel, void* workspace, size
     const size_t need = chunk_ws(static_cast<long long>(A.B) * A.H, A.T, d, e, true).bytes;
     char* ws = take(need);
     if (at > static_cast<char*>(workspace) + LA2_GDR_SELFTEST_BYTES) return LA2_ERR_WORKSPACE;
-    return chunk_backward<d, true>(A, ws, s);
+    if (kernel == LA2_GDR_KERNEL_WALK) return chunk_forward<d, true>(A, ws, s);
+    return kernel == LA2_GDR_KERNEL_WALKS ? chunk_backward<d, true, false>(A, ws, s) : chunk_backward<d, false, true>(A, ws, s);
 }
 
 la2_status la2_state_copy(float* states, const int* src, const int* dst, int n, int n_slots,

@@ -127,7 +127,7 @@ __device__ __noinline__ bool wait_slow(uint32_t b, uint32_t parity, int where, v
     }
 }
 
-template <bool kHold = false>
+template <bool kHold>
 struct Waiter {
     uint32_t bars;
     volatile int* abort;
@@ -161,7 +161,7 @@ __device__ __forceinline__ uint32_t tile_bits(uint32_t tile, int r, int c) {
 __device__ __forceinline__ float tile_at(uint32_t tile, int r, int c) { return __uint_as_float(tile_bits(tile, r, c) << 16); }
 
 // The walk of CTA `block` of seqs x parts
-template <int D, int kMode>
+template <int D, int kMode, bool kHold = false>
 __device__ __forceinline__ void walk_along(const Args& A, const ChunkWs* ws, const Saved& out, const Segments& sg, int chunks,
                                            const CUtensorMap& mk, const CUtensorMap& mq, const CUtensorMap& mv, int* status,
                                            int block) {
@@ -186,7 +186,8 @@ __device__ __forceinline__ void walk_along(const Args& A, const ChunkWs* ws, con
     const ChunkWs* cw = ws + static_cast<size_t>(n) * chunks;
     const uint32_t bars = smem_addr(sm.bar);
     volatile int* abort = &sm.abort;
-    const Waiter<> wait{bars, abort, status};
+    const Waiter<kHold> wait{bars, abort, status};
+    const auto drain = [&](int i, int parity) { mbar_wait(bars + 8 * i, parity & 1, kWaitNs<kHold>); };
     const auto bar = [&](int i) { return bars + 8 * i; };
 
     if (tid == 0) {
@@ -235,7 +236,7 @@ __device__ __forceinline__ void walk_along(const Args& A, const ChunkWs* ws, con
                     tma_load_4d(smem_addr(to), &m, bar(on), 64 * x, A.bthd ? head : t0, A.bthd ? t0 : head, b);
                 };
                 for (int x = 0; x < D / 64; ++x) {
-                    rows(st.kq[x][0], mk, hk, x);
+                    if (!(kHold && it == 1 && x == 0)) rows(st.kq[x][0], mk, hk, x);
                     if (!kNoQ) rows(st.kq[x][1], mq, hk, x);
                 }
                 for (int x = 0; x < kE / 64; ++x) rows(st.v[x], mv, h, x);
@@ -275,9 +276,9 @@ __device__ __forceinline__ void walk_along(const Args& A, const ChunkWs* ws, con
         for (int it = max(0, issued - 2); it < issued; ++it) {
             const int c = kRev ? nc - 1 - it : c0 + it;
             const bool cut = c * kC + kC > len && len < A.T;
-            mbar_wait(cut ? bar(kRaw) : bar(kFull + (it & 1)), cut ? 0 : (it >> 1) & 1);
-            // (a P that was never asked for, after an abort, costs this wait its two seconds)
-            if (kMode == kForward) mbar_wait(bar(kFullP + (it & 1)), (it >> 1) & 1);
+            drain(cut ? kRaw : kFull + (it & 1), cut ? 0 : it >> 1);
+            // (a P that was never asked for, after an abort, costs this wait its whole bound)
+            if (kMode == kForward) drain(kFullP + (it & 1), it >> 1);
         }
     } else if (warp == 1) {
         // ----------------------------------------------------------------- MMAs
@@ -702,7 +703,7 @@ __device__ __forceinline__ void walk_along(const Args& A, const ChunkWs* ws, con
     // MMAs in flight end before TMEM goes: the issuer's last commit is waited for
     if (warp == 1) {
         if (elect()) mma_commit(bar(kEnd));
-        mbar_wait(bar(kEnd), 0);
+        drain(kEnd, 0);
     }
     tc_fence_before();
     __syncthreads();
@@ -710,26 +711,26 @@ __device__ __forceinline__ void walk_along(const Args& A, const ChunkWs* ws, con
     if (warp == 2) tmem_dealloc(tm, 512);
 }
 
-template <int D, int kMode>
+template <int D, int kMode, bool kHold = false>
 __global__ void __launch_bounds__(kThreads, 1)
 gdr_walk(Args A, const ChunkWs* ws, Segments sg, int chunks, const __grid_constant__ CUtensorMap mk,
          const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mv, int* status) {
-    walk_along<D, kMode>(A, ws, Saved{}, sg, chunks, mk, mq, mv, status, blockIdx.x);
+    walk_along<D, kMode, kHold>(A, ws, Saved{}, sg, chunks, mk, mq, mv, status, blockIdx.x);
 }
 
 // Both walks of a backward: the gradient of the state needs nothing of the forward
 // walk, so they run side by side where the SMs suffice, the longer one's CTAs first.
 // 80 sequences of 96 chunks, d = 128: 647 us (12 CTAs find no SM at first), one after
 // the other 319 + 338 us.
-template <int D>
+template <int D, bool kHold = false>
 __global__ void __launch_bounds__(kThreads, 1)
 gdr_walks(Args A, const ChunkWs* ws, Saved out, int chunks, const __grid_constant__ CUtensorMap mk,
           const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mv,
           const __grid_constant__ CUtensorMap md, int* status) {
     const int seqs = gridDim.x / 2, block = blockIdx.x;
     const Segments whole = {1, chunks, nullptr};
-    if (block < seqs) walk_along<D, kBackward>(A, ws, out, whole, chunks, mk, mq, md, status, block);
-    else walk_along<D, kSave>(A, ws, out, whole, chunks, mk, mq, mv, status, block - seqs);
+    if (block < seqs) walk_along<D, kBackward, kHold>(A, ws, out, whole, chunks, mk, mq, md, status, block);
+    else walk_along<D, kSave, kHold>(A, ws, out, whole, chunks, mk, mq, mv, status, block - seqs);
 }
 
 // The states that enter segments 1, 2, ..: S_{s+1} = M_s S_s + B_s in fp32, 32

@@ -592,6 +592,8 @@ def la2_gdr_decode_raw(q, k, v, g, beta, states, slots, n_slots, out, B, Hk, H, 
 LA2_GDR_SELFTEST_BYTES = 16 << 20
 LA2_GDR_KERNEL_DECODE = 0
 LA2_GDR_KERNEL_GRAD = 1
+LA2_GDR_KERNEL_WALK = 2
+LA2_GDR_KERNEL_WALKS = 3
 
 
 def la2_gdr_selftest_timeout_raw(kernel, workspace, ws_bytes, stream=0) -> int:

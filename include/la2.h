@@ -490,7 +490,9 @@ la2_status la2_state_copy(float *states, const int *src, const int *dst, int n, 
 #define LA2_GDR_SELFTEST_BYTES (16u << 20)
 typedef enum la2_gdr_kernel {
     LA2_GDR_KERNEL_DECODE = 0, /* la2_gdr_decode, many states */
-    LA2_GDR_KERNEL_GRAD = 1    /* la2_gdr_bwd, the gradients of the chunks */
+    LA2_GDR_KERNEL_GRAD = 1,   /* la2_gdr_bwd, the gradients of the chunks */
+    LA2_GDR_KERNEL_WALK = 2,   /* la2_gdr_fwd, the walk along a sequence */
+    LA2_GDR_KERNEL_WALKS = 3   /* la2_gdr_bwd, both walks */
 } la2_gdr_kernel;
 
 la2_status la2_gdr_selftest_timeout(la2_gdr_kernel kernel, void *workspace, size_t workspace_bytes,

@@ -10,8 +10,10 @@ import torch
 import gdr_ref as R
 from causal_linear_attention_la2_b200 import la2 as L
 
-KERNELS = {"decode": L.LA2_GDR_KERNEL_DECODE, "gradients": L.LA2_GDR_KERNEL_GRAD}
-SITES = {"decode": {230}, "gradients": set(range(200, 230))}  # 200 + the barrier that the first role gave up on
+KERNELS = {"decode": L.LA2_GDR_KERNEL_DECODE, "gradients": L.LA2_GDR_KERNEL_GRAD, "walk": L.LA2_GDR_KERNEL_WALK,
+           "walks": L.LA2_GDR_KERNEL_WALKS}
+BARRIERS = set(range(200, 230))  # 200 + the barrier that the first role gave up on
+SITES = {"decode": {230}, "gradients": BARRIERS, "walk": BARRIERS, "walks": BARRIERS}
 FAKE = 1 << 20
 
 
