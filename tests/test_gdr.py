@@ -516,6 +516,128 @@ def test_long_sequences_in_segments(gpu, B, Hk, H, T, d, lens):
     _check_fwd(gpu, x)
 
 
+def _segments(B, H, T, d):
+    """Segments of the forward walk, from the states that the workspace holds for them (e = 64 is not cut)."""
+    need = [L.la2_gdr_workspace_bytes(B, 1, H, T, d, e, L.LA2_DTYPE_BF16, 0) for e in (128, 64)]
+    return 1 + (need[0] - need[1]) // (B * H * 3 * d * 128 * 4)
+
+
+def _on(dev, f, x):
+    """A function of gdr_ref in 64 bits on the device."""
+    with torch.device(dev):
+        r = f({n: t if t is None else t.to(dev) for n, t in x.items()})
+    return {n: t.cpu() for n, t in r.items()} if isinstance(r, dict) else [t.cpu() for t in r]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,B,H,T,lens,final", [
+    (64, 1, 1, 2100, None, True), (128, 1, 2, 2112, None, False), (128, 1, 1, 19195, None, True), (64, 1, 1, 9000, None, True),
+    (64, 6, 1, 2100, [2100, 0, 1, 576, 577, 1190], True), (128, 6, 1, 2100, [575, 0, 2100, 1152, 640, 1], True),
+    (128, 2, 2, 2100, [64, 1700], False), (64, 2, 3, 2100, [0, 0], True)])
+def test_segments_of_long_sequences(gpu, d, B, H, T, lens, final):
+    """Batches that the plan does cut: lengths of 0, 1, a segment's border (9 chunks) and beside it, ends inside a segment
+    and segments behind an end, states in and out, both layouts and output types."""
+    assert _segments(B, H, T, d) > 3
+    x = R.make(B, 1, H, T, d, 128, BF16, 24, init=True, lens=lens)
+    x["g"] *= 0.1  # states that last over many chunks
+    ro, rS = _on(gpu, R.forward, x)
+    for layout in ("bhtd", "bthd"):
+        y = _put(x, layout, gpu)
+        for odt in (F32, BF16):
+            o = L.la2_gdr_fwd(y["q"], y["k"], y["v"], y["g"], y["beta"], layout=layout, init_state=y["init"],
+                              seq_lens=y["lens"], want_final=final, out_dtype=odt)
+            if final:
+                o, S = o
+                _close(S.double().cpu(), rS, TOL[BF16], name="state")
+            _close(_back(o, layout), ro, TOL[BF16], name="o" + ("bf16" if odt == BF16 else ""))
+
+
+def _check_all(dev, x, layout):
+    """Forward and backward of many elements against the reference on the device: rms(err) <= 1.1e-5 rms(exact) over the
+    rows that exist.
+
+    An operand of two bf16 parts is off by at most 2^-17 of itself (half a step of the second part) and by 2^-17 / sqrt(3)
+    on average, a product of two of them by 6.2e-6, an element that is three such products deep (a state, the rows w or x,
+    a gradient) by sqrt(3) 6.2e-6 = 1.1e-5 of its size on average.  (The largest error has no such bound: the terms are
+    products of normal numbers, some elements the difference of two large ones.)  One element in 10^6 that is off by 2% of
+    rms would show."""
+    y = _put(x, layout, dev)
+    a = (y["q"], y["k"], y["v"], y["g"], y["beta"])
+    lens = [x["v"].shape[2]] * len(x["v"]) if x["lens"] is None else x["lens"].tolist()
+    live = lambda t: torch.cat([t[b, :, :n].flatten() for b, n in enumerate(lens)])  # noqa: E731
+
+    def near(t, want, name, extra=0.0):
+        err, size = _rms(t - want), _rms(want) + extra
+        assert err <= 1.1e-5 * size, f"{name}: {err:.3e} of {size:.3e}"
+
+    def rows(t, want, name, extra=0.0):
+        t = _back(t, layout)
+        for b, n in enumerate(lens):
+            assert not t[b, :, n:].any(), name
+        near(live(t), live(want), name, extra)
+
+    ro, rS = _on(dev, R.forward, x)
+    o, S = L.la2_gdr_fwd(*a, layout=layout, init_state=y["init"], seq_lens=y["lens"], want_final=True)
+    rows(o, ro, "o")
+    near(S.double().cpu(), rS, "state")
+    r = _on(dev, R.backward, x)
+    got = L.la2_gdr_bwd(*a, y["do"], layout=layout, init_state=y["init"], d_final_state=y["dfinal"], seq_lens=y["lens"],
+                        want_d_init=True)
+    for n, t in zip(("dq", "dk", "dv", "dg", "dbeta"), got):
+        rows(t, r[n], n, 8 * _rms(live(r["mag"])) if n == "dg" else 0.0)
+    near(got[5].double().cpu(), r["dinit"], "dinit")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [None, [600, 0, 65, 130, 599, 320]])
+@pytest.mark.parametrize("H", [4, 12])
+@pytest.mark.parametrize("d,e,layout", [(64, 64, "bhtd"), (128, 64, "bthd"), (64, 128, "bhtd"), (128, 128, "bthd")])
+def test_more_chunks_than_sms(gpu, d, e, layout, H, lens):
+    """240 chunks of key heads, so that CTAs of the gradients take a second one, chunks behind an end passed over."""
+    _check_all(gpu, R.make(6, 4, H, 600, d, e, BF16, 25, init=True, final=True, lens=lens), layout)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,e,layout", [(64, 64, "bthd"), (128, 64, "bhtd"), (64, 128, "bthd"), (128, 128, "bhtd")])
+def test_many_ragged_ends(gpu, d, e, layout):
+    """800 chunks of key heads of short sequences: a CTA of the gradients meets several that end inside a chunk."""
+    lens = torch.randint(0, 101, (50,), generator=torch.Generator().manual_seed(5)).tolist()
+    _check_all(gpu, R.make(50, 8, 8, 100, d, e, BF16, 26, init=True, final=True, lens=lens), layout)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,e,lens", [(128, 128, None), (64, 64, [1400, 1337]), (64, 128, [1281, 1400]), (128, 64, None)])
+def test_sequences_of_many_chunks(gpu, d, e, lens):
+    """22 chunks a sequence, forward and backward; gates near 0, so that states last over many of them."""
+    x = R.make(2, 4, 4, 1400, d, e, BF16, 27, init=True, final=True, lens=lens)
+    x["g"] *= 0.1
+    _check_all(gpu, x, "bhtd")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,e", [(64, 64), (128, 64), (64, 128), (128, 128)])
+def test_gate_gradient_of_a_first_row_without_a_state(gpu, d, e):
+    """The first gate of a sequence that starts from nothing multiplies zeros: dg is 0, the difference of sums over the
+    rows t of q_t . dq_t, k_t . row_t and k_t . col_t (what the row reads and what it writes), in which every pair of rows
+    appears twice.
+
+    The two appearances are made of the same operands, so what differs are the roundings of sums in fp32: an element of a
+    row is a sum over 64 rows, a term one over up to 128 elements, dg one over 64 rows: 256 roundings of at most 2^-24,
+    sqrt(256) 2^-24 = 9.5e-7 of a term, random between the 3 x 64 terms, so 9.5e-7 sqrt(sum of their squares), for which
+    `mag` (the sum of a row's terms) stands.  Keys are all the same, where the pairs' terms are largest: from operands of
+    their own, each of two bf16 parts, the 2016 pairs would be off by 1e-6 sqrt(2016) of one each, 5e-6 of that root."""
+    T = 64
+    x = R.make(4, 1, 32, T, d, e, BF16, 28)
+    x["k"] = x["k"][:, :, :1].expand(4, 1, T, d).contiguous()
+    x["g"] *= 0.1
+    y = _put(x, "bhtd", gpu)
+    dg = L.la2_gdr_bwd(y["q"], y["k"], y["v"], y["g"], y["beta"], y["do"])[3]
+    r = _on(gpu, R.backward, x)
+    assert float(r["dg"][:, :, 0].abs().max()) <= 1e-12
+    terms = float(r["mag"].square().sum(-1).mean().sqrt())
+    assert _rms(dg[:, :, 0].double().cpu()) <= 9.5e-7 * terms
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype,d,e", [(F32, 8, 8), (BF16, 64, 64), (BF16, 128, 128), (BF16, 64, 128)])
 def test_empty_sequences_hand_states_on(gpu, dtype, d, e):
