@@ -54,7 +54,7 @@ struct ChunkWs {
     unsigned char img[4][kC * kC * 2];  // N hi, N lo, P hi, P lo
     float eg[kC], rest[kC], beta[kC];
     float neg_eg[kC], neg_beta[kC], rest_beta[kC], neg_beta_eg[kC];
-    float g[kC], gl[kC], unused[3 * kC];
+    float g[kC], gl[kC];
 };
 constexpr int kCoefs = 7;  // eg .. neg_beta_eg
 static_assert(sizeof(ChunkWs) % 256 == 0, "chunks stay 256-byte aligned");
@@ -197,7 +197,7 @@ struct PrepSmem {  // four CTAs per SM
     struct {
         float eg[kC], rest[kC], beta[kC];
         float neg_eg[kC], neg_beta[kC], rest_beta[kC], neg_beta_eg[kC];
-        float g[kC], gl[kC], unused[3 * kC];
+        float g[kC], gl[kC];
     } out;  // as at the end of ChunkWs
 };
 
