@@ -187,8 +187,8 @@ bool by_chunks(la2_dtype dtype, int d, int e) {
 // `chunks` chunks, by the chunks that the busiest SM walks: a segment's own and,
 // with segments, those of the two walks that make its entering state; a join takes
 // about a chunk's time.  The whole forward, d = e = 128, cut and not: 16 sequences of 1024
-// chunks (T = 65,536) 1289 and 3388 us, of 256 chunks 372 and 859 us; 40 of 128 chunks
-// 382 and 503 us; 60 of 128 and 80 of 96 are not cut (554 and 460 us).
+// chunks (T = 65,536) 1219 and 3057 us, of 256 chunks 349 and 777 us; 40 of 128 chunks
+// 356 and 458 us; 60 of 128 and 80 of 96 are not cut (507 and 421 us).
 struct SegPlan {
     int segs, per;
 };

@@ -18,16 +18,21 @@
 //   dU = P^T dO + e^{G_C - G} K dS1,   X = dU - N^T (beta dU),   dV = beta X,
 //   dS0 = e^{G_C} dS1 + Q^T (e^G dO) - K^T (beta e^G X).
 //
-// gdr_prep makes N and P of all chunks at once; gdr_chain and gdr_chain_rev walk
+// gdr_prep makes N and P of all chunks at once; gdr_chain and gdr_chains walk
 // the chunks of a sequence for e = 64 (gdr_walk_sm100.cuh for e = 128);
 // gdr_grad_tc (gdr_grad_sm100.cuh), again for all chunks at once, makes dq, dk,
 // dv, dg and dbeta.
 //
 // Precision: q, k, v, dO enter the products as they are (bf16, exact); every
 // operand that is formed here (states, N, P, W, X, dP, E) is split into a high
-// and a low bf16 part, 2^-17 of the value being lost, and the product of two
-// low parts is dropped.  Sums, states and exponentials are fp32; cumulative
-// gates are fp64 sums kept as two floats.
+// and a low bf16 part, at most 2^-17 of the value being lost (half a step of the
+// low part, which is at most 2^-8 of the value), and the product of two low parts, at
+// most 2^-16 of a product, is dropped.  That leaves fp32 results 3e-6 to 9e-6 of their
+// norm off (fp32 throughout: 1e-7 to 5e-7), far below the rounding of bf16 outputs
+// (2^-8 of a value); a third part would take the products of each operand from two to
+// three and the states on the chunk borders from 4 to 6 bytes a number.  Sums, the
+// states that are carried and exponentials are fp32; cumulative gates are fp64 sums
+// kept as two floats.
 //
 // The walks run transposed, S^T [e][d] with 16 rows (value columns of the
 // state, which do not interact) per warp: the accumulator fragment of one
@@ -928,7 +933,7 @@ gdr_chain(Args A, const ChunkWs* ws, int chunks) {
 
 // Both walks of a backward: the gradient of the state needs nothing of the forward
 // walk, so they run side by side, the longer one's CTAs first.  128 sequences of
-// 2048 rows, d = e = 64: 152 us, one after the other 89 + 112 us.
+// 2048 rows, d = e = 64: 153 us, one after the other 89 + 112 us.
 template <int D>
 __global__ void __launch_bounds__(kWalkThreads, 2)
 gdr_chains(Args A, const ChunkWs* ws, Saved out, int chunks) {

@@ -12,8 +12,8 @@
 //   Most of it cancels (a pair of rows that are both summed does), so both sides are made of the
 //   same operands: row from E, like col (from x and w, k_t . row_t = beta_t x_t . (w_t - v_t), what the
 //   parts of E are off by stays), and with c_t = k_t . dS1 u_t e^{G_C - G_t}, the last term of
-//   k_t . col_t, <dS1, S1> = e^{G_C} <dS1, S0> + sum of c_t.  (From the saved S1, whose parts are
-//   off by 2^-18 each, dg was off by up to 1e-4 of its norm where the gates close and what a chunk
+//   k_t . col_t, <dS1, S1> = e^{G_C} <dS1, S0> + sum of c_t.  (From the saved S1, whose two parts
+//   are off by up to 2^-17 of a number, dg was off by up to 1e-4 of its norm where the gates close and what a chunk
 //   writes is all of S1.)
 //
 // The products run with d on the TMEM lanes (M = d; 128 rows for dP and E, which
@@ -24,7 +24,10 @@
 // item it reads 2 x 64 KB of states (dS1 and S0 once more, out of L2), 64 KB of w and x
 // and 48 KB of rows and writes 80 KB (d = 128); the conversions of w and x and the ring of
 // the state parts, one after the other, bound it.  80 sequences of 96 chunks, d = e = 128:
-// 533 us; 128 of 32 chunks, d = e = 64: 165 us.  Warps:
+// 535 us; 128 of 32 chunks, d = e = 64: 165 us.  The value heads of a key head follow one
+// another in one CTA, so that dq and dk are summed in their order without atomics; with
+// few chunks and one key head most SMs are idle (256 rows, 16 value heads, d = e = 128,
+// the whole backward: 179 us on one key head, 58 us on 16).  Warps:
 //   0      loads: dO and factors, K and Q, the four state parts through a ring
 //   1      MMAs
 //   2      TMEM allocation;  3  dg, dbeta

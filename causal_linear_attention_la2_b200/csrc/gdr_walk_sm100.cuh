@@ -21,7 +21,7 @@
 // cycles each; 78 under a test of the lane).  Each round from one product's
 // commit to the next one's issue costs some 1800 cycles, of which the MMAs are a
 // fraction: three of them bound the walk, 2.9 us a chunk (80 sequences of 96 chunks
-// of d = 128: 281 us; 28 warps instead of 16 took 338 us).
+// of d = 128: 287 us; 28 warps instead of 16 took 338 us).
 //
 // Warps (16): 0 loads (TMA tiles, bulk copies of what gdr_prep left), 1 issues
 // the MMAs, 2 owns the TMEM allocation; 4-7 and 8-11 are the chain's epilogue,
@@ -720,7 +720,7 @@ gdr_walk(Args A, const ChunkWs* ws, Segments sg, int chunks, const __grid_consta
 
 // Both walks of a backward: the gradient of the state needs nothing of the forward
 // walk, so they run side by side where the SMs suffice, the longer one's CTAs first.
-// 80 sequences of 96 chunks, d = 128: 647 us (12 CTAs find no SM at first), one after
+// 80 sequences of 96 chunks, d = 128: 649 us (12 CTAs find no SM at first), one after
 // the other 319 + 338 us.
 template <int D, bool kHold = false>
 __global__ void __launch_bounds__(kThreads, 1)

@@ -21,8 +21,8 @@ constexpr int kStepRows = 128 / 32;       // rows of the state per thread, at mo
 // The state is read and written once (2 d e words of a few flops each: bound by
 // memory bandwidth), so what counts is how much of it is on its way: a CTA takes
 // eight column units (W = 4 floats, 16-byte loads, where e % 4 == 0; W = 1
-// otherwise) of one (row, head) with four rows per thread at d = 128, and eight
-// CTAs share an SM.  64 x 40 states of 128 x 128: 116 us with whole states of 256
+// otherwise) of one (row, head) with four rows per thread at d = 128, and four
+// CTAs (64 registers a thread) share an SM.  64 x 40 states of 128 x 128: 116 us with whole states of 256
 // threads (154 registers, one CTA per SM), 85 us with 512 threads.
 //
 // slots[b] outside 0 .. n_slots - 1, or listed for an earlier row already:
